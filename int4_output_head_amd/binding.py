@@ -7,8 +7,10 @@ library has not been built the first call raises; there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -87,6 +89,32 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         L.requant_lm_head_int4_pack_timed.restype = i32
         L.requant_lm_head_int4.argtypes = [P, i32, i32, i32, P, i32, i32, P, P, P, P]
         L.requant_lm_head_int4.restype = i32
+        # row operators in front of the products (include/int4vh_norm.h)
+        i64, f32 = ctypes.c_int64, ctypes.c_float
+        L.rms_norm_rows.argtypes = [P, i64, P, i64, i32, P, i32, i32, i32, f32, P, P, i32, P]
+        L.rms_norm_rows.restype = i32
+        L.rms_norm_rows_int8.argtypes = [P, i64, P, i64, i32, P, i32, P, i32, i32, f32, P, P, P, P]
+        L.rms_norm_rows_int8.restype = i32
+        L.quantize_rows_int8.argtypes = [P, i64, i32, P, i32, i32, P, P, P]
+        L.quantize_rows_int8.restype = i32
+        # linear layers on packed int4 weights (include/int4vh_linear.h)
+        L.linear_int4_rows_workspace_bytes.argtypes = [i32, i32, i32]
+        L.linear_int4_rows_workspace_bytes.restype = sz
+        L.linear_int4_rows.argtypes = [P, i64, P, P, P, P, i32, P, i64, i32, i32, i32, P, i64, i32, P, sz, P]
+        L.linear_int4_rows.restype = i32
+        # rules on logits (include/int4vh_logits.h)
+        L.logit_rules_apply.argtypes = [P, i64, i32, P, i32, i32, i32, P, P, i64, P]
+        L.logit_rules_apply.restype = i32
+        L.logit_rules_verify_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        L.logit_rules_verify_workspace_bytes.restype = sz
+        L.logit_rules_verify.argtypes = [P, i64, i32, P, P, P, i32, i32, i32, P, i32, f32, P, P, P, P, P, P, P,
+                                         P, sz, P]
+        L.logit_rules_verify.restype = i32
+        L.verify_lm_head_int4_ruled_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+        L.verify_lm_head_int4_ruled_workspace_bytes.restype = sz
+        L.verify_lm_head_int4_ruled.argtypes = [P, P, P, P, P, P, i32, i32, i32, i32, P, i32, f32, P, P, P, P, P,
+                                                P, P, P, sz, P]
+        L.verify_lm_head_int4_ruled.restype = i32
         _lib = L
         return L
 
@@ -609,4 +637,464 @@ def stream_read(buf, mode: int = 0, *, out=None, events=None):
     st = load_library().int4vh_stream_read(_ptr(buf), nbytes, int(mode), _ptr(out), _stream_ptr(dev), e0, e1)
     if st != OK:
         _raise(st, "int4vh_stream_read")
+    return out
+
+
+# ---------------------------------------------------------------- rows in front of the products
+
+ROWS_F16, ROWS_BF16, ROWS_F32 = 0, 1, 2
+_ROW_DTYPES = {torch.float16: ROWS_F16, torch.bfloat16: ROWS_BF16, torch.float32: ROWS_F32}
+
+
+def _row_code(t, name):
+    code = _ROW_DTYPES.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if code is None or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor of float16, bfloat16 or float32")
+    return code
+
+
+def _raw_stream(dev):
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+_no_guard = contextlib.nullcontext()
+
+
+def _guard(dev):
+    """The tensors' device made current for a call that launches on it."""
+    return _no_guard if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _same_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+
+
+def _rows2d(t, name):
+    """t as rows [M, H] with contiguous channels, and the rows' distance."""
+    if t.dim() != 2:
+        if t.dim() < 1 or not t.is_contiguous():
+            raise ValueError(f"{name} must be [M, H], or contiguous with any leading dims")
+        t = t.reshape(-1, t.shape[-1])
+    M, H = t.shape
+    if M < 1 or H < 1:
+        raise ValueError(f"{name} must not be empty")
+    if H > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous channels")
+    stride = t.stride(0) if M > 1 else H
+    if stride < H:
+        raise ValueError(f"{name} must not have overlapping rows")
+    return t, stride
+
+
+def _norm_args(x, weight, residual):
+    dt = _row_code(x, "x")
+    wdt = _row_code(weight, "weight")
+    x2, xs = _rows2d(x, "x")
+    M, H = x2.shape
+    if weight.dim() != 1 or weight.shape[0] != H or not weight.is_contiguous():
+        raise ValueError("weight must be contiguous [H]")
+    r2, rs, total = None, 0, None
+    if residual is not None:
+        if residual.dtype != x.dtype or residual.shape != x.shape:
+            raise ValueError("residual must have the type and shape of x")
+        r2, rs = _rows2d(residual, "residual")
+        total = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _same_device(x.device, weight=weight, residual=residual)
+    return dt, wdt, x2, xs, r2, rs, total, M, H
+
+
+def rms_norm(x, weight, residual=None, *, eps: float = 1e-6, out_dtype=torch.float16):
+    """Root-mean-square norm of rows x [..., H] (float16, bfloat16 or float32;
+    a 2-D x may have strided rows), after adding the residual if one is given:
+    the hidden states of the verify calls (out_dtype float16).  weight [H].
+    Returns the normed rows, and with a residual also the sum x + residual in
+    x's type: (normed, sum)."""
+    dt, wdt, x2, xs, r2, rs, total, M, H = _norm_args(x, weight, residual)
+    odt = _ROW_DTYPES.get(out_dtype)
+    if odt is None:
+        raise TypeError("out_dtype must be float16, bfloat16 or float32")
+    dev = x.device
+    out = torch.empty(x.shape, dtype=out_dtype, device=dev)
+    with _guard(dev):
+        st = load_library().rms_norm_rows(x2.data_ptr(), xs, None if r2 is None else r2.data_ptr(), rs, dt,
+                                          weight.data_ptr(), wdt, M, H, eps,
+                                          None if total is None else total.data_ptr(), out.data_ptr(), odt,
+                                          _raw_stream(dev))
+    if st != OK:
+        _raise(st, "rms_norm_rows")
+    return out if total is None else (out, total)
+
+
+def rms_norm_int8(x, weight, residual=None, *, channel_scales=None, eps: float = 1e-6):
+    """rms_norm with an output in 8 bits, the activations of linear_int4:
+    channel_scales (float16 [H]), the per-channel scales of the packed int4
+    weights, are folded in.  Returns (codes int8 [..., H], row_scales float32
+    [M]), and with a residual also the sum: (codes, row_scales, sum)."""
+    dt, wdt, x2, xs, r2, rs, total, M, H = _norm_args(x, weight, residual)
+    dev = x.device
+    if channel_scales is not None:
+        _check(channel_scales, "channel_scales", torch.float16, 1)
+        if channel_scales.shape[0] != H:
+            raise ValueError("channel_scales must hold H values")
+        _same_device(dev, channel_scales=channel_scales)
+    codes = torch.empty(x.shape, dtype=torch.int8, device=dev)
+    row_scales = torch.empty(M, dtype=torch.float32, device=dev)
+    with _guard(dev):
+        st = load_library().rms_norm_rows_int8(x2.data_ptr(), xs, None if r2 is None else r2.data_ptr(), rs, dt,
+                                               weight.data_ptr(), wdt,
+                                               None if channel_scales is None else channel_scales.data_ptr(), M, H,
+                                               eps, None if total is None else total.data_ptr(), codes.data_ptr(),
+                                               row_scales.data_ptr(), _raw_stream(dev))
+    if st != OK:
+        _raise(st, "rms_norm_rows_int8")
+    return (codes, row_scales) if total is None else (codes, row_scales, total)
+
+
+def quantize_rows(x, *, channel_scales=None):
+    """Rows x [..., H] in 8 bits with one scale per row, without a norm (the
+    activations of a linear_int4 whose input is no norm).  Returns (codes int8
+    [..., H], row_scales float32 [M])."""
+    dt = _row_code(x, "x")
+    x2, xs = _rows2d(x, "x")
+    M, H = x2.shape
+    dev = x.device
+    if channel_scales is not None:
+        _check(channel_scales, "channel_scales", torch.float16, 1)
+        if channel_scales.shape[0] != H:
+            raise ValueError("channel_scales must hold H values")
+        _same_device(dev, channel_scales=channel_scales)
+    codes = torch.empty(x.shape, dtype=torch.int8, device=dev)
+    row_scales = torch.empty(M, dtype=torch.float32, device=dev)
+    with _guard(dev):
+        st = load_library().quantize_rows_int8(x2.data_ptr(), xs, dt,
+                                               None if channel_scales is None else channel_scales.data_ptr(), M, H,
+                                               codes.data_ptr(), row_scales.data_ptr(), _raw_stream(dev))
+    if st != OK:
+        _raise(st, "quantize_rows_int8")
+    return codes, row_scales
+
+
+# ---------------------------------------------------------------- linear layers on packed int4 weights
+
+_ACTIVATIONS = {None: 0, "relu": 1, "gelu": 2, "silu": 3}
+
+
+def linear_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(load_library().linear_int4_rows_workspace_bytes(M, N, K))
+
+
+def linear_int4(codes, row_scales, packed_w, *, out_scales=None, bias=None, activation=None, residual=None,
+                out_dtype=torch.float16, out=None):
+    """Linear layer of 8-bit rows (codes int8 [M, K], row_scales float32 [M];
+    rms_norm_int8, quantize_rows) on packed int4 weights (uint8 [N, K/2], as
+    requant_pack makes them): activation(codes @ q.T * row_scales * out_scales
+    + bias) + residual.  out_scales: float32 [N]; bias [N] and residual [M, N]
+    of out_dtype; activation: None, "relu", "gelu" or "silu".  out: the [M, N]
+    tensor to write, which may be residual itself.  Returns it."""
+    if not isinstance(codes, torch.Tensor) or not codes.is_cuda or codes.dtype != torch.int8:
+        raise TypeError("codes must be a CUDA (HIP) int8 tensor")
+    c2, cs = _rows2d(codes, "codes")
+    M, K = c2.shape
+    _check(row_scales, "row_scales", torch.float32, 1)
+    _check(packed_w, "packed_w", torch.uint8, 2)
+    N = packed_w.shape[0]
+    if row_scales.shape[0] != M or packed_w.shape[1] * 2 != K:
+        raise ValueError("shape mismatch between codes, row_scales and packed_w")
+    dt = _ROW_DTYPES.get(out_dtype)
+    if dt is None:
+        raise TypeError("out_dtype must be float16, bfloat16 or float32")
+    if activation not in _ACTIVATIONS:
+        raise ValueError("activation must be None, 'relu', 'gelu' or 'silu'")
+    dev = codes.device
+    if out_scales is not None:
+        _check(out_scales, "out_scales", torch.float32, 1)
+        if out_scales.shape[0] != N:
+            raise ValueError("out_scales must hold N values")
+    if bias is not None:
+        _check(bias, "bias", out_dtype, 1)
+        if bias.shape[0] != N:
+            raise ValueError("bias must hold N values")
+    rs, os_ = 0, N
+    shape = codes.shape[:-1] + (N,)
+    if residual is not None:
+        if _row_code(residual, "residual") != dt or residual.shape != shape:
+            raise ValueError("residual must be [M, N] of out_dtype")
+        residual, rs = _rows2d(residual, "residual")
+    if out is None:
+        res = out = torch.empty(shape, dtype=out_dtype, device=dev)
+    else:
+        if _row_code(out, "out") != dt or out.shape != shape:
+            raise ValueError("out must be [M, N] of out_dtype")
+        res = out
+        out, os_ = _rows2d(out, "out")
+    _same_device(dev, row_scales=row_scales, packed_w=packed_w, out_scales=out_scales, bias=bias, residual=residual,
+                 out=out)
+    L = load_library()
+    with _guard(dev):
+        need = L.linear_int4_rows_workspace_bytes(M, N, K)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        st = L.linear_int4_rows(c2.data_ptr(), cs, row_scales.data_ptr(), packed_w.data_ptr(),
+                                None if out_scales is None else out_scales.data_ptr(),
+                                None if bias is None else bias.data_ptr(), _ACTIVATIONS[activation],
+                                None if residual is None else residual.data_ptr(), rs, M, N, K, out.data_ptr(), os_,
+                                dt, None if ws is None else ws.data_ptr(), need, _raw_stream(dev))
+    if st != OK:
+        _raise(st, "linear_int4_rows")
+    return res
+
+
+# ---------------------------------------------------------------- rules on logits
+
+_RULES = struct.Struct("@PqPPPPPPPqPPqqP")     # int4vh_logit_rules
+
+
+class LogitRules:
+    """Penalties for repeated tokens, biases and grammar masks of R requests
+    (int4vh_logits.h), every part optional; device tensors, kept by reference.
+    history int32 [total] (the requests' tokens back to back, prompt first),
+    history_offsets int64 [R+1], n_prompt int32 [R]; repetition, frequency,
+    presence float32 [R]; bias_ids int32 and bias_values float32 [n],
+    bias_offsets int64 [R+1] (the last of entries with one id holds); mask
+    int32 [n, >= ceil(V/32)], bit v % 32 of word v // 32 set where token v is
+    allowed, and mask_index int32 [R*T], each row's mask (negative: the row is
+    free; without it row r has mask r)."""
+
+    __slots__ = ("device", "tensors", "packed", "requests", "mask_rows", "mask_words", "n_index")
+
+    def __init__(self, *, history=None, history_offsets=None, n_prompt=None, repetition=None, frequency=None,
+                 presence=None, bias_ids=None, bias_values=None, bias_offsets=None, mask=None, mask_index=None):
+        self.device = self.requests = None
+        self.tensors = (history, history_offsets, n_prompt, repetition, frequency, presence, bias_ids, bias_values,
+                        bias_offsets, mask, mask_index)
+        for t, name, dt, extra in ((history, "history", torch.int32, None),
+                                   (history_offsets, "history_offsets", torch.int64, 1),
+                                   (n_prompt, "n_prompt", torch.int32, 0),
+                                   (repetition, "repetition", torch.float32, 0),
+                                   (frequency, "frequency", torch.float32, 0),
+                                   (presence, "presence", torch.float32, 0),
+                                   (bias_ids, "bias_ids", torch.int32, None),
+                                   (bias_values, "bias_values", torch.float32, None),
+                                   (bias_offsets, "bias_offsets", torch.int64, 1),
+                                   (mask_index, "mask_index", torch.int32, None)):
+            if t is None:
+                continue
+            _check(t, name, dt, 1)
+            self._place(t, name)
+            if extra is not None:
+                if self.requests is None:
+                    self.requests = t.shape[0] - extra
+                elif self.requests != t.shape[0] - extra:
+                    raise ValueError(f"{name} is for {t.shape[0] - extra} requests, not {self.requests}")
+        if (history is None) != (history_offsets is None):
+            raise ValueError("history and history_offsets go together")
+        if n_prompt is not None and history is None:
+            raise ValueError("n_prompt needs a history")
+        if not ((bias_ids is None) == (bias_values is None) == (bias_offsets is None)):
+            raise ValueError("bias_ids, bias_values and bias_offsets go together")
+        if bias_ids is not None and bias_ids.shape != bias_values.shape:
+            raise ValueError("bias_ids and bias_values must have one length")
+        stride = 0
+        self.mask_rows = self.mask_words = 0
+        self.n_index = None
+        if mask is not None:
+            if not isinstance(mask, torch.Tensor) or not mask.is_cuda or mask.dtype != torch.int32 or mask.dim() != 2:
+                raise TypeError("mask must be a 2-D int32 CUDA (HIP) tensor")
+            self._place(mask, "mask")
+            self.mask_rows, self.mask_words = mask.shape
+            if self.mask_rows < 1 or (self.mask_words > 1 and mask.stride(1) != 1):
+                raise ValueError("mask must hold a row at least, with contiguous words")
+            stride = mask.stride(0) if self.mask_rows > 1 else self.mask_words
+            if stride < self.mask_words:
+                raise ValueError("mask must not have overlapping rows")
+            if mask_index is not None:
+                self.n_index = mask_index.shape[0]
+        elif mask_index is not None:
+            raise ValueError("mask_index needs a mask")
+
+        def at(t):
+            return 0 if t is None else t.data_ptr()
+        self.packed = _RULES.pack(at(history), 0 if history is None else history.shape[0], at(history_offsets),
+                                  at(n_prompt), at(repetition), at(frequency), at(presence), at(bias_ids),
+                                  at(bias_values), 0 if bias_ids is None else bias_ids.shape[0], at(bias_offsets),
+                                  at(mask), self.mask_rows, stride, at(mask_index))
+
+    def _place(self, t, name):
+        if self.device is None:
+            self.device = t.device
+        elif t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, not on {self.device}")
+
+    def check(self, dev, R, T, V):
+        if self.device is not None and self.device != dev:
+            raise ValueError(f"the rules are on {self.device}, not on {dev}")
+        if self.requests is not None and self.requests != R:
+            raise ValueError(f"the rules are for {self.requests} requests, not {R}")
+        if self.mask_rows:
+            if self.mask_words < (V + 31) // 32:
+                raise ValueError("mask must hold a bit per token")
+            if self.n_index is not None and self.n_index != R * T:
+                raise ValueError("mask_index must hold one index per row")
+            if self.n_index is None and self.mask_rows != R * T:
+                raise ValueError("mask must hold one row per row of the logits, or come with mask_index")
+
+
+def _logit_rows(logits, R):
+    """(rows [R*T, V], their distance, type code, R, T, V) of logits [R, T, V],
+    or [R*T, V] with R."""
+    code = _row_code(logits, "logits")
+    if logits.dim() == 3:
+        if R is not None and R != logits.shape[0]:
+            raise ValueError("R does not match the logits")
+        R = logits.shape[0]
+    elif logits.dim() != 2:
+        raise ValueError("logits must be [R, T, V], or [R*T, V] with R")
+    elif R is None:
+        raise ValueError("R is required for 2-D logits")
+    rows, stride = _rows2d(logits, "logits")
+    M, V = rows.shape
+    if R < 1 or M % R:
+        raise ValueError("the logits' rows must be R*T")
+    return rows, stride, code, R, M // R, V
+
+
+def _drafts(dev, R, T, draft_ids, draft_probs=None, uniforms=None):
+    if T == 1:
+        return None, None, None
+    if draft_ids is None:
+        raise ValueError("draft_ids is required when T > 1")
+    if (draft_probs is None) != (uniforms is None):
+        raise ValueError("draft_probs and uniforms go together")
+    for t, n, dt in ((draft_ids, "draft_ids", torch.int32), (draft_probs, "draft_probs", torch.float32),
+                     (uniforms, "uniforms", torch.float32)):
+        if t is not None:
+            _check(t, n, dt)
+            if t.numel() != R * (T - 1):
+                raise ValueError(f"{n} must hold R*(T-1) values")
+            if t.device != dev:
+                raise ValueError(f"{n} is on {t.device}, not on {dev}")
+    return (draft_ids.data_ptr(), None if draft_probs is None else draft_probs.data_ptr(),
+            None if uniforms is None else uniforms.data_ptr())
+
+
+def apply_logit_rules(logits, rules, draft_ids=None, *, R: int | None = None, out=None):
+    """The logits under the rules (LogitRules), written out: logits [R, T, V],
+    or [R*T, V] with R (float32, float16 or bfloat16; 2-D rows may be
+    strided); draft_ids int32 [R, T-1] (None when T == 1): row t counts drafts
+    0 .. t-1 as generated.  out: the tensor to write, of the logits' shape and
+    type, which may be the logits.  Returns it."""
+    rows, stride, code, R, T, V = _logit_rows(logits, R)
+    dev = logits.device
+    if rules is not None:
+        rules.check(dev, R, T, V)
+    dr, _, _ = _drafts(dev, R, T, draft_ids)
+    if out is None:
+        res = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+        ptr, os_ = res.data_ptr(), V
+    else:
+        if not isinstance(out, torch.Tensor) or out.shape != logits.shape or out.dtype != logits.dtype or out.device != dev:
+            raise ValueError("out must have the shape, type and device of the logits")
+        res = out
+        o2, os_ = _rows2d(out, "out")
+        ptr = o2.data_ptr()
+    with _guard(dev):
+        st = load_library().logit_rules_apply(rows.data_ptr(), stride, code, dr, R, T, V,
+                                              None if rules is None else rules.packed, ptr, os_, _raw_stream(dev))
+    if st != OK:
+        _raise(st, "logit_rules_apply")
+    return res
+
+
+def _verify_outputs(dev, M, R, T, k, sampled, want_lse):
+    f, i = torch.float32, torch.int32
+    return (torch.empty(M, dtype=f, device=dev), torch.empty(M, dtype=i, device=dev),
+            torch.empty((M, k), dtype=i, device=dev) if k else None,
+            torch.empty((M, k), dtype=f, device=dev) if k else None,
+            torch.empty((R, T - 1), dtype=f, device=dev) if sampled else None,
+            torch.empty(R, dtype=i, device=dev), torch.empty(M, dtype=f, device=dev) if want_lse else None)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def verify_logits(logits, rules=None, draft_ids=None, draft_probs=None, uniforms=None, *, top_k: int = 0,
+                  temperature: float = 1.0, R: int | None = None, want_lse: bool = False):
+    """Verification of drafted tokens straight from logits [R, T, V] (or [R*T,
+    V] with R) under rules (LogitRules, or None), in one pass over them.
+    With draft_probs and uniforms (float32 [R, T-1]) as verify_sampled: top-k
+    sampling at a temperature, or over the whole vocabulary (top_k == 0);
+    without them the drafts are verified greedily, as verify_batch does.
+    Returns (logits_max [R*T], argmax_ids [R*T], topk_ids [R*T, k], topk_logits
+    [R*T, k], p_draft [R, T-1], n_accepted [R], lse [R*T]); the top-k outputs
+    are None when top_k == 0, p_draft without draft_probs or when T == 1, lse
+    unless want_lse.  A row whose mask leaves nothing has argmax -1."""
+    rows, stride, code, R, T, V = _logit_rows(logits, R)
+    dev = logits.device
+    if rules is not None:
+        rules.check(dev, R, T, V)
+    dr, dp, un = _drafts(dev, R, T, draft_ids, draft_probs, uniforms)
+    M, k = R * T, int(top_k)
+    L = load_library()
+    need = L.logit_rules_verify_workspace_bytes(R, T, V, k)
+    if need == 0:
+        _raise(EINVAL, "logit_rules_verify")
+    out = lmax, amax, tids, tlog, pdr, nacc, lse = _verify_outputs(dev, M, R, T, k, dp is not None, want_lse)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    with _guard(dev):
+        st = L.logit_rules_verify(rows.data_ptr(), stride, code, dr, dp, un, R, T, V,
+                                  None if rules is None else rules.packed, k, temperature, lmax.data_ptr(),
+                                  amax.data_ptr(), _at(tids), _at(tlog), _at(lse), _at(pdr), nacc.data_ptr(),
+                                  ws.data_ptr(), need, _raw_stream(dev))
+    if st != OK:
+        _raise(st, "logit_rules_verify")
+    return out
+
+
+def verify_ruled(hidden, packed_w, scales, rules, draft_ids=None, draft_probs=None, uniforms=None, *,
+                 top_k: int = 0, temperature: float = 1.0, R: int | None = None, want_lse: bool = False,
+                 workspace: Workspace | None = None):
+    """Verification through the head under rules (LogitRules): verify_batch's
+    logits through verify_logits, in one call.  hidden: float16 [R, T, H] (or
+    [R*T, H] with R); the other arguments and the outputs as verify_logits.
+    The workspace also holds the call's logits
+    (verify_lm_head_int4_ruled_workspace_bytes)."""
+    if hidden.dim() == 3:
+        R, T, H = hidden.shape
+        hidden = hidden.reshape(R * T, H)
+    else:
+        if R is None:
+            raise ValueError("R is required for a 2-D hidden tensor")
+        T = hidden.shape[0] // R
+        H = hidden.shape[1]
+    _check(hidden, "hidden", torch.float16, 2)
+    _check(packed_w, "packed_w", torch.uint8, 2)
+    _check(scales, "scales", torch.float16, 1)
+    V = packed_w.shape[0]
+    if packed_w.shape[1] * 2 != H or scales.shape[0] != H or hidden.shape[0] != R * T:
+        raise ValueError("shape mismatch between hidden, packed_w and scales")
+    dev = hidden.device
+    _same_device(dev, packed_w=packed_w, scales=scales)
+    if rules is not None:
+        rules.check(dev, R, T, V)
+    dr, dp, un = _drafts(dev, R, T, draft_ids, draft_probs, uniforms)
+    k = int(top_k)
+    L = load_library()
+    need = L.verify_lm_head_int4_ruled_workspace_bytes(R, T, V, H, k)
+    if need == 0:
+        _raise(EINVAL, "verify_lm_head_int4_ruled")
+    out = lmax, amax, tids, tlog, pdr, nacc, lse = _verify_outputs(dev, R * T, R, T, k, dp is not None, want_lse)
+    with _guard(dev):
+        if workspace is None:
+            # a graph keeps its own: the stream's may be replaced by a larger one
+            capturing = torch.cuda.is_current_stream_capturing()
+            workspace = Workspace(need, dev) if capturing else _default_workspace(dev, need)
+        st = L.verify_lm_head_int4_ruled(hidden.data_ptr(), packed_w.data_ptr(), scales.data_ptr(), dr, dp, un, R, T,
+                                         V, H, None if rules is None else rules.packed, k, temperature,
+                                         lmax.data_ptr(), amax.data_ptr(), _at(tids), _at(tlog), _at(lse), _at(pdr),
+                                         nacc.data_ptr(), workspace.tensor.data_ptr(), workspace.nbytes,
+                                         _raw_stream(dev))
+    if st != OK:
+        _raise(st, "verify_lm_head_int4_ruled")
     return out

@@ -7,7 +7,9 @@ import subprocess
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRCS = [os.path.join(HERE, "csrc", f) for f in ("int4vh.hip", "requant.hip", "context_copy.hip", "stream_probe.hip")]
+SOURCES = ("int4vh.hip", "requant.hip", "context_copy.hip", "stream_probe.hip", "norm.hip", "linear.hip",
+           "logits.hip")
+SRCS = [os.path.join(HERE, "csrc", f) for f in SOURCES]
 OUT = os.path.join(HERE, "libint4vh.so")
 INCLUDE = os.path.join(ROOT, "include")
 

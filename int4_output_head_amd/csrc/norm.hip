@@ -1,0 +1,397 @@
+// norm.hip -- the row operators in front of the int4 products, for MI355X
+// (gfx950): the residual addition with the root-mean-square norm that gives
+// the verify calls their hidden states, and the same rows in 8 bits with one
+// scale per row (formulas and order of rounding in int4vh_norm.h).
+//
+// Bound by HBM for many rows and by latency for few: x and the residual are
+// read once, the sum and the normed row written once, and nothing else moves
+// (weights stay in registers).  A row lives in the registers of one workgroup,
+// 8 consecutive channels per thread and chunk, so one pass suffices: the sum
+// of squares and the largest |t| of the row come out of one reduction, because
+// t = (h * weight) * channel_scale does not depend on rstd -- the factor rstd
+// is common to the row and goes into its scale alone.  Workgroups walk over
+// rows with a stride of the grid and keep their channels' weights.
+//
+// Loads are 16 bytes wide whatever the rows' alignment (the hardware splits
+// unaligned ones); only the thread that holds the last, partial chunk of a row
+// goes element by element.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <stdint.h>
+
+#include "int4vh.h"
+#include "int4vh_internal.h"
+#include "int4vh_norm.h"
+#include "rows_common.h"
+
+#pragma clang fp contract(off)
+
+namespace {
+
+using namespace int4vh_detail;
+
+constexpr int kMaxThreads = 1024;
+constexpr float kTinyPeak = 0x1p-100f;    // rows below it have no finite 127 / peak worth using
+
+struct NormArgs {
+    const void *x;
+    const void *residual;      // or null
+    long long x_stride, residual_stride;
+    const void *weight;        // [H] of weight_dtype, or null (quantize_rows_int8)
+    const uint16_t *channel;   // binary16 [H], or null
+    void *sum_out;             // or null
+    void *out;                 // [M, H] of out_dtype (norm)
+    int8_t *codes;             // [M, H] (8 bits)
+    float *row_scales;         // [M]
+    int M, H;
+    int weight_dtype, out_dtype;
+    float eps;
+};
+
+// Channels c .. c+7 of a row (those below H), as binary32; 0 past H.
+template <int kDtype>
+__device__ __forceinline__ void load8(const void *row, int c, int H, float (&v)[8])
+{
+    if (c + 8 <= H) {
+        if constexpr (kDtype == INT4VH_ROWS_F32) {
+            const Words4 a = *reinterpret_cast<const Words4 *>(static_cast<const float *>(row) + c);
+            const Words4 b = *reinterpret_cast<const Words4 *>(static_cast<const float *>(row) + c + 4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[j] = __uint_as_float(a.w[j]);
+                v[4 + j] = __uint_as_float(b.w[j]);
+            }
+        } else {
+            const Words2 a = *reinterpret_cast<const Words2 *>(static_cast<const uint16_t *>(row) + c);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = from_bits16((a.w[j >> 1] >> (16 * (j & 1))) & 0xFFFFu, kDtype);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[j] = 0.0f;
+            if (c + j < H) {
+                if constexpr (kDtype == INT4VH_ROWS_F32)
+                    v[j] = static_cast<const float *>(row)[c + j];
+                else
+                    v[j] = from_bits16(static_cast<const uint16_t *>(row)[c + j], kDtype);
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void load8_any(const void *row, int dtype, int c, int H, float (&v)[8])
+{
+    if (dtype == INT4VH_ROWS_F16)
+        load8<INT4VH_ROWS_F16>(row, c, H, v);
+    else if (dtype == INT4VH_ROWS_BF16)
+        load8<INT4VH_ROWS_BF16>(row, c, H, v);
+    else
+        load8<INT4VH_ROWS_F32>(row, c, H, v);
+}
+
+// The one rounding of each value to the output's type.
+__device__ __forceinline__ void store8(void *row, int dtype, int c, int H, const float (&v)[8])
+{
+    if (dtype == INT4VH_ROWS_F32) {
+        float *p = static_cast<float *>(row) + c;
+        if (c + 8 <= H) {
+            Words4 a, b;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                a.w[j] = __float_as_uint(v[j]);
+                b.w[j] = __float_as_uint(v[4 + j]);
+            }
+            *reinterpret_cast<Words4 *>(p) = a;
+            *reinterpret_cast<Words4 *>(p + 4) = b;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c + j < H)
+                    p[j] = v[j];
+        }
+        return;
+    }
+    uint16_t *p = static_cast<uint16_t *>(row) + c;
+    uint32_t u[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        u[j] = to_bits16(v[j], dtype);
+    if (c + 8 <= H) {
+        Words2 a;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            a.w[j] = u[2 * j] | (u[2 * j + 1] << 16);
+        *reinterpret_cast<Words2 *>(p) = a;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (c + j < H)
+                p[j] = (uint16_t)u[j];
+    }
+}
+
+__device__ __forceinline__ void store_codes8(int8_t *p, int c, int H, const int (&q)[8])
+{
+    if (c + 8 <= H) {
+        Pair1 a;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            a.w[j] = (q[4 * j] & 0xFF) | ((q[4 * j + 1] & 0xFF) << 8) | ((q[4 * j + 2] & 0xFF) << 16) |
+                     ((uint32_t)q[4 * j + 3] << 24);
+        *reinterpret_cast<Pair1 *>(p + c) = a;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (c + j < H)
+                p[c + j] = (int8_t)q[j];
+    }
+}
+
+// Grid: workgroups over rows.  kChunks: chunks of 8 channels per thread (chunk
+// k of a thread starts at channel 8 * (tid + k * blockDim.x)).  kInt8: the
+// 8-bit output; kNorm: divide by the root mean square.
+template <int kDtype, int kChunks, bool kInt8, bool kNorm>
+__global__ void __launch_bounds__(kMaxThreads) norm_rows_kernel(NormArgs a)
+{
+    __shared__ float s_sum[2][kMaxThreads / 64];
+    __shared__ uint32_t s_peak[2][kMaxThreads / 64];
+    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 63, wave = tid >> 6, n_waves = nt >> 6;
+    const int H = a.H;
+    constexpr size_t kSize = kDtype == INT4VH_ROWS_F32 ? 4 : 2;
+    const size_t out_size = a.out_dtype == INT4VH_ROWS_F32 ? 4 : 2;
+
+    float w[kChunks][8], cs[kChunks][8];
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) {
+        const int c = 8 * (tid + k * nt);
+        if (kNorm)
+            load8_any(a.weight, a.weight_dtype, c, H, w[k]);
+        if (kInt8) {
+            if (a.channel) {
+                load8<INT4VH_ROWS_F16>(a.channel, c, H, cs[k]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    cs[k][j] = 1.0f;
+            }
+        }
+    }
+
+    int buf = 0;
+    for (int m = blockIdx.x; m < a.M; m += gridDim.x, buf ^= 1) {
+        const char *xr = static_cast<const char *>(a.x) + (size_t)m * a.x_stride * kSize;
+        float h[kChunks][8];
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k)
+            load8<kDtype>(xr, 8 * (tid + k * nt), H, h[k]);
+        if (a.residual) {
+            const char *rr = static_cast<const char *>(a.residual) + (size_t)m * a.residual_stride * kSize;
+            float r[kChunks][8];
+#pragma unroll
+            for (int k = 0; k < kChunks; ++k)
+                load8<kDtype>(rr, 8 * (tid + k * nt), H, r[k]);
+#pragma unroll
+            for (int k = 0; k < kChunks; ++k)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    h[k][j] += r[k][j];
+            if (a.sum_out) {
+                char *sr = static_cast<char *>(a.sum_out) + (size_t)m * H * kSize;
+#pragma unroll
+                for (int k = 0; k < kChunks; ++k)
+                    store8(sr, kDtype, 8 * (tid + k * nt), H, h[k]);
+            }
+        }
+
+        // one reduction: the sum of squares, and the largest |t| as an
+        // unsigned word (a NaN is above infinity, which is above every number)
+        float ss = 0.0f;
+        uint32_t peak = 0u;
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (kNorm)
+                    ss = __builtin_fmaf(h[k][j], h[k][j], ss);
+                if (kInt8) {
+                    float t = h[k][j];
+                    if (kNorm)
+                        t *= w[k][j];
+                    t *= cs[k][j];
+                    const uint32_t u = __float_as_uint(t) & 0x7FFFFFFFu;
+                    peak = u > peak ? u : peak;
+                }
+            }
+#pragma unroll
+        for (int off = 32; off >= 1; off >>= 1) {
+            if (kNorm)
+                ss += __shfl_xor(ss, off);
+            if (kInt8) {
+                const uint32_t o = __shfl_xor(peak, off);
+                peak = o > peak ? o : peak;
+            }
+        }
+        if (n_waves > 1) {
+            if (lane == 0) {
+                s_sum[buf][wave] = ss;
+                s_peak[buf][wave] = peak;
+            }
+            // the other half of the arrays is the next row's, so one barrier a row
+            __syncthreads();
+            ss = s_sum[buf][0];
+            peak = s_peak[buf][0];
+            for (int i = 1; i < n_waves; ++i) {
+                ss += s_sum[buf][i];
+                const uint32_t o = s_peak[buf][i];
+                peak = o > peak ? o : peak;
+            }
+        }
+        const float rstd = kNorm ? 1.0f / sqrtf(ss / (float)H + a.eps) : 1.0f;
+
+        if (kInt8) {
+            const float pk = __uint_as_float(peak);
+            const bool tiny = pk < kTinyPeak;
+            const bool live = !tiny && peak < 0x7F800000u;
+            const float inv = 127.0f / pk;
+            int8_t *cr = a.codes + (size_t)m * H;
+#pragma unroll
+            for (int k = 0; k < kChunks; ++k) {
+                int q[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float t = h[k][j];
+                    if (kNorm)
+                        t *= w[k][j];
+                    t *= cs[k][j];
+                    // |t * inv| <= 127 (1 + 2^-23): rint never leaves [-127, 127]
+                    q[j] = live ? (int)rintf(t * inv) : 0;
+                }
+                store_codes8(cr, 8 * (tid + k * nt), H, q);
+            }
+            if (tid == 0)
+                a.row_scales[m] = tiny ? 0.0f : (pk * rstd) / 127.0f;
+        } else {
+            char *orow = static_cast<char *>(a.out) + (size_t)m * H * out_size;
+#pragma unroll
+            for (int k = 0; k < kChunks; ++k) {
+                float y[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    y[j] = h[k][j] * rstd * w[k][j];
+                store8(orow, a.out_dtype, 8 * (tid + k * nt), H, y);
+            }
+        }
+    }
+}
+
+template <int kDtype, bool kInt8, bool kNorm>
+int launch_chunks(const NormArgs &a, hipStream_t s)
+{
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess)
+        return hip_fail(e, "hipGetDevice");
+    const int chunks = (a.H + 7) / 8;
+    // Few rows: one chunk per thread, so that a row is one round of loads.
+    // Many: two, which halves the waves that take part in each reduction.
+    const int per = a.M <= 4 * cu_count(dev) ? 1 : 2;
+    const int nt = ((chunks + per - 1) / per + 63) / 64 * 64;
+    const int resident = cu_count(dev) * (2048 / nt);
+    const int grid = a.M < resident ? a.M : resident;
+    if (nt > kMaxThreads)
+        return INT4VH_EUNSUPPORTED;
+    if (per == 1)
+        hipLaunchKernelGGL((norm_rows_kernel<kDtype, 1, kInt8, kNorm>), dim3(grid), dim3(nt), 0, s, a);
+    else
+        hipLaunchKernelGGL((norm_rows_kernel<kDtype, 2, kInt8, kNorm>), dim3(grid), dim3(nt), 0, s, a);
+    e = hipGetLastError();
+    return e == hipSuccess ? INT4VH_OK : hip_fail(e, "norm kernel launch");
+}
+
+template <bool kInt8, bool kNorm>
+int launch(const NormArgs &a, int dtype, hipStream_t s)
+{
+    if (dtype == INT4VH_ROWS_F16)
+        return launch_chunks<INT4VH_ROWS_F16, kInt8, kNorm>(a, s);
+    if (dtype == INT4VH_ROWS_BF16)
+        return launch_chunks<INT4VH_ROWS_BF16, kInt8, kNorm>(a, s);
+    return launch_chunks<INT4VH_ROWS_F32, kInt8, kNorm>(a, s);
+}
+
+// What every entry point checks of its rows.
+int check_rows(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride, int dtype, int M, int H,
+               const void *sum_out)
+{
+    if (M < 1 || H < 1 || !rows_known(dtype) || !x || (sum_out && !residual))
+        return INT4VH_EINVAL;
+    if (M > 1 && (x_stride < H || (residual && residual_stride < H)))
+        return INT4VH_EINVAL;
+    if (!rows_aligned(x, rows_size(dtype)) || !rows_aligned(residual, rows_size(dtype)) || !rows_aligned(sum_out, rows_size(dtype)))
+        return INT4VH_EALIGN;
+    return H > INT4VH_MAX_H ? INT4VH_EUNSUPPORTED : INT4VH_OK;
+}
+
+} // namespace
+
+extern "C" {
+
+int rms_norm_rows(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride, int dtype,
+                  const void *weight, int weight_dtype, int M, int H, float eps, void *sum_out, void *out,
+                  int out_dtype, void *stream)
+{
+    if (!rows_known(weight_dtype) || !rows_known(out_dtype) || !weight || !out || !(eps >= 0.0f) || !std::isfinite(eps))
+        return INT4VH_EINVAL;
+    const int st = check_rows(x, x_stride, residual, residual_stride, dtype, M, H, sum_out);
+    if (st == INT4VH_EINVAL)
+        return st;
+    if (!rows_aligned(weight, rows_size(weight_dtype)) || !rows_aligned(out, rows_size(out_dtype)))
+        return INT4VH_EALIGN;
+    if (st != INT4VH_OK)
+        return st;
+    const NormArgs a = {x,       residual, x_stride, residual_stride, weight, nullptr,      sum_out,
+                        out,     nullptr,  nullptr,  M,               H,      weight_dtype, out_dtype,
+                        eps};
+    return launch<false, true>(a, dtype, static_cast<hipStream_t>(stream));
+}
+
+int rms_norm_rows_int8(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride, int dtype,
+                       const void *weight, int weight_dtype, const void *channel_scales, int M, int H, float eps,
+                       void *sum_out, int8_t *codes, float *row_scales, void *stream)
+{
+    if (!rows_known(weight_dtype) || !weight || !codes || !row_scales || !(eps >= 0.0f) || !std::isfinite(eps))
+        return INT4VH_EINVAL;
+    const int st = check_rows(x, x_stride, residual, residual_stride, dtype, M, H, sum_out);
+    if (st == INT4VH_EINVAL)
+        return st;
+    if (!rows_aligned(weight, rows_size(weight_dtype)) || !rows_aligned(channel_scales, 2) || !rows_aligned(row_scales, 4))
+        return INT4VH_EALIGN;
+    if (st != INT4VH_OK)
+        return st;
+    const NormArgs a = {x,       residual, x_stride,   residual_stride, weight, static_cast<const uint16_t *>(channel_scales),
+                        sum_out, nullptr,  codes,      row_scales,      M,      H,
+                        weight_dtype, INT4VH_ROWS_F16, eps};
+    return launch<true, true>(a, dtype, static_cast<hipStream_t>(stream));
+}
+
+int quantize_rows_int8(const void *x, int64_t x_stride, int dtype, const void *channel_scales, int M, int H,
+                       int8_t *codes, float *row_scales, void *stream)
+{
+    if (!codes || !row_scales)
+        return INT4VH_EINVAL;
+    const int st = check_rows(x, x_stride, nullptr, 0, dtype, M, H, nullptr);
+    if (st == INT4VH_EINVAL)
+        return st;
+    if (!rows_aligned(channel_scales, 2) || !rows_aligned(row_scales, 4))
+        return INT4VH_EALIGN;
+    if (st != INT4VH_OK)
+        return st;
+    const NormArgs a = {x,       nullptr, x_stride, 0, nullptr, static_cast<const uint16_t *>(channel_scales),
+                        nullptr, nullptr, codes,    row_scales, M, H,
+                        INT4VH_ROWS_F16, INT4VH_ROWS_F16, 0.0f};
+    return launch<true, false>(a, dtype, static_cast<hipStream_t>(stream));
+}
+
+} // extern "C"
