@@ -42,8 +42,8 @@
  * that is NULL, a stride below the row's length (M > 1);
  * INT4VH_EALIGN for a misaligned pointer or a codes_stride that is no multiple
  * of 16 (M > 1); INT4VH_EWORKSPACE for a workspace that is too small;
- * INT4VH_EUNSUPPORTED for K > 65536, N > 2^24, M > 2^20 or
- * M * N >= 2^40; INT4VH_EHIP for a launch failure.
+ * INT4VH_EUNSUPPORTED for K > 65536, N > 2^24, M > 2^20, M * N >= 2^40 or a
+ * codes_stride of 2^24 or more (M > 1); INT4VH_EHIP for a launch failure.
  */
 #ifndef INT4VH_LINEAR_H
 #define INT4VH_LINEAR_H

@@ -10,15 +10,15 @@
 // ones, within every 8).  All sums are exact in int32: |16 * acc| <=
 // 128 * 128 * K <= 2^30 for K <= 65536.
 //
-// Two kernels.  Up to 32 rows the call is the weights' stream (N * K / 2
+// Two kernels.  Up to 16 rows the call is the weights' stream (N * K / 2
 // bytes): linear_stream_kernel gives each wave a slice of K whose activations
-// stay in its registers, loads a tile of 16 weight rows per workgroup
-// straight into registers with every load in flight, and adds the waves'
-// exact sums through LDS.  Beyond, linear_tile_kernel is a tiled product,
-// bound by the int8 matrix cores: weights stay packed until the wave that
-// multiplies them has them in registers, so LDS moves half the bytes of an
-// int8 tile.  Where a product has too few tiles to fill the card, its sum over
-// K is split and the int32 parts are added by linear_join_kernel.
+// stay in its registers, loads a tile of 16 weight rows per workgroup straight
+// into registers with every load in flight, and adds the waves' exact sums
+// through LDS.  Beyond, linear_tile_kernel is a tiled product, bound by the
+// int8 matrix cores: weights stay packed until the wave that multiplies them
+// has them in registers, so LDS moves half the bytes of an int8 tile.  Where a
+// product has too few tiles to fill the card, its sum over K is split and the
+// int32 parts are added by linear_join_kernel.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -67,15 +67,21 @@ __device__ __forceinline__ void barrier_no_fence()
     asm volatile("" ::: "memory");
 }
 
-// 32 consecutive activation bytes -> the two operands (channels 0-15 and
-// 16-31), even channels before odd ones within every 8
-__device__ __forceinline__ void order_codes(const u32x4 &lo, const u32x4 &hi, i32x4 &a0, i32x4 &a1)
+// LDS written and read by one wave alone: its accesses execute in order, so
+// only the compiler has to be held back.
+__device__ __forceinline__ void wave_fence()
+{
+    __builtin_amdgcn_wave_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// 16 consecutive activation bytes as an operand: even channels before odd ones
+// within every 8
+__device__ __forceinline__ i32x4 order_codes(const u32x4 &c)
 {
     const uint32_t ev = 0x06040200u, od = 0x07050301u;
-    a0 = i32x4{(int32_t)__builtin_amdgcn_perm(lo[1], lo[0], ev), (int32_t)__builtin_amdgcn_perm(lo[1], lo[0], od),
-               (int32_t)__builtin_amdgcn_perm(lo[3], lo[2], ev), (int32_t)__builtin_amdgcn_perm(lo[3], lo[2], od)};
-    a1 = i32x4{(int32_t)__builtin_amdgcn_perm(hi[1], hi[0], ev), (int32_t)__builtin_amdgcn_perm(hi[1], hi[0], od),
-               (int32_t)__builtin_amdgcn_perm(hi[3], hi[2], ev), (int32_t)__builtin_amdgcn_perm(hi[3], hi[2], od)};
+    return i32x4{(int32_t)__builtin_amdgcn_perm(c[1], c[0], ev), (int32_t)__builtin_amdgcn_perm(c[1], c[0], od),
+                 (int32_t)__builtin_amdgcn_perm(c[3], c[2], ev), (int32_t)__builtin_amdgcn_perm(c[3], c[2], od)};
 }
 
 // half h (16 of 32 channels) of a packed 16-byte chunk as an operand
@@ -91,78 +97,76 @@ __device__ __forceinline__ float load_one(const void *p, size_t i, int dtype)
                                     : from_bits16(static_cast<const uint16_t *>(p)[i], dtype);
 }
 
-__device__ __forceinline__ float activate(float y, int activation)
+// One uniform branch for kN values.
+template <int kN>
+__device__ __forceinline__ void activate(float (&y)[kN], int activation)
 {
-    if (activation == INT4VH_ACT_RELU)
-        return y < 0.0f ? 0.0f : y;      // a NaN stays one
-    if (activation == INT4VH_ACT_GELU)
-        return (0.5f * y) * (1.0f + erff(y * 0.70710678118654752f));
-    if (activation == INT4VH_ACT_SILU)
-        return y / (1.0f + expf(-y));
-    return y;
+    if (activation == INT4VH_ACT_RELU) {
+#pragma unroll
+        for (int r = 0; r < kN; ++r)
+            y[r] = y[r] < 0.0f ? 0.0f : y[r];      // a NaN stays one
+    } else if (activation == INT4VH_ACT_GELU) {
+#pragma unroll
+        for (int r = 0; r < kN; ++r)
+            y[r] = (0.5f * y[r]) * (1.0f + erff(y[r] * 0.70710678118654752f));
+    } else if (activation == INT4VH_ACT_SILU) {
+#pragma unroll
+        for (int r = 0; r < kN; ++r)
+            y[r] = y[r] / (1.0f + expf(-y[r]));
+    }
 }
 
 // acc holds 16 times the exact sum; row_scale / 16 is exact, and so is the
 // conversion for |acc| < 2^28 (its low four bits are zero).  Without fused
-// multiply-adds, in the order of int4vh_linear.h.
-__device__ __forceinline__ float scale_bias(int32_t acc, float row_scale, float out_scale, float bias, bool scaled,
-                                            bool biased)
+// multiply-adds, in the order of int4vh_linear.h; an absent out_scale is 1 and
+// an absent bias 0, which change no value.
+__device__ __forceinline__ float scale_bias(int32_t acc, float row_scale, float out_scale, float bias)
 {
-    float y = ((float)acc * 0.0625f) * row_scale;
-    if (scaled)
-        y = y * out_scale;
-    if (biased)
-        y = y + bias;
-    return y;
+    return ((float)acc * 0.0625f) * row_scale * out_scale + bias;
+}
+
+__device__ __forceinline__ float column_scale(const LinArgs &a, int n)
+{
+    return a.out_scales ? a.out_scales[n] : 1.0f;
+}
+__device__ __forceinline__ float column_bias(const LinArgs &a, int n)
+{
+    return a.bias ? load_one(a.bias, n, a.dtype) : 0.0f;
 }
 
 // One output element.
 __device__ __forceinline__ void finish_one(const LinArgs &a, int m, int n, int32_t acc, float row_scale,
                                            float out_scale, float bias)
 {
-    float y = activate(scale_bias(acc, row_scale, out_scale, bias, a.out_scales != nullptr, a.bias != nullptr),
-                       a.activation);
+    float y[1] = {scale_bias(acc, row_scale, out_scale, bias)};
+    activate(y, a.activation);
     if (a.residual)
-        y = y + load_one(a.residual, (size_t)m * a.residual_stride + n, a.dtype);
+        y[0] += load_one(a.residual, (size_t)m * a.residual_stride + n, a.dtype);
     const size_t o = (size_t)m * a.out_stride + n;
     if (a.dtype == INT4VH_ROWS_F32)
-        static_cast<float *>(a.out)[o] = y;
+        static_cast<float *>(a.out)[o] = y[0];
     else
-        static_cast<uint16_t *>(a.out)[o] = (uint16_t)to_bits16(y, a.dtype);
+        static_cast<uint16_t *>(a.out)[o] = (uint16_t)to_bits16(y[0], a.dtype);
 }
 
-// Four consecutive output elements n .. n+3 of row m (n % 4 == 0).
+// Four consecutive output elements n .. n+3 <= N-1 of row m; res: the
+// residual's 16-bit words where `with` is set.
 __device__ __forceinline__ void finish_four(const LinArgs &a, int m, int n, const i32x4 &acc, float row_scale,
-                                            const float (&out_scale)[4], const float (&bias)[4])
+                                            const float (&out_scale)[4], const float (&bias)[4], bool with,
+                                            uint2 res)
 {
-    if (n + 4 > a.N) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            if (n + r < a.N)
-                finish_one(a, m, n + r, acc[r], row_scale, out_scale[r], bias[r]);
-        return;
-    }
     float y[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-        y[r] = activate(
-            scale_bias(acc[r], row_scale, out_scale[r], bias[r], a.out_scales != nullptr, a.bias != nullptr),
-            a.activation);
-    const size_t o = (size_t)m * a.out_stride + n;
-    if (a.residual) {
-        const size_t i = (size_t)m * a.residual_stride + n;
-        if (a.dtype == INT4VH_ROWS_F32) {
-            const Words4 v = *reinterpret_cast<const Words4 *>(static_cast<const float *>(a.residual) + i);
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                y[r] += __uint_as_float(v.w[r]);
-        } else {
-            const Pair2 v = *reinterpret_cast<const Pair2 *>(static_cast<const uint16_t *>(a.residual) + i);
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                y[r] += from_bits16((v.w[r >> 1] >> (16 * (r & 1))) & 0xFFFFu, a.dtype);
-        }
+        y[r] = scale_bias(acc[r], row_scale, out_scale[r], bias[r]);
+    activate(y, a.activation);
+    if (with) {
+        y[0] += from_bits16(res.x & 0xFFFFu, a.dtype);
+        y[1] += from_bits16(res.x >> 16, a.dtype);
+        y[2] += from_bits16(res.y & 0xFFFFu, a.dtype);
+        y[3] += from_bits16(res.y >> 16, a.dtype);
     }
+    const size_t o = (size_t)m * a.out_stride + n;
     if (a.dtype == INT4VH_ROWS_F32) {
         Words4 v;
 #pragma unroll
@@ -177,107 +181,147 @@ __device__ __forceinline__ void finish_four(const LinArgs &a, int m, int n, cons
     }
 }
 
-// out_scales and bias of columns n .. n+3 (neutral past N or where absent)
+// out_scales and bias of columns n .. n+3 (neutral where absent; past N the
+// last column's, unused).  Every load is in flight before one is waited for.
 __device__ __forceinline__ void load_columns(const LinArgs &a, int n, float (&os)[4], float (&bs)[4])
 {
+    int c[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-        const bool in = n + r < a.N;
-        os[r] = in && a.out_scales ? a.out_scales[n + r] : 1.0f;
-        bs[r] = in && a.bias ? load_one(a.bias, n + r, a.dtype) : 0.0f;
+        c[r] = min(n + r, a.N - 1);
+        os[r] = 1.0f;
+        bs[r] = 0.0f;
+    }
+    if (a.out_scales)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            os[r] = a.out_scales[c[r]];
+    if (a.bias) {
+        if (a.dtype == INT4VH_ROWS_F32) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                bs[r] = static_cast<const float *>(a.bias)[c[r]];
+        } else {
+            uint32_t u[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                u[r] = static_cast<const uint16_t *>(a.bias)[c[r]];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                bs[r] = from_bits16(u[r], a.dtype);
+        }
     }
 }
 
-// ---------------------------------------------------------------- up to 32 rows
+// ---------------------------------------------------------------- up to 16 rows
+constexpr int kSRows = 16;
 constexpr int kSWaves = 8;
 constexpr int kSThreads = 64 * kSWaves;
 constexpr int kSMaxUnits = 8;                         // units of 128 channels per wave
 constexpr int kSMaxK = kSWaves * kSMaxUnits * 128;    // 8192 channels per workgroup
 
-// Grid (workgroups over tiles of 16 weight rows, parts of K).  kMB: blocks of
-// 16 activation rows; kUnits: units per wave.
-template <int kMB, int kUnits>
-__global__ void __launch_bounds__(kSThreads) linear_stream_kernel(LinArgs a)
+// Grid (workgroups over tiles of 16 weight rows, parts of K); kUnits: units per
+// wave.  Loads go along the rows (4 lanes a unit's 64 bytes of weights, 8 lanes
+// its 128 activation bytes: the cache looks up a line per row, not per lane)
+// and turn into fragments, whose lanes go along the column, in LDS of the
+// wave's own, without a barrier.  Slots are exchanged by chunk, against bank
+// conflicts.
+template <int kUnits>
+__global__ void __launch_bounds__(kSThreads, kUnits > 5 ? 2 : 4) linear_stream_kernel(LinArgs a)
 {
-    __shared__ __attribute__((aligned(16))) int32_t s_part[2][kSWaves][kMB][256];
+    constexpr int kTurn = kUnits > 2 ? kUnits : 2;    // KB per wave: its weights, or one unit of activations
+    __shared__ u32x4 s_turn[kSWaves][kTurn][64];
+    __shared__ __attribute__((aligned(16))) int32_t s_part[2][kSWaves][256];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int n16 = lane & 15, grp = lane >> 4;
     const int k_begin = (int)blockIdx.y * a.split_units * 128;
     const int k_end = min(a.K, k_begin + a.split_units * 128);
     const int n_tiles = a.tiles_n;
-    const int ch0 = k_begin + wave * (kUnits * 128) + 32 * grp;   // this lane's channels in its wave's unit 0
+    const int ch0 = k_begin + wave * (kUnits * 128);  // this wave's first channel
+    u32x4 *turn = &s_turn[wave][0][0];
 
+    const int wr = lane >> 2, wc = lane & 3;          // row and chunk of this lane's weight loads
+    const int wslot = wc * 16 + (wr ^ (2 * wc)), wread = grp * 16 + (n16 ^ (2 * grp));
     const size_t row_bytes = (size_t)(a.K / 2);
     auto load_w = [&](int tile, u32x4 (&q)[kUnits]) {
-        const int n = min(tile * 16 + n16, a.N - 1);
-        const uint8_t *row = a.w + (size_t)n * row_bytes;
+        const uint8_t *row = a.w + (size_t)min(tile * 16 + wr, a.N - 1) * row_bytes;
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
             // past the end: any valid chunk, it meets zero codes
-            const int c = min(ch0 + 128 * u, a.K - 32);
+            const int c = min(ch0 + 128 * u + 32 * wc, a.K - 32);
             q[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(row + c / 2));
         }
     };
-
     u32x4 q[kUnits];
     int tile = blockIdx.x;
     load_w(tile, q);
+    // the output element of this thread in every tile (the first 4 waves at
+    // most), its scales and bias asked for ahead of the sums
+    const int m = tid >> 4, nn = tid & 15;
+    const float row_scale = a.row_scales[min(m, a.M - 1)];
 
-    i32x4 A[kMB][kUnits][2];
+    i32x4 A[kUnits][2];
+    {
+        const int ac = lane & 7, ar = lane >> 3;      // chunk, and row within 8, of the activation loads
+        constexpr int kFly = kUnits < 4 ? kUnits : 4; // units whose loads are in flight together
 #pragma unroll
-    for (int mb = 0; mb < kMB; ++mb) {
-        const int m = mb * 16 + n16;
-        const int8_t *row = a.codes + (size_t)min(m, a.M - 1) * a.codes_stride;
+        for (int u0 = 0; u0 < kUnits; u0 += kFly) {
+            u32x4 raw[kFly][2];
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
-            const int c = ch0 + 128 * u;
-            u32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
-            if (m < a.M && c < k_end) {
-                lo = *reinterpret_cast<const u32x4 *>(row + c);
-                hi = *reinterpret_cast<const u32x4 *>(row + c + 16);
+            for (int v = 0; v < kFly; ++v)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = 8 * i + ar, c = ch0 + 128 * (u0 + v) + 16 * ac;
+                    raw[v][i] = u32x4{0, 0, 0, 0};
+                    if (u0 + v < kUnits && r < a.M && c < k_end)
+                        raw[v][i] = *reinterpret_cast<const u32x4 *>(a.codes + (size_t)r * a.codes_stride + c);
+                }
+#pragma unroll
+            for (int v = 0; v < kFly && u0 + v < kUnits; ++v) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    turn[(ac & 1) * 64 + (ac >> 1) * 16 + ((8 * i + ar) ^ ac)] =
+                        __builtin_bit_cast(u32x4, order_codes(raw[v][i]));
+                wave_fence();
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    A[u0 + v][h] = __builtin_bit_cast(i32x4, turn[h * 64 + grp * 16 + (n16 ^ (2 * grp + h))]);
+                wave_fence();
             }
-            order_codes(lo, hi, A[mb][u][0], A[mb][u][1]);
         }
     }
 
     for (int buf = 0; tile < n_tiles; buf ^= 1) {
-        const int next = tile + gridDim.x;
-        i32x4 acc[kMB];
+        const int next = tile + gridDim.x, n = tile * 16 + nn;
+        const float os = column_scale(a, min(n, a.N - 1)), bs = column_bias(a, min(n, a.N - 1));
 #pragma unroll
-        for (int mb = 0; mb < kMB; ++mb)
-            acc[mb] = i32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
-            const i32x4 w0 = weight_half(q[u], 0), w1 = weight_half(q[u], 1);
-#pragma unroll
-            for (int mb = 0; mb < kMB; ++mb) {
-                acc[mb] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w0, A[mb][u][0], acc[mb], 0, 0, 0);
-                acc[mb] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w1, A[mb][u][1], acc[mb], 0, 0, 0);
-            }
-        }
+        for (int u = 0; u < kUnits; ++u)
+            turn[u * 64 + wslot] = q[u];
+        wave_fence();
         if (next < n_tiles)
             load_w(next, q);
-        // D: column = activation row lane & 15, rows = weight rows 4 * grp + r
+        i32x4 acc = {0, 0, 0, 0};
 #pragma unroll
-        for (int mb = 0; mb < kMB; ++mb)
-            *reinterpret_cast<i32x4 *>(&s_part[buf][wave][mb][lane * 4]) = acc[mb];
+        for (int u = 0; u < kUnits; ++u) {
+            const u32x4 f = turn[u * 64 + wread];
+            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(weight_half(f, 0), A[u][0], acc, 0, 0, 0);
+            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(weight_half(f, 1), A[u][1], acc, 0, 0, 0);
+        }
+        wave_fence();
+        // D: column = activation row lane & 15, rows = weight rows 4 * grp + r
+        *reinterpret_cast<i32x4 *>(&s_part[buf][wave][lane * 4]) = acc;
         __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
         barrier_no_fence();                 // the other buffer is the next tile's
-        for (int o = tid; o < kMB * 256; o += kSThreads) {
-            const int mb = o >> 8, m = mb * 16 + ((o >> 4) & 15), nn = o & 15;
-            const int n = tile * 16 + nn;
-            if (m < a.M && n < a.N) {
-                const int at = ((nn >> 2) * 16 + (m & 15)) * 4 + (nn & 3);
-                int32_t sum = 0;
+        if (m < a.M && n < a.N) {
+            const int at = ((nn >> 2) * 16 + m) * 4 + (nn & 3);
+            int32_t sum = 0;
 #pragma unroll
-                for (int w = 0; w < kSWaves; ++w)
-                    sum += s_part[buf][w][mb][at];
-                if (a.parts)
-                    a.parts[((size_t)blockIdx.y * a.M + m) * a.n_pad + n] = sum;
-                else
-                    finish_one(a, m, n, sum, a.row_scales[m], a.out_scales ? a.out_scales[n] : 1.0f,
-                               a.bias ? load_one(a.bias, n, a.dtype) : 0.0f);
-            }
+            for (int w = 0; w < kSWaves; ++w)
+                sum += s_part[buf][w][at];
+            if (a.parts)
+                a.parts[((size_t)blockIdx.y * a.M + m) * a.n_pad + n] = sum;
+            else
+                finish_one(a, m, n, sum, row_scale, os, bs);
         }
         tile = next;
     }
@@ -285,23 +329,30 @@ __global__ void __launch_bounds__(kSThreads) linear_stream_kernel(LinArgs a)
 
 // ---------------------------------------------------------------- tiles
 // A workgroup computes kWM*kMB*16 activation rows x kWN*kNB*16 weight rows
-// with kWM x kWN waves.  Per K step of 128 channels each thread brings
-// 32-byte pieces of activations and 16-byte pieces of packed weights through
-// registers into LDS, in fragment order (every LDS access is 1 KB contiguous
-// per wave, no bank conflicts), one step ahead; two LDS buffers, one barrier a
-// step.
-template <int kWM, int kWN, int kMB, int kNB>
-__global__ void __launch_bounds__(64 * kWM *kWN) linear_tile_kernel(LinArgs a)
+// with kWM x kWN waves.  Per K step of 128 channels each thread brings 16-byte
+// chunks of activations and packed weights through registers into LDS, one
+// step ahead (two LDS buffers, one barrier a step); 8 (4) consecutive lanes
+// load a row's 128 (64) bytes, since a load costs the cache a lookup per line
+// and 16 lanes.  LDS holds fragments: chunk c of row r of a block of 16 rows
+// lies in group c, slot r ^ x(c), which keeps both the writes (lanes along a
+// row) and the reads (lanes along a column) free of bank conflicts.
+template <int kWM, int kWN, int kMB, int kNB, int kPerCu, int kDepth>
+__global__ void __launch_bounds__(64 * kWM *kWN, kWM *kWN *kPerCu / 4) linear_tile_kernel(LinArgs a)
 {
     constexpr int kThreads = 64 * kWM * kWN;
     constexpr int kBM = kWM * kMB, kBN = kWN * kNB;           // blocks of 16
-    constexpr int kAPer = kBM * 64 / kThreads, kWPer = kBN * 64 / kThreads;
-    static_assert(kAPer * kThreads == kBM * 64 && kWPer * kThreads == kBN * 64, "whole pieces per thread");
+    constexpr int kAPer = kBM * 128 / kThreads, kWPer = kBN * 64 / kThreads;
+    static_assert(kAPer * kThreads == kBM * 128 && kWPer * kThreads == kBN * 64, "whole chunks per thread");
     struct Lds {
         u32x4 act[kBM][2][64];
         u32x4 w[kBN][64];
     };
-    __shared__ Lds lds[2];
+    // the epilogue's use of LDS (per wave: 16 rows of sums and of residuals)
+    constexpr int kCols = kNB * 16, kPitch = kCols + 4;        // the pitch spreads the rows over the banks
+    constexpr int kRest = kCols / 2 + 2, kArea = 16 * (kPitch + kRest);
+    constexpr size_t kTurn = sizeof(int32_t) * kWM * kWN * kArea;
+    __shared__ __attribute__((aligned(16))) uint8_t mem[2 * sizeof(Lds) > kTurn ? 2 * sizeof(Lds) : kTurn];
+    Lds *lds = reinterpret_cast<Lds *>(mem);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int n16 = lane & 15, grp = lane >> 4;
     const int wm = wave % kWM, wn = wave / kWM;
@@ -319,45 +370,55 @@ __global__ void __launch_bounds__(64 * kWM *kWN) linear_tile_kernel(LinArgs a)
     const int m0 = (first + in % rows) * kBM * 16, n0 = (in / rows) * kBN * 16;
     const int s0 = part * a.split_units, s1 = min(s0 + a.split_units, (a.K + 127) / 128);
 
-    const int8_t *arow[kAPer];
-    const uint8_t *wrow[kWPer];
+    // Rows past the end load the last one (never stored).  Addresses are a
+    // uniform base, advanced by the step, and a 32-bit offset per chunk.
+    const int ac = tid & 7, wc = tid & 3;                      // this thread's chunk of its rows
+    const uint8_t *abase = reinterpret_cast<const uint8_t *>(a.codes) + (size_t)m0 * a.codes_stride;
+    const uint8_t *wbase = a.w + (size_t)n0 * (size_t)(a.K / 2);
+    uint32_t aoff[kAPer], woff[kWPer];
+    int aslot[kAPer], wslot[kWPer];
 #pragma unroll
     for (int j = 0; j < kAPer; ++j) {
-        const int m = m0 + ((tid + j * kThreads) >> 6) * 16 + n16;
-        arow[j] = a.codes + (size_t)min(m, a.M - 1) * a.codes_stride;
+        const int r = (tid + j * kThreads) >> 3;
+        aoff[j] = (uint32_t)min(r, a.M - 1 - m0) * (uint32_t)a.codes_stride + 16u * ac;
+        aslot[j] = ((r >> 4) * 2 + (ac & 1)) * 64 + (ac >> 1) * 16 + ((r & 15) ^ ac);
     }
 #pragma unroll
     for (int j = 0; j < kWPer; ++j) {
-        const int n = n0 + ((tid + j * kThreads) >> 6) * 16 + n16;
-        wrow[j] = a.w + (size_t)min(n, a.N - 1) * (size_t)(a.K / 2);
+        const int r = (tid + j * kThreads) >> 2;
+        woff[j] = (uint32_t)min(r, a.N - 1 - n0) * (uint32_t)(a.K / 2) + 16u * wc;
+        wslot[j] = (r >> 4) * 64 + wc * 16 + ((r & 15) ^ (2 * wc));
     }
-    u32x4 ra[kAPer][2], rw[kWPer];
-    auto load = [&](int s) {
-        const int c = s * 128 + 32 * grp;
-        const int cc = min(c, a.K - 32);
+    // kDepth steps are on their way in registers.  Loads past the last step
+    // repeat it, and chunks past K load the row's last one, so that every step
+    // issues the same loads without a branch; the codes past K are cleared on
+    // their way to LDS.
+    u32x4 ra[kDepth][kAPer], rw[kDepth][kWPer];
+    auto load = [&](int d, int step) {
+        const int s = min(step, s1 - 1);
+        const uint8_t *pa = abase + (size_t)s * 128, *pw = wbase + (size_t)s * 64;
+        const uint32_t backa = (uint32_t)max(0, s * 128 + 16 * ac - (a.K - 16));
+        const uint32_t backw = (uint32_t)max(0, s * 64 + 16 * wc - (a.K / 2 - 16));
 #pragma unroll
-        for (int j = 0; j < kAPer; ++j) {
-            const u32x4 *p = reinterpret_cast<const u32x4 *>(arow[j] + cc);
-            ra[j][0] = p[0];
-            ra[j][1] = p[1];
-        }
+        for (int j = 0; j < kAPer; ++j)
+            ra[d][j] = *reinterpret_cast<const u32x4 *>(pa + (aoff[j] - backa));
 #pragma unroll
         for (int j = 0; j < kWPer; ++j)
-            rw[j] = *reinterpret_cast<const u32x4 *>(wrow[j] + cc / 2);
+            rw[d][j] = *reinterpret_cast<const u32x4 *>(pw + (woff[j] - backw));
     };
-    auto store = [&](int s, Lds &l) {
-        const bool live = s * 128 + 32 * grp < a.K;            // channels past K: zero codes
+    auto store = [&](int d, int s, Lds &l) {
+        if (s * 128 + 128 > a.K) {
+            const bool live = s * 128 + 16 * ac < a.K;
 #pragma unroll
-        for (int j = 0; j < kAPer; ++j) {
-            i32x4 x0, x1;
-            order_codes(ra[j][0], ra[j][1], x0, x1);
-            const int b = (tid + j * kThreads) >> 6;
-            l.act[b][0][lane] = __builtin_bit_cast(u32x4, live ? x0 : i32x4{0, 0, 0, 0});
-            l.act[b][1][lane] = __builtin_bit_cast(u32x4, live ? x1 : i32x4{0, 0, 0, 0});
+            for (int j = 0; j < kAPer; ++j)
+                ra[d][j] = live ? ra[d][j] : u32x4{0, 0, 0, 0};
         }
 #pragma unroll
+        for (int j = 0; j < kAPer; ++j)
+            (&l.act[0][0][0])[aslot[j]] = __builtin_bit_cast(u32x4, order_codes(ra[d][j]));
+#pragma unroll
         for (int j = 0; j < kWPer; ++j)
-            l.w[(tid + j * kThreads) >> 6][lane] = rw[j];
+            (&l.w[0][0])[wslot[j]] = rw[d][j];
     };
 
     i32x4 acc[kMB][kNB];
@@ -367,24 +428,22 @@ __global__ void __launch_bounds__(64 * kWM *kWN) linear_tile_kernel(LinArgs a)
         for (int j = 0; j < kNB; ++j)
             acc[i][j] = i32x4{0, 0, 0, 0};
 
-    load(s0);
-    store(s0, lds[0]);
-    for (int s = s0; s < s1; ++s) {
-        const Lds &l = lds[(s - s0) & 1];
-        __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
-        barrier_no_fence();
-        const int sn = min(s + 1, s1 - 1);                     // the last step loads itself again, unused
-        load(sn);
+    const int rslot[2] = {grp * 16 + (n16 ^ (2 * grp)), grp * 16 + (n16 ^ (2 * grp + 1))};
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d)
+        load(d, s0 + d);
+    store(0, s0, lds[0]);
+    auto step = [&](const Lds &l) {
         u32x4 q[kNB];
 #pragma unroll
         for (int j = 0; j < kNB; ++j)
-            q[j] = l.w[wn * kNB + j][lane];
+            q[j] = l.w[wn * kNB + j][rslot[0]];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             i32x4 x[kMB];
 #pragma unroll
             for (int i = 0; i < kMB; ++i)
-                x[i] = __builtin_bit_cast(i32x4, l.act[wm * kMB + i][h][lane]);
+                x[i] = __builtin_bit_cast(i32x4, l.act[wm * kMB + i][h][rslot[h]]);
 #pragma unroll
             for (int j = 0; j < kNB; ++j) {
                 const i32x4 w = weight_half(q[j], h);
@@ -393,88 +452,149 @@ __global__ void __launch_bounds__(64 * kWM *kWN) linear_tile_kernel(LinArgs a)
                     acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, x[i], acc[i][j], 0, 0, 0);
             }
         }
-        if (s + 1 < s1)
-            store(s + 1, lds[(s + 1 - s0) & 1]);
+    };
+    constexpr int kTurns = kDepth % 2 ? 2 * kDepth : kDepth;   // steps after which buffers and registers repeat
+    for (int s = s0; s < s1; s += kTurns) {
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) {
+            if (s + i >= s1)
+                break;
+            __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+            barrier_no_fence();
+            load(i % kDepth, s + i + kDepth);
+            step(lds[i & 1]);
+            store((i + 1) % kDepth, s + i + 1, lds[(i + 1) & 1]);
+        }
     }
 
-    // D: column = activation row lane & 15, rows = weight rows 4 * grp + r
-    if (a.parts) {
+    // D: column = activation row lane & 15, rows = weight rows 4 * grp + r.
+    // Each wave turns its sums around in LDS, 16 activation rows at a time, so
+    // that its lanes hold four columns of a row and rows are written whole.
+    // The residual passes through LDS as well, loaded before anything is
+    // stored: a wait for a load also waits for the stores in front of it.
+    int32_t *turn = reinterpret_cast<int32_t *>(mem) + wave * kArea;
+    uint32_t *rest = reinterpret_cast<uint32_t *>(turn + 16 * kPitch);
+    constexpr int kLanes = kCols / 4, kStep = 64 / kLanes, kIter = 16 / kStep;   // lanes of a row; rows at a time
+    const int c4 = (lane % kLanes) * 4, n = n0 + wn * kCols + c4, r0 = lane / kLanes;
+    const int mw = m0 + wm * kMB * 16;
+    static_assert(kMB <= 8, "two registers hold a wave's row scales");
+    float os[4], bs[4], rs0 = 0.0f, rs1 = 0.0f;
+    Pair2 res[kMB][kIter];
+    // The usual case handles four columns at a time, with a 16-bit residual or
+    // none; rows that end inside a lane's four columns, and binary32 residuals,
+    // go element by element.
+    const bool wide = !a.parts && a.N % 4 == 0 && (!a.residual || a.dtype != INT4VH_ROWS_F32);
+    const bool early = wide && a.residual;
+    if (!a.parts) {
+        load_columns(a, n, os, bs);
+        rs0 = a.row_scales[min(mw + lane, a.M - 1)];
+        rs1 = a.row_scales[min(mw + 64 + lane, a.M - 1)];
+        if (early)
 #pragma unroll
-        for (int i = 0; i < kMB; ++i) {
-            const int m = m0 + (wm * kMB + i) * 16 + n16;
+            for (int i = 0; i < kMB; ++i)
 #pragma unroll
-            for (int j = 0; j < kNB; ++j) {
-                const int n = n0 + (wn * kNB + j) * 16 + 4 * grp;
-                if (m < a.M && n < a.n_pad)
-                    *reinterpret_cast<i32x4 *>(&a.parts[((size_t)part * a.M + m) * a.n_pad + n]) = acc[i][j];
+                for (int k = 0; k < kIter; ++k) {
+                    const int m = min(mw + i * 16 + r0 + k * kStep, a.M - 1);
+                    res[i][k] = *reinterpret_cast<const Pair2 *>(static_cast<const uint16_t *>(a.residual) +
+                                                                 (size_t)m * a.residual_stride + min(n, a.N - 4));
+                }
+    }
+    // nothing below loads from memory in the usual case: a wait for a load
+    // would also wait for the stores in front of it
+    __builtin_amdgcn_s_waitcnt(0);
+    barrier_no_fence();                                        // the last step's reads are done
+#pragma unroll
+    for (int i = 0; i < kMB; ++i) {
+        const int mi = mw + i * 16;
+#pragma unroll
+        for (int j = 0; j < kNB; ++j)
+            *reinterpret_cast<i32x4 *>(turn + n16 * kPitch + j * 16 + 4 * grp) = acc[i][j];
+        if (early)
+#pragma unroll
+            for (int k = 0; k < kIter; ++k)
+                *reinterpret_cast<uint2 *>(rest + (r0 + k * kStep) * kRest + c4 / 2) =
+                    make_uint2(res[i][k].w[0], res[i][k].w[1]);
+        wave_fence();
+        const float rsi = i < 4 ? rs0 : rs1;
+        if (wide) {
+#pragma nounroll
+            for (int r = r0; r < 16; r += kStep) {
+                const i32x4 v = *reinterpret_cast<const i32x4 *>(turn + r * kPitch + c4);
+                const uint2 rv = *reinterpret_cast<const uint2 *>(rest + r * kRest + c4 / 2);
+                const float row_scale = __shfl(rsi, (i & 3) * 16 + r);
+                if (mi + r < a.M && n < a.N)
+                    finish_four(a, mi + r, n, v, row_scale, os, bs, early, rv);
+            }
+        } else if (a.parts) {
+#pragma nounroll
+            for (int r = r0; r < 16; r += kStep)
+                if (mi + r < a.M && n < a.N)
+                    *reinterpret_cast<i32x4 *>(&a.parts[((size_t)part * a.M + mi + r) * a.n_pad + n]) =
+                        *reinterpret_cast<const i32x4 *>(turn + r * kPitch + c4);
+        } else {
+#pragma nounroll
+            for (int e = lane; e < 16 * kCols; e += 64) {
+                const int m = mi + e / kCols, c = n0 + wn * kCols + e % kCols;
+                if (m < a.M && c < a.N)
+                    finish_one(a, m, c, turn[e / kCols * kPitch + e % kCols], a.row_scales[m],
+                               column_scale(a, c), column_bias(a, c));
             }
         }
-        return;
-    }
-    float rs[kMB];
-#pragma unroll
-    for (int i = 0; i < kMB; ++i)
-        rs[i] = a.row_scales[min(m0 + (wm * kMB + i) * 16 + n16, a.M - 1)];
-#pragma unroll
-    for (int j = 0; j < kNB; ++j) {
-        const int n = n0 + (wn * kNB + j) * 16 + 4 * grp;
-        float os[4], bs[4];
-        load_columns(a, n, os, bs);
-#pragma unroll
-        for (int i = 0; i < kMB; ++i) {
-            const int m = m0 + (wm * kMB + i) * 16 + n16;
-            if (m < a.M && n < a.N)
-                finish_four(a, m, n, acc[i][j], rs[i], os, bs);
-        }
+        wave_fence();
     }
 }
 
-// The parts' sums and the epilogue: one thread per four columns.
+// The parts' sums and the epilogue: one thread per element.
 __global__ void __launch_bounds__(256) linear_join_kernel(LinArgs a)
 {
-    const int per_row = a.n_pad / 4;
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (i >= (long long)a.M * per_row)
+    if (i >= (long long)a.M * a.N)
         return;
-    const int m = (int)(i / per_row), n = (int)(i % per_row) * 4;
-    i32x4 sum = {0, 0, 0, 0};
+    const int m = (int)(i / a.N), n = (int)(i % a.N);
+    int32_t sum = 0;
     for (int p = 0; p < a.splits; ++p)
-        sum += *reinterpret_cast<const i32x4 *>(&a.parts[((size_t)p * a.M + m) * a.n_pad + n]);
-    float os[4], bs[4];
-    load_columns(a, n, os, bs);
-    finish_four(a, m, n, sum, a.row_scales[m], os, bs);
+        sum += a.parts[((size_t)p * a.M + m) * a.n_pad + n];
+    finish_one(a, m, n, sum, a.row_scales[m], column_scale(a, n), column_bias(a, n));
 }
 
 // ---------------------------------------------------------------- host side
 
 // How a call of these sizes runs.
+enum Kind { kStream, kTile32, kTile64, kTile128 };   // tiles of 32, 64, 128 rows x 128 columns
 struct Plan {
-    int kind;                  // 0: stream, 1: tiles of 256 x 256, 2: 128 x 128, 3: 64 x 128
+    Kind kind;
     int splits, split_units;
     int tiles_m, tiles_n;
 };
 
+long long tiles_of(int M, int N, int bm)
+{
+    return (long long)((M + bm - 1) / bm) * ((N + 127) / 128);
+}
+
+// Larger tiles reuse more of what they load, smaller ones fill more compute
+// units.
 Plan plan_for(int M, int N, int K, int cus)
 {
     Plan p;
     const int units = (K + 127) / 128;
-    if (M <= 32) {
-        p.kind = 0;
+    p.splits = 1;
+    if (M <= kSRows) {
+        p.kind = kStream;
         p.tiles_m = 1;
         p.tiles_n = (N + 15) / 16;
         p.splits = (K + kSMaxK - 1) / kSMaxK;
     } else {
-        const int bm[4] = {0, 256, 128, 64}, bn[4] = {0, 256, 128, 128};
-        p.kind = 3;
-        if (M > 64)
-            p.kind = (long long)((M + 255) / 256) * ((N + 255) / 256) >= cus ? 1 : 2;
-        p.tiles_m = (M + bm[p.kind] - 1) / bm[p.kind];
-        p.tiles_n = (N + bn[p.kind] - 1) / bn[p.kind];
-        const long long tiles = (long long)p.tiles_m * p.tiles_n;
-        p.splits = 1;
-        // at least 4 steps of 128 channels in a part
-        while (p.splits * 2 * tiles <= 2 * cus && units / (p.splits * 2) >= 4)
-            p.splits *= 2;
+        p.kind = 2 * tiles_of(M, N, 128) >= 5ll * cus  ? kTile128
+                 : 4 * tiles_of(M, N, 64) >= 5ll * cus ? kTile64
+                                                       : kTile32;
+        const int bm = p.kind == kTile128 ? 128 : p.kind == kTile64 ? 64 : 32;
+        p.tiles_m = (M + bm - 1) / bm;
+        p.tiles_n = (N + 127) / 128;
+        // few tiles: parts of at least 4 units, up to two workgroups a compute unit
+        if (p.kind == kTile32)
+            while (2 * p.splits * tiles_of(M, N, 32) <= 2ll * cus && units / (2 * p.splits) >= 4)
+                p.splits *= 2;
     }
     p.split_units = (units + p.splits - 1) / p.splits;
     p.splits = (units + p.split_units - 1) / p.split_units;
@@ -507,21 +627,20 @@ bool sizes_supported(int M, int N, int K)
     return K <= 65536 && N <= (1 << 24) && M <= (1 << 20) && (long long)M * N < (1ll << 40);
 }
 
-template <int kMB>
 void launch_stream(const LinArgs &a, dim3 grid, hipStream_t s)
 {
     const int per_wave = (a.split_units + kSWaves - 1) / kSWaves;
     const dim3 block(kSThreads);
     if (per_wave <= 1)
-        hipLaunchKernelGGL((linear_stream_kernel<kMB, 1>), grid, block, 0, s, a);
+        hipLaunchKernelGGL(linear_stream_kernel<1>, grid, block, 0, s, a);
     else if (per_wave <= 2)
-        hipLaunchKernelGGL((linear_stream_kernel<kMB, 2>), grid, block, 0, s, a);
+        hipLaunchKernelGGL(linear_stream_kernel<2>, grid, block, 0, s, a);
     else if (per_wave <= 3)
-        hipLaunchKernelGGL((linear_stream_kernel<kMB, 3>), grid, block, 0, s, a);
+        hipLaunchKernelGGL(linear_stream_kernel<3>, grid, block, 0, s, a);
     else if (per_wave <= 5)
-        hipLaunchKernelGGL((linear_stream_kernel<kMB, 5>), grid, block, 0, s, a);
+        hipLaunchKernelGGL(linear_stream_kernel<5>, grid, block, 0, s, a);
     else
-        hipLaunchKernelGGL((linear_stream_kernel<kMB, 8>), grid, block, 0, s, a);
+        hipLaunchKernelGGL(linear_stream_kernel<8>, grid, block, 0, s, a);
 }
 
 } // namespace
@@ -550,7 +669,7 @@ int linear_int4_rows(const int8_t *codes, int64_t codes_stride, const float *row
         !rows_aligned(row_scales, 4) || !rows_aligned(out_scales, 4) || !rows_aligned(bias, el) ||
         !rows_aligned(residual, el) || !rows_aligned(out, el))
         return INT4VH_EALIGN;
-    if (!sizes_supported(M, N, K))
+    if (!sizes_supported(M, N, K) || (M > 1 && codes_stride >= (1ll << 24)))   // a tile's chunks have 32-bit offsets
         return INT4VH_EUNSUPPORTED;
     const int cus = current_cus();
     const Plan p = plan_for(M, N, K, cus);
@@ -587,25 +706,20 @@ int linear_int4_rows(const int8_t *codes, int64_t codes_stride, const float *row
     a.tiles_n = p.tiles_n;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     const dim3 tiles((unsigned)((long long)p.tiles_m * p.tiles_n * p.splits));
-    if (p.kind == 0) {
-        const dim3 grid(p.tiles_n < 2 * cus ? p.tiles_n : 2 * cus, p.splits);
-        if (M <= 16)
-            launch_stream<1>(a, grid, s);
-        else
-            launch_stream<2>(a, grid, s);
-    } else if (p.kind == 1) {
-        hipLaunchKernelGGL((linear_tile_kernel<4, 2, 4, 8>), tiles, dim3(512), 0, s, a);
-    } else if (p.kind == 2) {
-        hipLaunchKernelGGL((linear_tile_kernel<2, 2, 4, 4>), tiles, dim3(256), 0, s, a);
-    } else {
-        hipLaunchKernelGGL((linear_tile_kernel<1, 4, 4, 2>), tiles, dim3(256), 0, s, a);
-    }
+    if (p.kind == kStream)
+        launch_stream(a, dim3(p.tiles_n < 2 * cus ? p.tiles_n : 2 * cus, p.splits), s);
+    else if (p.kind == kTile32)
+        hipLaunchKernelGGL((linear_tile_kernel<1, 4, 2, 2, 4, 3>), tiles, dim3(256), 0, s, a);
+    else if (p.kind == kTile64)
+        hipLaunchKernelGGL((linear_tile_kernel<1, 4, 4, 2, 4, 2>), tiles, dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((linear_tile_kernel<2, 2, 4, 4, 2, 2>), tiles, dim3(256), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return hip_fail(e, "linear kernel launch");
     if (need) {
-        const long long n4 = (long long)M * (a.n_pad / 4);
-        hipLaunchKernelGGL(linear_join_kernel, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, s, a);
+        const long long n1 = (long long)M * N;
+        hipLaunchKernelGGL(linear_join_kernel, dim3((unsigned)((n1 + 255) / 256)), dim3(256), 0, s, a);
         e = hipGetLastError();
         if (e != hipSuccess)
             return hip_fail(e, "linear join kernel launch");
