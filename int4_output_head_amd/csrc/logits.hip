@@ -6,18 +6,20 @@
 // call); a row of 151936 binary32 logits is 608 KB against a few KB of rules.
 // The rules' cost is finding each token's count, which depends on the request
 // and hardly on the row: a workgroup takes a slice of the vocabulary and
-// several rows of ONE request, counts the slice's tokens of the request's
-// history in LDS (integer atomics: any order gives the same counts), and then
-// walks its rows; a row's draft is counted for the rows behind it.  The
-// history is read once per slice and row group, from L2.
+// several rows of ONE request and counts the slice's tokens of the request's
+// history in LDS (integer atomics: any order gives the same counts).  Its
+// waves then walk the slice, one or more to a row, 1024 tokens at a time with
+// the next ones' loads in flight; a lane's tokens lie 64 apart, so that a
+// mask's 64 bits are one scalar and a group without counts costs one test.
+// The history is read once per slice and row group, from L2.
 //
-// Verification keeps one pass over the logits: each wave reduces 1024 tokens
-// of a row, held in registers (16 per lane), to the best keys, (max, sum) and
-// the draft's logit; rules_merge_kernel joins the chunks of each row and
-// counts accepted drafts.  A chunk's top-k goes by a threshold: the k-th
-// largest of the 64 lanes' maxima is at most the chunk's k-th value, so the
-// few values that reach it are the candidates; they are ranked by counting
-// the larger ones.  Everything is exact, ties included (keys are distinct).
+// Verification keeps one pass over the logits: each wave keeps its tokens'
+// best keys in a small buffer, their (max, sum) and the draft's logit, and
+// rules_merge_kernel joins the waves' lists of each row and counts accepted
+// drafts.  The top-k goes by thresholds: at first the k-th largest of the 64
+// lanes' maxima, which is at most the k-th value, then the k-th key held; the
+// few values that reach it are ranked by counting the larger ones.  Exact for
+// any input, ties included (keys are distinct, and a later token loses a tie).
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -36,14 +38,28 @@ using namespace int4vh_detail;
 
 typedef unsigned long long u64;
 
-constexpr int kChunk = 1024;              // tokens of a row per wave
-constexpr int kPer = kChunk / 64;         // tokens per lane: 4 at a time, 256 apart
+constexpr int kChunk = 1024;              // tokens of a row that a wave holds at a time
+constexpr int kPer = kChunk / 64;         // tokens per lane, 64 apart
 constexpr int kMaxWaves = 8;
+constexpr int kMaxSlice = kMaxWaves * kChunk;   // tokens of a workgroup's slice
 constexpr int kMaxTopK = 16;
 constexpr int kMaxRows = 4096;
 constexpr int kBuf = 128;                 // candidate keys per wave
 constexpr float kNegInf = -__builtin_huge_valf();
-constexpr uint32_t kSeen = 0x80000000u;   // count word: in the history's prompt; low bits: times generated
+
+// A token's word in LDS: times generated, whether it is in the prompt, and the
+// number of its last bias entry (from 1; 0: none).  Where a call's histories
+// and biases are short enough all three share 32 bits, which halves the LDS of
+// a slice (three workgroups a compute unit instead of two); otherwise entries
+// have words of their own.
+struct WordLayout {
+    uint32_t count, seen;     // bits
+    int entry_shift;          // of the entry in a shared word; 0: not shared
+};
+constexpr WordLayout kShared = {(1u << 20) - 1u, 1u << 20, 21};
+constexpr WordLayout kApart = {0x7FFFFFFFu, 0x80000000u, 0};
+constexpr long long kSharedHistory = (1ll << 20) - 32;   // generated tokens, drafts on top
+constexpr long long kSharedEntries = (1 << 11) - 1;
 
 struct RulesArgs {
     const void *logits;
@@ -52,16 +68,19 @@ struct RulesArgs {
     int R, T, V;
     int4vh_logit_rules r;      // zeros for none
     int has_penalty, has_bias;
+    WordLayout word;
     int row_group;             // rows per workgroup
+    int ways;                  // waves per row
+    int slice;                 // tokens per workgroup: a multiple of ways * kChunk
     // apply
     void *out;
     long long out_stride;
     // verify
-    int top_k, n_chunks;
+    int top_k, n_lists;
     float lse_scale;           // log2(e) / temperature
-    u64 *heads;                // [R*T, n_chunks] best key of each chunk, 0 if none
-    u64 *lists;                // [R*T, n_chunks, top_k] best keys, best first, 0 past the last
-    float2 *sums;              // [R*T, n_chunks] (max, sum of exp2((x - max) * lse_scale))
+    u64 *heads;                // [R*T, n_lists] best key of each wave's tokens, 0 if none
+    u64 *lists;                // [R*T, n_lists, top_k] best keys, best first, 0 past the last
+    float2 *sums;              // [R*T, n_lists] (max, sum of exp2((x - max) * lse_scale))
     float *draft_logit;        // [R*T] ruled logit of the row's draft, where it is in [0, V)
 };
 
@@ -76,10 +95,13 @@ __device__ __forceinline__ u64 order_key(float v, int token)
 {
     return ((u64)order_word(v) << 32) | (u64)(~(uint32_t)token);
 }
+__device__ __forceinline__ float word_value(uint32_t u)
+{
+    return __uint_as_float((u & 0x80000000u) ? (u & 0x7FFFFFFFu) : ~u);
+}
 __device__ __forceinline__ float key_value(u64 k)
 {
-    const uint32_t u = (uint32_t)(k >> 32);
-    return __uint_as_float((u & 0x80000000u) ? (u & 0x7FFFFFFFu) : ~u);
+    return word_value((uint32_t)(k >> 32));
 }
 __device__ __forceinline__ int key_token(u64 k)
 {
@@ -130,23 +152,48 @@ __device__ __forceinline__ void wave_fence()
     asm volatile("" ::: "memory");
 }
 
+__device__ __forceinline__ u64 readlane64(u64 k, int src)
+{
+    return (u64)(uint32_t)__builtin_amdgcn_readlane((uint32_t)(k >> 32), src) << 32 |
+           (uint32_t)__builtin_amdgcn_readlane((uint32_t)k, src);
+}
+
+// The number of lanes of m below this one.
+__device__ __forceinline__ int lane_rank(u64 m)
+{
+    return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
+}
+
 // Keeps the k best of the n (<= kBuf) distinct keys buf[0, n), best first, and
 // returns how many there are (min(n, k)).  A key's rank is the number of
-// larger ones.  Called by a whole wave on its own buffer.
+// larger ones, which pass by in scalar registers.  Called by a whole wave on
+// its own buffer.
 __device__ __forceinline__ int keep_best(volatile u64 *buf, int n, int k, int lane)
 {
-    const u64 a = lane < n ? buf[lane] : 0ull, b = lane + 64 < n ? buf[lane + 64] : 0ull;
-    int ra = 0, rb = 0;
-    for (int i = 0; i < n; ++i) {
-        const u64 o = buf[i];
-        ra += o > a;
-        rb += o > b;
+    const u64 a = lane < n ? buf[lane] : 0ull;
+    int ra = 0;
+    if (n <= 64) {
+        for (int i = 0; i < n; ++i)
+            ra += readlane64(a, i) > a;
+    } else {
+        const u64 b = lane + 64 < n ? buf[lane + 64] : 0ull;
+        int rb = 0;
+        for (int i = 0; i < 64; ++i) {
+            const u64 o = readlane64(a, i);
+            ra += o > a;
+            rb += o > b;
+        }
+        for (int i = 0; i < n - 64; ++i) {
+            const u64 o = readlane64(b, i);
+            ra += o > a;
+            rb += o > b;
+        }
+        if (lane + 64 < n && rb < k)
+            buf[rb] = b;
     }
-    wave_fence();
+    // (a lane's own keys are in registers: no read follows these writes)
     if (lane < n && ra < k)
         buf[ra] = a;
-    if (lane + 64 < n && rb < k)
-        buf[rb] = b;
     wave_fence();
     return n < k ? n : k;
 }
@@ -163,7 +210,7 @@ __device__ __forceinline__ void push(volatile u64 *buf, int &n, u64 key, u64 mas
         }
     }
     if (mask >> lane & 1ull)
-        buf[n + __popcll(mask & ((1ull << lane) - 1ull))] = key;
+        buf[n + lane_rank(mask)] = key;
     wave_fence();
     n += __popcll(mask);
 }
@@ -188,67 +235,23 @@ __device__ __forceinline__ uint32_t reach_threshold(uint32_t word, int k)
     return th ? th : 1u;
 }
 
-// Four consecutive logits token .. token+3 of a row (-infinity past V).
+// Logit `token` of a row.
 template <int kDtype>
-__device__ __forceinline__ void load4(const void *row, int token, int V, float (&v)[4])
+__device__ __forceinline__ float load_logit(const void *row, int token)
 {
-    if (token + 4 <= V) {
-        if constexpr (kDtype == INT4VH_ROWS_F32) {
-            const Words4 w = *reinterpret_cast<const Words4 *>(static_cast<const float *>(row) + token);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                v[j] = __uint_as_float(w.w[j]);
-        } else {
-            const Pair2 w = *reinterpret_cast<const Pair2 *>(static_cast<const uint16_t *>(row) + token);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                v[j] = from_bits16((w.w[j >> 1] >> (16 * (j & 1))) & 0xFFFFu, kDtype);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[j] = kNegInf;
-            if (token + j < V) {
-                if constexpr (kDtype == INT4VH_ROWS_F32)
-                    v[j] = static_cast<const float *>(row)[token + j];
-                else
-                    v[j] = from_bits16(static_cast<const uint16_t *>(row)[token + j], kDtype);
-            }
-        }
-    }
+    if constexpr (kDtype == INT4VH_ROWS_F32)
+        return static_cast<const float *>(row)[token];
+    else
+        return from_bits16(static_cast<const uint16_t *>(row)[token], kDtype);
 }
 
 template <int kDtype>
-__device__ __forceinline__ void store4(void *row, int token, int V, const float (&v)[4])
+__device__ __forceinline__ void store_logit(void *row, int token, float v)
 {
-    if constexpr (kDtype == INT4VH_ROWS_F32) {
-        float *p = static_cast<float *>(row) + token;
-        if (token + 4 <= V) {
-            Words4 w;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                w.w[j] = __float_as_uint(v[j]);
-            *reinterpret_cast<Words4 *>(p) = w;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (token + j < V)
-                    p[j] = v[j];
-        }
-    } else {
-        uint16_t *p = static_cast<uint16_t *>(row) + token;
-        if (token + 4 <= V) {
-            Pair2 w;
-            w.w[0] = to_bits16(v[0], kDtype) | (to_bits16(v[1], kDtype) << 16);
-            w.w[1] = to_bits16(v[2], kDtype) | (to_bits16(v[3], kDtype) << 16);
-            *reinterpret_cast<Pair2 *>(p) = w;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (token + j < V)
-                    p[j] = (uint16_t)to_bits16(v[j], kDtype);
-        }
-    }
+    if constexpr (kDtype == INT4VH_ROWS_F32)
+        static_cast<float *>(row)[token] = v;
+    else
+        static_cast<uint16_t *>(row)[token] = (uint16_t)to_bits16(v, kDtype);
 }
 
 __device__ __forceinline__ long long clamp64(long long v, long long lo, long long hi)
@@ -256,230 +259,324 @@ __device__ __forceinline__ long long clamp64(long long v, long long lo, long lon
     return v < lo ? lo : v > hi ? hi : v;
 }
 
-// The slice's counts and biases of one request, with the drafts in front of
-// row t0 counted.  cnt: words (kSeen | times generated) of tokens base ..
-// base + S - 1; bias: their biases.  Called by the whole workgroup, which
-// waits at the end.
-__device__ __forceinline__ void prepare_slice(const RulesArgs &a, int req, int t0, int base, int S, uint32_t *cnt,
-                                              float *bias)
+// The slice's tokens in one request's history and biases: the words of tokens
+// base .. base + S - 1, and the entries' where they lie apart.  Called by the
+// whole workgroup, which waits at the end.
+__device__ __forceinline__ void prepare_slice(const RulesArgs &a, int req, int base, int S, uint32_t *words,
+                                              uint32_t *entries)
 {
     const int tid = threadIdx.x, nt = blockDim.x;
-    if (a.has_penalty)
-        for (int i = tid; i < S; i += nt)
-            cnt[i] = 0u;
-    uint32_t *order = reinterpret_cast<uint32_t *>(bias);
-    if (a.has_bias)
-        for (int i = tid; i < S; i += nt)
-            order[i] = 0u;
-    __syncthreads();
-    if (a.has_penalty) {
-        if (a.r.history) {
-            const long long b = clamp64(a.r.history_offsets[req], 0, a.r.n_history);
-            const long long e = clamp64(a.r.history_offsets[req + 1], 0, a.r.n_history);
-            const long long made = b + (a.r.n_prompt ? a.r.n_prompt[req] : 0);
-            constexpr int kFly = 8;                 // loads in flight per thread
-            for (long long i0 = b + tid; i0 < e; i0 += (long long)nt * kFly) {
-                int32_t v[kFly];
-#pragma unroll
-                for (int u = 0; u < kFly; ++u) {
-                    const long long i = i0 + (long long)u * nt;
-                    v[u] = i < e ? a.r.history[i] : -1;
-                }
-#pragma unroll
-                for (int u = 0; u < kFly; ++u) {
-                    const uint32_t at = (uint32_t)v[u] - (uint32_t)base;
-                    if (v[u] >= 0 && at < (uint32_t)S) {
-                        if (i0 + (long long)u * nt < made)
-                            atomicOr(&cnt[at], kSeen);
-                        else
-                            atomicAdd(&cnt[at], 1u);
-                    }
-                }
-            }
-        }
-        if (tid < t0) {
-            const int d = a.draft[(size_t)req * (a.T - 1) + tid];
-            const uint32_t at = (uint32_t)d - (uint32_t)base;
-            if (d >= 0 && at < (uint32_t)S)
-                atomicAdd(&cnt[at], 1u);
-        }
+    long long hb = 0, he = 0, made = 0, bb = 0, be = 0;
+    if (a.has_penalty && a.r.history) {
+        hb = clamp64(a.r.history_offsets[req], 0, a.r.n_history);
+        he = clamp64(a.r.history_offsets[req + 1], 0, a.r.n_history);
+        made = hb + (a.r.n_prompt ? a.r.n_prompt[req] : 0);
     }
     if (a.has_bias) {
-        // the last entry of an id holds: the largest entry number, then, each
-        // thread at its own tokens, that entry's value
-        const long long b = clamp64(a.r.bias_offsets[req], 0, a.r.n_bias);
-        const long long e = clamp64(a.r.bias_offsets[req + 1], 0, a.r.n_bias);
-        for (long long i = b + tid; i < e; i += nt) {
-            const int32_t v = a.r.bias_ids[i];
-            const uint32_t at = (uint32_t)v - (uint32_t)base;
-            if (v >= 0 && at < (uint32_t)S)
-                atomicMax(&order[at], (uint32_t)(i - b) + 1u);
+        bb = clamp64(a.r.bias_offsets[req], 0, a.r.n_bias);
+        be = clamp64(a.r.bias_offsets[req + 1], 0, a.r.n_bias);
+    }
+    constexpr int kFly = 4;                   // loads of four tokens in flight per thread
+    Words4 v[kFly];
+    auto load = [&](long long i0) {
+#pragma unroll
+        for (int u = 0; u < kFly; ++u) {
+            const long long i = i0 + 4ll * u * nt;
+            v[u] = Words4{{~0u, ~0u, ~0u, ~0u}};
+            if (i + 4 <= he) {
+                v[u] = *reinterpret_cast<const Words4 *>(a.r.history + i);
+            } else {
+                for (int j = 0; j < 3; ++j)
+                    if (i + j < he)
+                        v[u].w[j] = (uint32_t)a.r.history[i + j];
+            }
         }
-        __syncthreads();
-        for (int i = tid; i < S; i += nt) {
-            const uint32_t o = order[i];
-            bias[i] = o ? a.r.bias_values[b + (o - 1u)] : 0.0f;
+    };
+    load(hb + 4 * tid);
+    int32_t id = -1;
+    if (bb + tid < be)
+        id = a.r.bias_ids[bb + tid];
+    const int n_words = entries == words ? S : 2 * S;
+    uint4 *clear = reinterpret_cast<uint4 *>(words);
+    for (int i = tid; i < n_words / 4; i += nt)
+        clear[i] = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
+    if (a.has_bias) {
+        for (long long i = bb + tid; i < be; i += nt) {
+            if (i != bb + tid)
+                id = a.r.bias_ids[i];
+            const uint32_t at = (uint32_t)id - (uint32_t)base;
+            if (id >= 0 && at < (uint32_t)S)
+                atomicMax(&entries[at], ((uint32_t)(i - bb) + 1u) << a.word.entry_shift);
         }
+        if (entries == words)
+            __syncthreads();                  // the maxima are taken before anything is added to them
+    }
+    for (long long i0 = hb + 4 * tid; i0 < he; i0 += 4ll * nt * kFly) {
+        if (i0 != hb + 4 * tid)
+            load(i0);
+#pragma unroll
+        for (int u = 0; u < kFly; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int32_t token = (int32_t)v[u].w[j];
+                const uint32_t at = (uint32_t)token - (uint32_t)base;
+                if (token >= 0 && at < (uint32_t)S) {
+                    if (i0 + 4ll * u * nt + j < made)
+                        atomicOr(&words[at], a.word.seen);
+                    else
+                        atomicAdd(&words[at], 1u);
+                }
+            }
     }
     __syncthreads();
 }
 
-__device__ __forceinline__ float penalise(float l, uint32_t word, float rep, float freq, float pres)
+__device__ __forceinline__ float penalise(float l, uint32_t count, float rep, float freq, float pres)
 {
-    const uint32_t count = word & ~kSeen;
     float x = l > 0.0f ? l / rep : l * rep;
     x = x - freq * (float)count;
     return x - (count ? pres : 0.0f);
 }
 
-// Grid (slices of the vocabulary, requests, row groups); each wave takes a
-// chunk of kChunk tokens.  kVerify: reduce the rows; otherwise write them out.
+// Grid (slices of the vocabulary, requests, row groups); wave w takes row w /
+// ways of the group and the (w % ways)-th part of the slice.  kVerify: reduce
+// the rows; otherwise write them out.
 template <int kDtype, bool kVerify, bool kTopK, bool kLse>
 __global__ void __launch_bounds__(64 * kMaxWaves) rules_kernel(RulesArgs a)
 {
     extern __shared__ __attribute__((aligned(16))) uint32_t s_mem[];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n_waves = blockDim.x >> 6;
-    const int S = n_waves * kChunk;
-    uint32_t *cnt = s_mem;
-    float *bias = reinterpret_cast<float *>(s_mem + (a.has_penalty ? S : 0));
-    volatile u64 *buf = reinterpret_cast<u64 *>(s_mem + (a.has_penalty ? S : 0) + (a.has_bias ? S : 0)) + wave * kBuf;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int S = a.slice, V = a.V;
+    uint32_t *words = s_mem;
+    uint32_t *entries = s_mem + (a.has_penalty && a.has_bias && !a.word.entry_shift ? S : 0);
+    volatile u64 *buf = reinterpret_cast<u64 *>(entries + (a.has_penalty || a.has_bias ? S : 0)) + wave * kBuf;
     const int base = blockIdx.x * S;
     const int req = blockIdx.y;
-    const int t0 = blockIdx.z * a.row_group, t1 = min(a.T, t0 + a.row_group);
-    const int V = a.V;
+    const int t = blockIdx.z * a.row_group + wave / a.ways, way = wave % a.ways;
+    const int part = S / a.ways, begin = base + way * part;        // this wave's tokens
+    const int n_chunks = begin < V ? (min(part, V - begin) + kChunk - 1) / kChunk : 0;
+    const int row = req * a.T + min(t, a.T - 1);
+    constexpr size_t kSize = kDtype == INT4VH_ROWS_F32 ? 4 : 2;
+    const char *lrow = static_cast<const char *>(a.logits) + (size_t)row * a.logits_stride * kSize;
+
+    const uint32_t *mask = nullptr;
+    bool none = false;                        // nothing is allowed
+    if (a.r.mask) {
+        const long long mi = a.r.mask_index ? a.r.mask_index[row] : row;
+        none = mi >= a.r.n_masks;
+        if (mi >= 0 && !none)
+            mask = a.r.mask + (size_t)mi * a.r.mask_stride;
+    }
+    const int mask_words = (V + 31) / 32;
+
+    // A chunk's logits, and its mask in the lanes below 32, a word each.
+    // Tokens past V load the row's last one and are struck out below.
+    struct Held {
+        float x[kPer];
+        uint32_t bits;
+    };
+    const uint32_t last = (uint32_t)(V - 1) * (uint32_t)kSize;
+    auto load = [&](int c, Held &h) {
+        const int t0 = begin + min(c, n_chunks - 1) * kChunk;
+        const uint32_t at = (uint32_t)(t0 + lane) * (uint32_t)kSize;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            h.x[i] = load_logit<kDtype>(lrow + min(at + (uint32_t)(64 * kSize) * i, last), 0);
+        if (mask)
+            h.bits = mask[min((t0 >> 5) + (lane & 31), mask_words - 1)];
+    };
+    Held ha, hb;
+    ha.bits = hb.bits = 0u;
+    if (n_chunks > 0)
+        load(0, ha);                          // on its way while the slice is counted
 
     if (a.has_penalty || a.has_bias)
-        prepare_slice(a, req, t0, base, S, cnt, bias);
-    const int chunk0 = base + wave * kChunk;
-    if (chunk0 >= V)
+        prepare_slice(a, req, base, S, words, entries);
+    if (t >= a.T || t >= (int)(blockIdx.z + 1) * a.row_group)
         return;                               // no barrier follows
-    const int chunk = chunk0 / kChunk;
-    uint32_t *my_cnt = cnt + wave * kChunk;
-    const float *my_bias = bias + wave * kChunk;
+
     const float rep = a.r.repetition ? a.r.repetition[req] : 1.0f;
     const float freq = a.r.frequency ? a.r.frequency[req] : 0.0f;
     const float pres = a.r.presence ? a.r.presence[req] : 0.0f;
-    constexpr size_t kSize = kDtype == INT4VH_ROWS_F32 ? 4 : 2;
+    const float *bias = a.has_bias ? a.r.bias_values + clamp64(a.r.bias_offsets[req], 0, a.r.n_bias) : nullptr;
+    // lane j holds draft j, for the rows behind it; the row's own draft
+    int mine = -1, d = -1;
+    if (a.T > 1) {
+        const int32_t *dr = a.draft + (size_t)req * (a.T - 1);
+        mine = lane < t ? dr[lane] : -1;
+        d = t < a.T - 1 ? dr[t] : -1;
+    }
 
-    for (int t = t0; t < t1; ++t) {
-        const int row = req * a.T + t;
-        const char *lrow = static_cast<const char *>(a.logits) + (size_t)row * a.logits_stride * kSize;
-        const uint32_t *mask = nullptr;
-        bool none = false;                    // nothing is allowed
-        if (a.r.mask) {
-            const long long mi = a.r.mask_index ? a.r.mask_index[row] : row;
-            none = mi >= a.r.n_masks;
-            if (mi >= 0 && !none)
-                mask = a.r.mask + (size_t)mi * a.r.mask_stride;
-        }
-        const int d = t < a.T - 1 ? a.draft[(size_t)req * (a.T - 1) + t] : -1;
+    int n = 0;                                // keys in buf
+    float above = kNegInf;                    // once k keys are held: a value has to be at least this
+    float bv = kNegInf;                       // this lane's largest value, and its lowest token
+    int bt = -1;
+    float lm = kNegInf, ls = 0.0f;            // this lane's (max, sum)
 
-        float x[kPer / 4][4];
+    auto process = [&](int c, Held &held) {
+        float (&x)[kPer] = held.x;
+        const int chunk0 = begin + c * kChunk;
+        const int at0 = chunk0 - base + lane;
+        if (a.has_penalty || a.has_bias) {
+            uint32_t w[kPer], any = 0u;
 #pragma unroll
-        for (int i = 0; i < kPer / 4; ++i)
-            load4<kDtype>(lrow, chunk0 + 256 * i + 4 * lane, V, x[i]);
-#pragma unroll
-        for (int i = 0; i < kPer / 4; ++i) {
-            const int at = 256 * i + 4 * lane, token = chunk0 + at;
+            for (int i = 0; i < kPer; ++i)
+                w[i] = words[at0 + 64 * i];
             if (a.has_penalty) {
-                const uint4 c = *reinterpret_cast<const uint4 *>(my_cnt + at);
-                const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-                if ((c.x | c.y | c.z | c.w) != 0u) {
+                // the drafts in front of this row that lie in the chunk
+                for (u64 m = __ballot(mine >= 0 && (uint32_t)(mine - chunk0) < (uint32_t)kChunk); m; m &= m - 1) {
+                    const int at = __builtin_amdgcn_readlane(mine, __builtin_ctzll(m)) - chunk0 - lane;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (w[j])
-                            x[i][j] = penalise(x[i][j], w[j], rep, freq, pres);
+                    for (int i = 0; i < kPer; ++i)
+                        w[i] += at == 64 * i ? 1u : 0u;
                 }
+                const uint32_t known = a.word.count | a.word.seen;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    if (__ballot((w[i] & known) != 0u))
+                        x[i] = w[i] & known ? penalise(x[i], w[i] & a.word.count, rep, freq, pres) : x[i];
             }
             if (a.has_bias) {
-                const float4 b = *reinterpret_cast<const float4 *>(my_bias + at);
-                x[i][0] += b.x;
-                x[i][1] += b.y;
-                x[i][2] += b.z;
-                x[i][3] += b.w;
-            }
-            if (mask || none) {
-                const uint32_t bits = mask && token < V ? mask[token >> 5] >> (token & 31) : 0u;
+                if (a.has_penalty && !a.word.entry_shift)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    x[i][j] = (bits >> j) & 1u ? x[i][j] : kNegInf;
+                    for (int i = 0; i < kPer; ++i)
+                        w[i] = entries[at0 + 64 * i];
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    w[i] >>= a.word.entry_shift;
+                    any |= w[i];
+                }
+                if (__ballot(any != 0u))
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i)
+                        x[i] = w[i] ? x[i] + bias[w[i] - 1u] : x[i];
             }
         }
+        if (mask || none) {
+            const uint32_t bits = none ? 0u : held.bits;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const u64 allowed = (u64)__builtin_amdgcn_readlane(bits, 2 * i + 1) << 32 |
+                                    (uint32_t)__builtin_amdgcn_readlane(bits, 2 * i);
+                x[i] = (allowed >> lane) & 1ull ? x[i] : kNegInf;
+            }
+        }
+        if (chunk0 + kChunk > V)
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                x[i] = chunk0 + 64 * i + lane < V ? x[i] : kNegInf;
+
         if constexpr (!kVerify) {
             char *orow = static_cast<char *>(a.out) + (size_t)row * a.out_stride * kSize;
 #pragma unroll
-            for (int i = 0; i < kPer / 4; ++i)
-                store4<kDtype>(orow, chunk0 + 256 * i + 4 * lane, V, x[i]);
-        } else {
-            // tokens past V are -infinity here: biases do not reach them
-            float best = kNegInf;             // fmaxf passes over NaN
+            for (int i = 0; i < kPer; ++i)
+                if (chunk0 + 64 * i + lane < V)
+                    store_logit<kDtype>(orow, chunk0 + 64 * i + lane, x[i]);
+            return;
+        }
+        float best = kNegInf;                 // fmaxf passes over NaN
+        if constexpr (kTopK || kLse) {
 #pragma unroll
-            for (int i = 0; i < kPer / 4; ++i)
+            for (int i = 0; i < kPer; ++i)
+                best = fmaxf(best, x[i]);
+        }
+        if constexpr (kLse) {
+            const float m = fmaxf(lm, best);
+            ls *= exp2_below(lm, m, a.lse_scale);
+            lm = m;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    best = fmaxf(best, x[i][j]);
-            const size_t slot = (size_t)row * a.n_chunks + chunk;
-            if constexpr (kLse) {
-                const float m = wave_max(best);
-                float s = 0.0f;
-#pragma unroll
-                for (int i = 0; i < kPer / 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        s += exp2_below(x[i][j], m, a.lse_scale);
-                s = wave_sum(s);
-                if (lane == 0)
-                    a.sums[slot] = make_float2(m, m > kNegInf ? s : 0.0f);
-            }
-            if constexpr (kTopK) {
-                const int k = a.top_k;
+            for (int i = 0; i < kPer; ++i)
+                ls += exp2_below(x[i], m, a.lse_scale);
+            ls = m > kNegInf ? ls : 0.0f;
+        }
+        if constexpr (kTopK) {
+            // the values from `from` on are candidates: before k keys are held,
+            // those that reach the chunk's threshold
+            const int k = a.top_k;
+            float from = above;
+            if (n < k) {
                 const uint32_t th = reach_threshold(best > kNegInf ? order_word(best) : 0u, k);
-                int n = 0;
-#pragma unroll
-                for (int i = 0; i < kPer / 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const bool take = x[i][j] > kNegInf && order_word(x[i][j]) >= th;
-                        const u64 m = __ballot(take);
-                        if (m)
-                            push(buf, n, order_key(x[i][j], chunk0 + 256 * i + 4 * lane + j), m, k, lane);
-                    }
-                n = keep_best(buf, n, k, lane);
-                const u64 key = lane < n ? buf[lane] : 0ull;
-                if (lane < k)
-                    a.lists[slot * k + lane] = key;
-                if (lane == 0)
-                    a.heads[slot] = key;
-            } else {
-                u64 key = 0ull;
-#pragma unroll
-                for (int i = 0; i < kPer / 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const u64 o = x[i][j] > kNegInf ? order_key(x[i][j], chunk0 + 256 * i + 4 * lane + j) : 0ull;
-                        key = o > key ? o : key;
-                    }
-                key = wave_max64(key);
-                if (lane == 0)
-                    a.heads[slot] = key;
+                from = th > 1u ? word_value(th) : -3.402823466e38f;
             }
-            const uint32_t da = (uint32_t)d - (uint32_t)chunk0;
-            if (d >= 0 && d < V && da < (uint32_t)kChunk && (int)((da >> 2) & 63u) == lane) {
-                float v = kNegInf;
+            if (__ballot(best >= from)) {
+                u64 m[kPer];
+                int count = 0;
 #pragma unroll
-                for (int i = 0; i < kPer / 4; ++i)
+                for (int i = 0; i < kPer; ++i) {
+                    m[i] = __ballot(x[i] >= from);
+                    count += __popcll(m[i]);
+                }
+                if (n + count <= kBuf) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        v = (int)(da >> 8) == i && (int)(da & 3u) == j ? x[i][j] : v;
-                a.draft_logit[row] = v;
+                    for (int i = 0; i < kPer; ++i)
+                        if (m[i]) {
+                            if (x[i] >= from)
+                                buf[n + lane_rank(m[i])] = order_key(x[i], chunk0 + 64 * i + lane);
+                            n += __popcll(m[i]);
+                        }
+                    wave_fence();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i)
+                        if (m[i])
+                            push(buf, n, order_key(x[i], chunk0 + 64 * i + lane), m[i], k, lane);
+                }
+                if (above == kNegInf || n > 48) {
+                    n = keep_best(buf, n, k, lane);
+                    // later tokens lose a tie: the next larger value
+                    if (n == k)
+                        above = word_value((uint32_t)(buf[k - 1] >> 32) + 1u);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const bool more = x[i] > bv;
+                bv = more ? x[i] : bv;
+                bt = more ? chunk0 + 64 * i + lane : bt;
             }
         }
-        // the rows behind this one count its draft: this wave's own words
-        if (a.has_penalty && t + 1 < t1) {
-            const uint32_t da = (uint32_t)d - (uint32_t)chunk0;
-            if (d >= 0 && da < (uint32_t)kChunk && lane == 0)
-                my_cnt[da] += 1u;
-            wave_fence();
+        const uint32_t da = (uint32_t)d - (uint32_t)chunk0;
+        if (d >= 0 && d < V && da < (uint32_t)kChunk) {
+            float v = kNegInf;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                v = (int)(da >> 6) == i ? x[i] : v;
+            if ((int)(da & 63u) == lane)
+                a.draft_logit[row] = v;
+        }
+    };
+    for (int c = 0; c < n_chunks; c += 2) {
+        load(c + 1, hb);
+        process(c, ha);
+        if (c + 1 < n_chunks) {
+            load(c + 2, ha);
+            process(c + 1, hb);
+        }
+    }
+
+    if constexpr (kVerify) {
+        const size_t slot = (size_t)row * a.n_lists + blockIdx.x * a.ways + way;
+        if constexpr (kLse) {
+            const float m = wave_max(lm);
+            const float s = wave_sum(ls * exp2_below(lm, m, a.lse_scale));
+            if (lane == 0)
+                a.sums[slot] = make_float2(m, m > kNegInf ? s : 0.0f);
+        }
+        if constexpr (kTopK) {
+            const int k = a.top_k;
+            if (n > k)
+                n = keep_best(buf, n, k, lane);
+            const u64 key = lane < n ? buf[lane] : 0ull;
+            if (lane < k)
+                a.lists[slot * k + lane] = key;
+            if (lane == 0)
+                a.heads[slot] = key;
+        } else {
+            const u64 key = wave_max64(bt >= 0 ? order_key(bv, bt) : 0ull);
+            if (lane == 0)
+                a.heads[slot] = key;
         }
     }
 }
@@ -490,7 +587,7 @@ struct MergeArgs {
     const float *draft_logit;
     const int32_t *draft;
     const float *draft_probs, *uniforms;   // both or neither
-    int R, T, V, top_k, n_chunks;
+    int R, T, V, top_k, n_lists;
     float temperature, lse_scale;
     float *logits_max;
     int32_t *argmax, *topk_ids;
@@ -498,28 +595,35 @@ struct MergeArgs {
     int32_t *n_acc;
 };
 
-// One workgroup per request, one wave per row: the row's chunks joined, then
+// One workgroup per request, one wave per row: the row's lists joined, then
 // the request's accepted count.
 template <bool kTopK, bool kLse>
 __global__ void __launch_bounds__(64 * 16) rules_merge_kernel(MergeArgs a)
 {
     __shared__ u64 s_buf[16][kBuf];
+    __shared__ int s_open[16][64];
     __shared__ int s_ok[16];
     const int lane = threadIdx.x & 63, t = threadIdx.x >> 6, req = blockIdx.x;
     const int row = req * a.T + t;
-    const int n_chunks = a.n_chunks;
-    const u64 *heads = a.heads + (size_t)row * n_chunks;
+    const int n_lists = a.n_lists;
+    const u64 *heads = a.heads + (size_t)row * n_lists;
     const bool drafted = t < a.T - 1;
     const size_t di = drafted ? (size_t)req * (a.T - 1) + t : 0;
     const int d = drafted ? a.draft[di] : -1;
+    const float bar = drafted && a.draft_probs ? a.uniforms[di] * a.draft_probs[di] : 0.0f;
 
+    u64 best = 0ull;                          // of this lane's lists
+    for (int c = lane; c < n_lists; c += 64) {
+        const u64 h = heads[c];
+        best = h > best ? h : best;
+    }
     float gm = kNegInf, gs = 0.0f;
     if constexpr (kLse) {
-        const float2 *sums = a.sums + (size_t)row * n_chunks;
-        for (int c = lane; c < n_chunks; c += 64)
+        const float2 *sums = a.sums + (size_t)row * n_lists;
+        for (int c = lane; c < n_lists; c += 64)
             gm = fmaxf(gm, sums[c].x);
         gm = wave_max(gm);
-        for (int c = lane; c < n_chunks; c += 64) {
+        for (int c = lane; c < n_lists; c += 64) {
             const float2 p = sums[c];
             gs += p.y * exp2_below(p.x, gm, a.lse_scale);
         }
@@ -528,33 +632,42 @@ __global__ void __launch_bounds__(64 * 16) rules_merge_kernel(MergeArgs a)
             a.lse[row] = gs > 0.0f ? gm / a.temperature + logf(gs) : kNegInf;
     }
 
-    u64 best = 0ull;                          // of this lane's chunks
-    for (int c = lane; c < n_chunks; c += 64) {
-        const u64 h = heads[c];
-        best = h > best ? h : best;
-    }
     float p = 0.0f;
     u64 top;                                  // the row's best key
     if constexpr (kTopK) {
         volatile u64 *buf = s_buf[t];
+        volatile int *open = s_open[t];
         const int k = a.top_k;
         const uint32_t th = reach_threshold((uint32_t)(best >> 32), k);
         int n = 0;
-        for (int c0 = 0; c0 < n_chunks; c0 += 64) {
+        for (int c0 = 0; c0 < n_lists; c0 += 64) {
+            // the lists whose best key reaches the threshold, then all their
+            // keys at once
             const int c = c0 + lane;
-            const u64 h = c < n_chunks ? heads[c] : 0ull;
-            // the lists whose best key reaches the threshold, a lane each
-            const bool open = h != 0ull && (uint32_t)(h >> 32) >= th;
-            if (!__ballot(open))
-                continue;
-            const u64 *list = a.lists + ((size_t)row * n_chunks + (open ? c : 0)) * k;
-            for (int j = 0; j < k; ++j) {
-                const u64 key = open ? list[j] : 0ull;
-                const u64 m = __ballot(key != 0ull && (uint32_t)(key >> 32) >= th);
-                if (!m)
-                    break;                    // lists are best first
-                push(buf, n, key, m, k, lane);
+            const u64 h = c < n_lists ? heads[c] : 0ull;
+            const bool reach = h != 0ull && (uint32_t)(h >> 32) >= th;
+            const u64 m = __ballot(reach);
+            if (reach)
+                open[lane_rank(m)] = c;
+            wave_fence();
+            // 16 lanes a list
+            const int n_open = __popcll(m), rank = lane & 15;
+            constexpr int kFly = 4;
+            for (int i0 = 0; i0 < n_open; i0 += 4 * kFly) {
+                u64 key[kFly];
+#pragma unroll
+                for (int u = 0; u < kFly; ++u) {
+                    const int i = i0 + 4 * u + (lane >> 4);
+                    key[u] = i < n_open && rank < k ? a.lists[((size_t)row * n_lists + open[i]) * k + rank] : 0ull;
+                }
+#pragma unroll
+                for (int u = 0; u < kFly; ++u) {
+                    const u64 take = __ballot(key[u] != 0ull && (uint32_t)(key[u] >> 32) >= th);
+                    if (take)
+                        push(buf, n, key[u], take, k, lane);
+                }
             }
+            wave_fence();
         }
         n = keep_best(buf, n, k, lane);
         const u64 key = lane < n ? buf[lane] : 0ull;
@@ -584,7 +697,7 @@ __global__ void __launch_bounds__(64 * 16) rules_merge_kernel(MergeArgs a)
         if (drafted) {
             if (a.draft_probs) {
                 a.p_draft[di] = p;
-                ok = a.uniforms[di] * a.draft_probs[di] < p;
+                ok = bar < p;
             } else {
                 ok = id >= 0 && id == d;
             }
@@ -604,7 +717,6 @@ __global__ void __launch_bounds__(64 * 16) rules_merge_kernel(MergeArgs a)
 
 struct Layout {
     size_t heads, lists, sums, draft_logit, bytes;
-    int n_chunks;
 };
 
 size_t round256(size_t n)
@@ -615,12 +727,13 @@ size_t round256(size_t n)
 Layout layout_for(int R, int T, int V, int top_k)
 {
     Layout l;
-    const size_t M = (size_t)R * T;
-    l.n_chunks = (V + kChunk - 1) / kChunk;
+    // a list covers kChunk tokens at least, but for those past the vocabulary's
+    // end in the last slice
+    const size_t M = (size_t)R * T, n = (V + kChunk - 1) / kChunk + kMaxWaves;
     l.heads = 0;
-    l.lists = round256(M * l.n_chunks * 8);
-    l.sums = l.lists + round256(M * l.n_chunks * 8 * top_k);
-    l.draft_logit = l.sums + round256(M * l.n_chunks * 8);
+    l.lists = round256(M * n * 8);
+    l.sums = l.lists + round256(M * n * 8 * top_k);
+    l.draft_logit = l.sums + round256(M * n * 8);
     l.bytes = l.draft_logit + round256(M * 4);
     return l;
 }
@@ -667,6 +780,9 @@ void fill_rules(RulesArgs &a, const int4vh_logit_rules *r, int T)
     const bool any = a.r.repetition || a.r.frequency || a.r.presence;
     a.has_penalty = any && (a.r.history || T > 1);
     a.has_bias = a.r.bias_ids != nullptr;
+    // words are shared where both are there; alone, either has the plain ones
+    a.word = a.has_penalty && a.has_bias && a.r.n_history <= kSharedHistory && a.r.n_bias <= kSharedEntries ? kShared
+                                                                                                         : kApart;
 }
 
 struct Shape {
@@ -674,22 +790,31 @@ struct Shape {
     size_t lds;
 };
 
+// Slices as long as kMaxSlice spread the counting and a wave's threshold over
+// many tokens; shorter ones where there would be fewer than two workgroups a
+// compute unit.  A wave has kChunk tokens of a row at least.
 Shape shape_for(RulesArgs &a, bool topk, int cus)
 {
-    const int n_chunks = (a.V + kChunk - 1) / kChunk;
-    const int waves = n_chunks < kMaxWaves ? n_chunks : kMaxWaves;
-    const int slices = (n_chunks + waves - 1) / waves;
-    // rows of one workgroup share its counts; few requests: fewer rows each,
-    // so that two workgroups a compute unit are there
-    int groups = 1;
-    while (groups < a.T && (long long)slices * a.R * groups < 2ll * cus)
-        ++groups;
-    a.row_group = (a.T + groups - 1) / groups;
+    const int chunks = (a.V + kChunk - 1) / kChunk;
+    a.row_group = a.T < kMaxWaves ? a.T : kMaxWaves;
+    a.ways = kMaxWaves / a.row_group;
+    while (a.ways > chunks)
+        --a.ways;
+    const int groups = (a.T + a.row_group - 1) / a.row_group;
+    int per = kMaxWaves / a.ways;             // chunks per wave
+    while (per > 1 && (long long)((chunks + per * a.ways - 1) / (per * a.ways)) * a.R * groups < 2ll * cus)
+        per /= 2;
+    while (per > 1 && (per / 2) * a.ways >= chunks)
+        per /= 2;                             // no longer than the vocabulary
+    a.slice = per * a.ways * kChunk;
+    const int slices = (a.V + a.slice - 1) / a.slice;
+    a.n_lists = slices * a.ways;
+    const int waves = a.row_group * a.ways;
     Shape s;
-    s.grid = dim3(slices, a.R, (a.T + a.row_group - 1) / a.row_group);
+    s.grid = dim3(slices, a.R, groups);
     s.block = dim3(64 * waves);
-    s.lds = (size_t)waves * kChunk * 4 * ((a.has_penalty ? 1 : 0) + (a.has_bias ? 1 : 0)) +
-            (topk ? (size_t)waves * kBuf * 8 : 0);
+    const int arrays = a.word.entry_shift ? 1 : (a.has_penalty ? 1 : 0) + (a.has_bias ? 1 : 0);
+    s.lds = (size_t)a.slice * 4 * arrays + (topk ? (size_t)waves * kBuf * 8 : 0);
     return s;
 }
 
@@ -807,7 +932,6 @@ int logit_rules_verify(const void *logits, int64_t logits_stride, int dtype, con
     a.V = V;
     fill_rules(a, rules, T);
     a.top_k = top_k;
-    a.n_chunks = l.n_chunks;
     a.lse_scale = 1.4426950408889634f / temperature;
     a.heads = reinterpret_cast<u64 *>(ws + l.heads);
     a.lists = reinterpret_cast<u64 *>(ws + l.lists);
@@ -836,7 +960,7 @@ int logit_rules_verify(const void *logits, int64_t logits_stride, int dtype, con
     m.T = T;
     m.V = V;
     m.top_k = top_k;
-    m.n_chunks = l.n_chunks;
+    m.n_lists = a.n_lists;
     m.temperature = temperature;
     m.lse_scale = a.lse_scale;
     m.logits_max = logits_max;

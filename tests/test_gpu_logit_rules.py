@@ -142,6 +142,39 @@ def test_long_history(b):
         same(got, lr.ruled(logits, rules, drafts, R, T))
 
 
+@pytest.mark.parametrize("n,nb", [((1 << 20) + 5, 40), (300, 4000), (300, 2047), ((1 << 20) - 32, 2047)])
+def test_counts_and_entries_too_many_for_one_word(b, n, nb):
+    """On both sides of the lengths up to which a token's count and its bias
+    entry share a word; one token fills the history, and the last entry of an
+    id holds."""
+    R, T, V = 1, 3, 3000
+    g = np.random.default_rng(n + nb)
+    logits, rules, drafts = make(R, T, V, 1, history=0, bias=0, mask=None)
+    rules["history"] = np.full(n, 17, np.int32)
+    rules["history"][: n // 3] = g.integers(0, V, n // 3)
+    rules["history_offsets"] = np.array([0, n], np.int64)
+    rules["n_prompt"] = np.array([n // 5], np.int32)
+    rules["bias_ids"] = g.integers(0, V, nb).astype(np.int32)
+    rules["bias_values"] = g.normal(0, 4, nb).astype(np.float32)
+    rules["bias_offsets"] = np.array([0, nb], np.int64)
+    drafts[0, :] = 17
+    want = logits.copy()
+    made = np.bincount(rules["history"][n // 5:], minlength=V)
+    seen = np.bincount(rules["history"], minlength=V) > 0
+    last = dict(zip(rules["bias_ids"].tolist(), rules["bias_values"]))
+    rep, freq, pres = (rules[k][0] for k in ("repetition", "frequency", "presence"))
+    for t in range(T):
+        row, count = want[t], made.copy()
+        count[17] += t
+        row[seen] = np.where(row[seen] > 0, row[seen] / rep, row[seen] * rep)
+        m = count > 0
+        row[m] = row[m] - freq * count[m].astype(np.float32)
+        row[m] = row[m] - pres
+        for v, x in last.items():
+            row[v] = row[v] + np.float32(x)
+    same(b.apply_logit_rules(dev(logits), device_rules(b, rules), dev(drafts), R=R), want)
+
+
 def test_offsets_outside_are_clamped(b):
     logits, rules, drafts = make(2, 2, 500, 3)
     n, m = len(rules["history"]), len(rules["bias_ids"])
