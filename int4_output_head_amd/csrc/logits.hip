@@ -78,8 +78,8 @@ struct RulesArgs {
     // verify
     int top_k, n_lists;
     float lse_scale;           // log2(e) / temperature
-    u64 *heads;                // [R*T, n_lists] best key of each wave's tokens, 0 if none
-    u64 *lists;                // [R*T, n_lists, top_k] best keys, best first, 0 past the last
+    u64 *lists;                // [R*T, n_lists, max(top_k, 1)] best keys of each wave's tokens, best first, 0 past the last
+    u64 *heads;                // [R*T, n_lists] the lists' first keys (top_k >= 1)
     float2 *sums;              // [R*T, n_lists] (max, sum of exp2((x - max) * lse_scale))
     float *draft_logit;        // [R*T] ruled logit of the row's draft, where it is in [0, V)
 };
@@ -168,26 +168,28 @@ __device__ __forceinline__ int lane_rank(u64 m)
 // returns how many there are (min(n, k)).  A key's rank is the number of
 // larger ones, which pass by in scalar registers.  Called by a whole wave on
 // its own buffer.
-__device__ __forceinline__ int keep_best(volatile u64 *buf, int n, int k, int lane)
+__device__ __forceinline__ int keep_best(u64 *buf, int n, int k, int lane)
 {
     const u64 a = lane < n ? buf[lane] : 0ull;
     int ra = 0;
+    // four at a time: lanes past n hold key 0, which is larger than none
     if (n <= 64) {
-        for (int i = 0; i < n; ++i)
-            ra += readlane64(a, i) > a;
+#pragma nounroll
+        for (int i = 0; i < n; i += 4)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                ra += readlane64(a, i + j) > a;
     } else {
         const u64 b = lane + 64 < n ? buf[lane + 64] : 0ull;
         int rb = 0;
-        for (int i = 0; i < 64; ++i) {
-            const u64 o = readlane64(a, i);
-            ra += o > a;
-            rb += o > b;
-        }
-        for (int i = 0; i < n - 64; ++i) {
-            const u64 o = readlane64(b, i);
-            ra += o > a;
-            rb += o > b;
-        }
+#pragma nounroll
+        for (int i = 0; i < 64; i += 2)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const u64 o = readlane64(a, i + j), q = readlane64(b, i + j);
+                ra += (o > a) + (q > a);
+                rb += (o > b) + (q > b);
+            }
         if (lane + 64 < n && rb < k)
             buf[rb] = b;
     }
@@ -200,7 +202,7 @@ __device__ __forceinline__ int keep_best(volatile u64 *buf, int n, int k, int la
 
 // Appends the keys of the lanes in `mask`; a buffer that could overflow is
 // first cut to its k best.  Wave-uniform control flow.
-__device__ __forceinline__ void push(volatile u64 *buf, int &n, u64 key, u64 mask, int k, int lane)
+__device__ __forceinline__ void push(u64 *buf, int &n, u64 key, u64 mask, int k, int lane)
 {
     if (n + __popcll(mask) > kBuf) {
         n = keep_best(buf, n, k, lane);
@@ -215,22 +217,65 @@ __device__ __forceinline__ void push(volatile u64 *buf, int &n, u64 key, u64 mas
     n += __popcll(mask);
 }
 
+// Appends those of every lane's kN keys whose value reaches the word th (above
+// 0): a lane's place is the sum of the lower lanes' numbers, taken bit by bit.
+template <int kN>
+__device__ __forceinline__ void push_some(u64 *buf, int &n, const u64 (&key)[kN], uint32_t th, int k,
+                                          int lane)
+{
+    uint32_t mine = 0u;
+#pragma unroll
+    for (int u = 0; u < kN; ++u)
+        mine += (uint32_t)(key[u] >> 32) >= th ? 1u : 0u;
+    int at = n, all = n;
+#pragma unroll
+    for (int b = 0; (1 << b) <= kN; ++b) {
+        const u64 m = __ballot((mine >> b & 1u) != 0u);
+        at += lane_rank(m) << b;
+        all += __popcll(m) << b;
+    }
+    if (all <= kBuf) {
+#pragma unroll
+        for (int u = 0; u < kN; ++u)
+            if ((uint32_t)(key[u] >> 32) >= th)
+                buf[at++] = key[u];
+        n = all;
+        wave_fence();
+    } else {
+        // one at a time, in one copy of the code: the keys move down
+        u64 rest[kN];
+#pragma unroll
+        for (int u = 0; u < kN; ++u)
+            rest[u] = key[u];
+#pragma nounroll
+        for (int i = 0; i < kN; ++i) {
+            push(buf, n, rest[0], __ballot((uint32_t)(rest[0] >> 32) >= th), k, lane);
+#pragma unroll
+            for (int u = 0; u + 1 < kN; ++u)
+                rest[u] = rest[u + 1];
+        }
+    }
+}
+
 // A word th (at least 1) that at least k lanes' words reach, and where it can
 // be no more than k + 8; 1 where fewer than k lanes have a word, since then
-// lower values of the same lanes are wanted too.  Bits are set from the top
-// while enough lanes still reach the word.
+// lower values of the same lanes are wanted too.  Two bits at a time are set
+// from the top while enough lanes still reach the word.
 __device__ __forceinline__ uint32_t reach_threshold(uint32_t word, int k)
 {
     uint32_t th = 0u;
     if (__popcll(__ballot(word != 0u)) < k)
         return 1u;
-    for (uint32_t bit = 0x80000000u; bit; bit >>= 1) {
-        const int c = __popcll(__ballot(word >= (th | bit)));
-        if (c >= k) {
-            th |= bit;
-            if (c <= k + 8)
-                break;
-        }
+#pragma nounroll
+    for (int shift = 30; shift >= 0; shift -= 2) {
+        const int c1 = __popcll(__ballot(word >= (th | 1u << shift)));
+        const int c2 = __popcll(__ballot(word >= (th | 2u << shift)));
+        const int c3 = __popcll(__ballot(word >= (th | 3u << shift)));
+        const uint32_t bits = c3 >= k ? 3u : c2 >= k ? 2u : c1 >= k ? 1u : 0u;
+        const int c = c3 >= k ? c3 : c2 >= k ? c2 : c1;
+        th |= bits << shift;
+        if (bits && c <= k + 8)
+            break;
     }
     return th ? th : 1u;
 }
@@ -350,7 +395,7 @@ __global__ void __launch_bounds__(64 * kMaxWaves) rules_kernel(RulesArgs a)
     const int S = a.slice, V = a.V;
     uint32_t *words = s_mem;
     uint32_t *entries = s_mem + (a.has_penalty && a.has_bias && !a.word.entry_shift ? S : 0);
-    volatile u64 *buf = reinterpret_cast<u64 *>(entries + (a.has_penalty || a.has_bias ? S : 0)) + wave * kBuf;
+    u64 *buf = reinterpret_cast<u64 *>(entries + (a.has_penalty || a.has_bias ? S : 0)) + wave * kBuf;
     const int base = blockIdx.x * S;
     const int req = blockIdx.y;
     const int t = blockIdx.z * a.row_group + wave / a.ways, way = wave % a.ways;
@@ -517,10 +562,18 @@ __global__ void __launch_bounds__(64 * kMaxWaves) rules_kernel(RulesArgs a)
                         }
                     wave_fence();
                 } else {
+                    // one at a time, in one copy of the code: the values move down
+                    float rest[kPer];
 #pragma unroll
                     for (int i = 0; i < kPer; ++i)
-                        if (m[i])
-                            push(buf, n, order_key(x[i], chunk0 + 64 * i + lane), m[i], k, lane);
+                        rest[i] = x[i];
+#pragma nounroll
+                    for (int i = 0; i < kPer; ++i) {
+                        push(buf, n, order_key(rest[0], chunk0 + 64 * i + lane), __ballot(rest[0] >= from), k, lane);
+#pragma unroll
+                        for (int j = 0; j + 1 < kPer; ++j)
+                            rest[j] = rest[j + 1];
+                    }
                 }
                 if (above == kNegInf || n > 48) {
                     n = keep_best(buf, n, k, lane);
@@ -576,13 +629,13 @@ __global__ void __launch_bounds__(64 * kMaxWaves) rules_kernel(RulesArgs a)
         } else {
             const u64 key = wave_max64(bt >= 0 ? order_key(bv, bt) : 0ull);
             if (lane == 0)
-                a.heads[slot] = key;
+                a.lists[slot] = key;
         }
     }
 }
 
 struct MergeArgs {
-    const u64 *heads, *lists;
+    const u64 *lists, *heads;
     const float2 *sums;
     const float *draft_logit;
     const int32_t *draft;
@@ -596,27 +649,47 @@ struct MergeArgs {
 };
 
 // One workgroup per request, one wave per row: the row's lists joined, then
-// the request's accepted count.
-template <bool kTopK, bool kLse>
+// the request's accepted count.  A few hundred or thousand keys a row, from
+// other XCDs' caches: latency counts.  Up to 64 lists are loaded at once, 16
+// lanes a list, and their first keys meet in LDS for the threshold.  Of more
+// lists (a short call's rows are cut into many) the first keys alone come
+// first, and then the lists that reach the threshold: one compute unit would
+// take longer for all of them (149 lists of 16 rows: 14.4 us, so 8.5).
+constexpr int kHeads = 4;                     // first keys per lane at a time
+
+// kMany: a top-k call of more than 64 lists a row.
+template <bool kTopK, bool kLse, bool kMany>
 __global__ void __launch_bounds__(64 * 16) rules_merge_kernel(MergeArgs a)
 {
-    __shared__ u64 s_buf[16][kBuf];
-    __shared__ int s_open[16][64];
+    __shared__ u64 s_buf[kTopK ? 16 : 1][kBuf];
+    __shared__ uint32_t s_head[kTopK && !kMany ? 16 : 1][64];
+    __shared__ int s_open[kMany ? 16 : 1][64 * kHeads];
     __shared__ int s_ok[16];
     const int lane = threadIdx.x & 63, t = threadIdx.x >> 6, req = blockIdx.x;
     const int row = req * a.T + t;
     const int n_lists = a.n_lists;
-    const u64 *heads = a.heads + (size_t)row * n_lists;
     const bool drafted = t < a.T - 1;
     const size_t di = drafted ? (size_t)req * (a.T - 1) + t : 0;
     const int d = drafted ? a.draft[di] : -1;
     const float bar = drafted && a.draft_probs ? a.uniforms[di] * a.draft_probs[di] : 0.0f;
 
-    u64 best = 0ull;                          // of this lane's lists
-    for (int c = lane; c < n_lists; c += 64) {
-        const u64 h = heads[c];
-        best = h > best ? h : best;
-    }
+    const int k = kTopK ? a.top_k : 1;
+    const u64 *lists = a.lists + (size_t)row * n_lists * k;
+    constexpr int kKeys = kTopK ? kMaxTopK : 1;
+    u64 key[kKeys];                           // of the (i0 + 4u + lane / 16)-th of n lists; greedy: the lane-th
+    auto load_lists = [&](int i0, int n, const int *open) {
+        const int rank = kTopK ? lane & 15 : 0, first = kTopK ? lane >> 4 : lane;
+#pragma unroll
+        for (int u = 0; u < kKeys; ++u) {
+            const int i = min(i0 + 4 * u + first, n - 1);
+            key[u] = lists[(uint32_t)((open ? open[i] : i) * k + min(rank, k - 1))];
+        }
+#pragma unroll
+        for (int u = 0; u < kKeys; ++u)
+            key[u] = i0 + 4 * u + first < n && rank < k ? key[u] : 0ull;
+    };
+    if constexpr (!kMany)
+        load_lists(0, n_lists, nullptr);
     float gm = kNegInf, gs = 0.0f;
     if constexpr (kLse) {
         const float2 *sums = a.sums + (size_t)row * n_lists;
@@ -635,56 +708,76 @@ __global__ void __launch_bounds__(64 * 16) rules_merge_kernel(MergeArgs a)
     float p = 0.0f;
     u64 top;                                  // the row's best key
     if constexpr (kTopK) {
-        volatile u64 *buf = s_buf[t];
-        volatile int *open = s_open[t];
-        const int k = a.top_k;
-        const uint32_t th = reach_threshold((uint32_t)(best >> 32), k);
+        u64 *buf = s_buf[t];
         int n = 0;
-        for (int c0 = 0; c0 < n_lists; c0 += 64) {
-            // the lists whose best key reaches the threshold, then all their
-            // keys at once
-            const int c = c0 + lane;
-            const u64 h = c < n_lists ? heads[c] : 0ull;
-            const bool reach = h != 0ull && (uint32_t)(h >> 32) >= th;
-            const u64 m = __ballot(reach);
-            if (reach)
-                open[lane_rank(m)] = c;
+        if constexpr (!kMany) {
+            if ((lane & 15) == 0)
+#pragma unroll
+                for (int u = 0; u < kKeys; ++u)
+                    s_head[t][4 * u + (lane >> 4)] = (uint32_t)(key[u] >> 32);
             wave_fence();
-            // 16 lanes a list
-            const int n_open = __popcll(m), rank = lane & 15;
-            constexpr int kFly = 4;
-            for (int i0 = 0; i0 < n_open; i0 += 4 * kFly) {
-                u64 key[kFly];
+            push_some(buf, n, key, reach_threshold(s_head[t][lane], k), k, lane);
+        } else {
+            int *open = s_open[t];
+            const u64 *heads = a.heads + (size_t)row * n_lists;
+            u64 h[kHeads], best = 0ull;
+            auto load_heads = [&](int c0) {
 #pragma unroll
-                for (int u = 0; u < kFly; ++u) {
-                    const int i = i0 + 4 * u + (lane >> 4);
-                    key[u] = i < n_open && rank < k ? a.lists[((size_t)row * n_lists + open[i]) * k + rank] : 0ull;
-                }
+                for (int u = 0; u < kHeads; ++u)
+                    h[u] = heads[min(c0 + 64 * u + lane, n_lists - 1)];
 #pragma unroll
-                for (int u = 0; u < kFly; ++u) {
-                    const u64 take = __ballot(key[u] != 0ull && (uint32_t)(key[u] >> 32) >= th);
-                    if (take)
-                        push(buf, n, key[u], take, k, lane);
-                }
+                for (int u = 0; u < kHeads; ++u)
+                    h[u] = c0 + 64 * u + lane < n_lists ? h[u] : 0ull;
+            };
+            for (int c0 = 0; c0 < n_lists; c0 += 64 * kHeads) {
+                load_heads(c0);
+#pragma unroll
+                for (int u = 0; u < kHeads; ++u)
+                    best = h[u] > best ? h[u] : best;
             }
-            wave_fence();
+            const uint32_t th = reach_threshold((uint32_t)(best >> 32), k);
+            for (int c0 = 0; c0 < n_lists; c0 += 64 * kHeads) {
+                if (n_lists > 64 * kHeads)
+                    load_heads(c0);
+                int n_open = 0;
+#pragma unroll
+                for (int u = 0; u < kHeads; ++u) {
+                    const bool reach = (uint32_t)(h[u] >> 32) >= th;
+                    const u64 m = __ballot(reach);
+                    if (reach)
+                        open[n_open + lane_rank(m)] = c0 + 64 * u + lane;
+                    n_open += __popcll(m);
+                }
+                wave_fence();
+                for (int i0 = 0; i0 < n_open; i0 += 64) {
+                    load_lists(i0, n_open, open);
+                    push_some(buf, n, key, th, k, lane);
+                }
+                wave_fence();
+            }
         }
         n = keep_best(buf, n, k, lane);
-        const u64 key = lane < n ? buf[lane] : 0ull;
-        top = n ? buf[0] : 0ull;
-        const float v = key ? key_value(key) : kNegInf;
-        const int id = key ? key_token(key) : -1;
+        const u64 mine = lane < n ? buf[lane] : 0ull;
+        top = readlane64(mine, 0);
+        const float v = mine ? key_value(mine) : kNegInf;
+        const int id = mine ? key_token(mine) : -1;
         if (lane < k) {
             a.topk_ids[(size_t)row * k + lane] = id;
             a.topk_logits[(size_t)row * k + lane] = v;
         }
         if (a.draft_probs && drafted) {
-            const float m = key_value(top);
-            const float e = key ? exp2_below(v, m, a.lse_scale) : 0.0f;
-            const float sum = wave_sum(e), e_d = wave_sum(key && id == d ? e : 0.0f);
-            p = n ? e_d / sum : 0.0f;
+            float e = mine ? exp2_below(v, key_value(top), a.lse_scale) : 0.0f, e_d = id == d ? e : 0.0f;
+#pragma unroll
+            for (int off = 8; off >= 1; off >>= 1) {          // the keys are in the first 16 lanes
+                e += __shfl_xor(e, off);
+                e_d += __shfl_xor(e_d, off);
+            }
+            p = n ? e_d / e : 0.0f;
         }
     } else {
+        u64 best = key[0];
+        for (int c = 64 + lane; c < n_lists; c += 64)
+            best = lists[c] > best ? lists[c] : best;
         top = wave_max64(best);
         if (kLse && a.draft_probs && drafted && d >= 0 && d < a.V && gs > 0.0f)
             p = exp2_below(a.draft_logit[row], gm, a.lse_scale) / gs;
@@ -705,18 +798,17 @@ __global__ void __launch_bounds__(64 * 16) rules_merge_kernel(MergeArgs a)
         s_ok[t] = ok;
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        int n = 0;
-        while (n < a.T - 1 && s_ok[n])
-            ++n;
-        a.n_acc[req] = n;
+    if (t == 0) {
+        const u64 accepted = __ballot(lane < a.T - 1 && s_ok[lane < 16 ? lane : 0]);
+        if (lane == 0)
+            a.n_acc[req] = __builtin_ctzll(~accepted);        // the leading ones
     }
 }
 
 // ---------------------------------------------------------------- host side
 
 struct Layout {
-    size_t heads, lists, sums, draft_logit, bytes;
+    size_t lists, heads, sums, draft_logit, bytes;
 };
 
 size_t round256(size_t n)
@@ -730,9 +822,9 @@ Layout layout_for(int R, int T, int V, int top_k)
     // a list covers kChunk tokens at least, but for those past the vocabulary's
     // end in the last slice
     const size_t M = (size_t)R * T, n = (V + kChunk - 1) / kChunk + kMaxWaves;
-    l.heads = 0;
-    l.lists = round256(M * n * 8);
-    l.sums = l.lists + round256(M * n * 8 * top_k);
+    l.lists = 0;
+    l.heads = round256(M * n * 8 * (top_k ? top_k : 1));
+    l.sums = l.heads + (top_k ? round256(M * n * 8) : 0);
     l.draft_logit = l.sums + round256(M * n * 8);
     l.bytes = l.draft_logit + round256(M * 4);
     return l;
@@ -933,8 +1025,8 @@ int logit_rules_verify(const void *logits, int64_t logits_stride, int dtype, con
     fill_rules(a, rules, T);
     a.top_k = top_k;
     a.lse_scale = 1.4426950408889634f / temperature;
-    a.heads = reinterpret_cast<u64 *>(ws + l.heads);
     a.lists = reinterpret_cast<u64 *>(ws + l.lists);
+    a.heads = reinterpret_cast<u64 *>(ws + l.heads);
     a.sums = reinterpret_cast<float2 *>(ws + l.sums);
     a.draft_logit = reinterpret_cast<float *>(ws + l.draft_logit);
     const Shape sh = shape_for(a, top_k > 0, cus);
@@ -949,8 +1041,8 @@ int logit_rules_verify(const void *logits, int64_t logits_stride, int dtype, con
         return hip_fail(e, "rules kernel launch");
 
     MergeArgs m;
-    m.heads = a.heads;
     m.lists = a.lists;
+    m.heads = a.heads;
     m.sums = a.sums;
     m.draft_logit = a.draft_logit;
     m.draft = draft_ids;
@@ -970,8 +1062,10 @@ int logit_rules_verify(const void *logits, int64_t logits_stride, int dtype, con
     m.lse = lse;
     m.p_draft = p_draft;
     m.n_acc = n_accepted;
-    void (*k)(MergeArgs) = top_k ? (want_lse ? rules_merge_kernel<true, true> : rules_merge_kernel<true, false>)
-                                 : (want_lse ? rules_merge_kernel<false, true> : rules_merge_kernel<false, false>);
+    const bool many = a.n_lists > 64;
+    void (*k)(MergeArgs) = !top_k ? (want_lse ? rules_merge_kernel<false, true, false> : rules_merge_kernel<false, false, false>)
+                           : many ? (want_lse ? rules_merge_kernel<true, true, true> : rules_merge_kernel<true, false, true>)
+                                  : (want_lse ? rules_merge_kernel<true, true, false> : rules_merge_kernel<true, false, false>);
     hipLaunchKernelGGL(k, dim3(R), dim3(64 * T), 0, s, m);
     e = hipGetLastError();
     return e == hipSuccess ? INT4VH_OK : hip_fail(e, "rules merge kernel launch");
