@@ -321,20 +321,18 @@ __device__ __forceinline__ void prepare_slice(const RulesArgs &a, int req, int b
         bb = clamp64(a.r.bias_offsets[req], 0, a.r.n_bias);
         be = clamp64(a.r.bias_offsets[req + 1], 0, a.r.n_bias);
     }
-    constexpr int kFly = 4;                   // loads of four tokens in flight per thread
+    // Four tokens a load, kFly loads in flight per thread; loads past the end
+    // take the last four tokens instead, whose earlier ones are not theirs.
+    constexpr int kFly = 4;
+    const bool few = he - hb < 4;
     Words4 v[kFly];
     auto load = [&](long long i0) {
+        if (few)
+            return;
 #pragma unroll
         for (int u = 0; u < kFly; ++u) {
             const long long i = i0 + 4ll * u * nt;
-            v[u] = Words4{{~0u, ~0u, ~0u, ~0u}};
-            if (i + 4 <= he) {
-                v[u] = *reinterpret_cast<const Words4 *>(a.r.history + i);
-            } else {
-                for (int j = 0; j < 3; ++j)
-                    if (i + j < he)
-                        v[u].w[j] = (uint32_t)a.r.history[i + j];
-            }
+            v[u] = *reinterpret_cast<const Words4 *>(a.r.history + (i < he - 4 ? i : he - 4));
         }
     };
     load(hb + 4 * tid);
@@ -357,22 +355,31 @@ __device__ __forceinline__ void prepare_slice(const RulesArgs &a, int req, int b
         if (entries == words)
             __syncthreads();                  // the maxima are taken before anything is added to them
     }
-    for (long long i0 = hb + 4 * tid; i0 < he; i0 += 4ll * nt * kFly) {
-        if (i0 != hb + 4 * tid)
-            load(i0);
+    auto count = [&](int32_t token, bool prompt) {
+        const uint32_t at = (uint32_t)token - (uint32_t)base;
+        if (token >= 0 && at < (uint32_t)S) {
+            if (prompt)
+                atomicOr(&words[at], a.word.seen);
+            else
+                atomicAdd(&words[at], 1u);
+        }
+    };
+    if (few) {
+        if (hb + tid < he)
+            count(a.r.history[hb + tid], hb + tid < made);
+    } else {
+        for (long long i0 = hb + 4 * tid; i0 < he; i0 += 4ll * nt * kFly) {
+            if (i0 != hb + 4 * tid)
+                load(i0);
 #pragma unroll
-        for (int u = 0; u < kFly; ++u)
+            for (int u = 0; u < kFly; ++u) {
+                const long long i = i0 + 4ll * u * nt, from = i < he - 4 ? i : he - 4;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int32_t token = (int32_t)v[u].w[j];
-                const uint32_t at = (uint32_t)token - (uint32_t)base;
-                if (token >= 0 && at < (uint32_t)S) {
-                    if (i0 + 4ll * u * nt + j < made)
-                        atomicOr(&words[at], a.word.seen);
-                    else
-                        atomicAdd(&words[at], 1u);
-                }
+                for (int j = 0; j < 4; ++j)
+                    if (from + j >= i)
+                        count((int32_t)v[u].w[j], from + j < made);
             }
+        }
     }
     __syncthreads();
 }
@@ -464,7 +471,7 @@ __global__ void __launch_bounds__(64 * kMaxWaves) rules_kernel(RulesArgs a)
         const int chunk0 = begin + c * kChunk;
         const int at0 = chunk0 - base + lane;
         if (a.has_penalty || a.has_bias) {
-            uint32_t w[kPer], any = 0u;
+            uint32_t w[kPer];
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
                 w[i] = words[at0 + 64 * i];
@@ -476,27 +483,28 @@ __global__ void __launch_bounds__(64 * kMaxWaves) rules_kernel(RulesArgs a)
                     for (int i = 0; i < kPer; ++i)
                         w[i] += at == 64 * i ? 1u : 0u;
                 }
-                const uint32_t known = a.word.count | a.word.seen;
-#pragma unroll
-                for (int i = 0; i < kPer; ++i)
-                    if (__ballot((w[i] & known) != 0u))
-                        x[i] = w[i] & known ? penalise(x[i], w[i] & a.word.count, rep, freq, pres) : x[i];
             }
-            if (a.has_bias) {
-                if (a.has_penalty && !a.word.entry_shift)
+            const uint32_t known = a.has_penalty ? a.word.count | a.word.seen : 0u;
+            const bool here = a.has_bias && entries == words;
 #pragma unroll
-                    for (int i = 0; i < kPer; ++i)
-                        w[i] = entries[at0 + 64 * i];
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    w[i] >>= a.word.entry_shift;
-                    any |= w[i];
+            for (int i = 0; i < kPer; ++i)
+                if (__ballot(w[i] != 0u)) {   // few groups of 64 tokens have any
+                    if (w[i] & known)
+                        x[i] = penalise(x[i], w[i] & a.word.count, rep, freq, pres);
+                    const uint32_t e = here ? w[i] >> a.word.entry_shift : 0u;
+                    if (e)
+                        x[i] = x[i] + bias[e - 1u];
                 }
-                if (__ballot(any != 0u))
+        }
+        if (a.has_bias && entries != words) {
+            uint32_t e[kPer];
 #pragma unroll
-                    for (int i = 0; i < kPer; ++i)
-                        x[i] = w[i] ? x[i] + bias[w[i] - 1u] : x[i];
-            }
+            for (int i = 0; i < kPer; ++i)
+                e[i] = entries[at0 + 64 * i];
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (e[i])
+                    x[i] = x[i] + bias[e[i] - 1u];
         }
         if (mask || none) {
             const uint32_t bits = none ? 0u : held.bits;
@@ -504,7 +512,7 @@ __global__ void __launch_bounds__(64 * kMaxWaves) rules_kernel(RulesArgs a)
             for (int i = 0; i < kPer; ++i) {
                 const u64 allowed = (u64)__builtin_amdgcn_readlane(bits, 2 * i + 1) << 32 |
                                     (uint32_t)__builtin_amdgcn_readlane(bits, 2 * i);
-                x[i] = (allowed >> lane) & 1ull ? x[i] : kNegInf;
+                x[i] = __builtin_amdgcn_inverse_ballot_w64(allowed) ? x[i] : kNegInf;
             }
         }
         if (chunk0 + kChunk > V)
