@@ -7,7 +7,6 @@ library has not been built the first call raises; there is no fallback.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import struct
@@ -644,6 +643,8 @@ def stream_read(buf, mode: int = 0, *, out=None, events=None):
 
 ROWS_F16, ROWS_BF16, ROWS_F32 = 0, 1, 2
 _ROW_DTYPES = {torch.float16: ROWS_F16, torch.bfloat16: ROWS_BF16, torch.float32: ROWS_F32}
+_raw_stream = torch._C._cuda_getCurrentRawStream     # by device index
+_current_device = torch._C._cuda_getDevice
 
 
 def _row_code(t, name):
@@ -653,56 +654,69 @@ def _row_code(t, name):
     return code
 
 
-def _raw_stream(dev):
-    return torch._C._cuda_getCurrentRawStream(dev.index)
+def _on(index, call, *args):
+    """A call that launches on the device of that index, made current for it."""
+    if index == _current_device():
+        return call(*args)
+    with torch.cuda.device(index):
+        return call(*args)
 
 
-_no_guard = contextlib.nullcontext()
-
-
-def _guard(dev):
-    """The tensors' device made current for a call that launches on it."""
-    return _no_guard if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-
-
-def _same_device(dev, **tensors):
+def _same_device(index, **tensors):
     for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, not on device {index}")
 
 
 def _rows2d(t, name):
-    """t as rows [M, H] with contiguous channels, and the rows' distance."""
-    if t.dim() != 2:
-        if t.dim() < 1 or not t.is_contiguous():
+    """Rows and channels of t [M, H], and the rows' distance in elements; other
+    numbers of dims must be contiguous and count as rows of their last."""
+    shape = t.shape
+    if len(shape) == 2:
+        M, H = shape
+        stride, inner = t.stride()
+        if H > 1 and inner != 1:
+            raise ValueError(f"{name} must have contiguous channels")
+        if M <= 1:
+            stride = H
+    else:
+        if not shape or not t.is_contiguous():
             raise ValueError(f"{name} must be [M, H], or contiguous with any leading dims")
-        t = t.reshape(-1, t.shape[-1])
-    M, H = t.shape
+        stride = H = shape[-1]
+        M = t.numel() // H if H else 0
     if M < 1 or H < 1:
         raise ValueError(f"{name} must not be empty")
-    if H > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must have contiguous channels")
-    stride = t.stride(0) if M > 1 else H
     if stride < H:
         raise ValueError(f"{name} must not have overlapping rows")
-    return t, stride
+    return M, H, stride
+
+
+def _vector(t, name, dtype, n):
+    """Checks a contiguous vector of n values."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
+        _check(t, name, dtype, 1)
+    if t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and hold {n} values")
 
 
 def _norm_args(x, weight, residual):
     dt = _row_code(x, "x")
     wdt = _row_code(weight, "weight")
-    x2, xs = _rows2d(x, "x")
-    M, H = x2.shape
-    if weight.dim() != 1 or weight.shape[0] != H or not weight.is_contiguous():
+    M, H, xs = _rows2d(x, "x")
+    if weight.shape != (H,) or not weight.is_contiguous():
         raise ValueError("weight must be contiguous [H]")
-    r2, rs, total = None, 0, None
-    if residual is not None:
-        if residual.dtype != x.dtype or residual.shape != x.shape:
-            raise ValueError("residual must have the type and shape of x")
-        r2, rs = _rows2d(residual, "residual")
-        total = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _same_device(x.device, weight=weight, residual=residual)
-    return dt, wdt, x2, xs, r2, rs, total, M, H
+    index = x.get_device()
+    if weight.get_device() != index:
+        _same_device(index, weight=weight)
+    if residual is None:
+        return dt, wdt, xs, None, 0, None, M, H, index
+    if residual.dtype != x.dtype or residual.shape != x.shape:
+        raise ValueError("residual must have the type and shape of x")
+    rs = _rows2d(residual, "residual")[2]
+    if residual.get_device() != index:
+        _same_device(index, residual=residual)
+    total = torch.empty_like(x, memory_format=torch.contiguous_format)
+    return dt, wdt, xs, residual.data_ptr(), rs, total, M, H, index
 
 
 def rms_norm(x, weight, residual=None, *, eps: float = 1e-6, out_dtype=torch.float16):
@@ -711,17 +725,14 @@ def rms_norm(x, weight, residual=None, *, eps: float = 1e-6, out_dtype=torch.flo
     the hidden states of the verify calls (out_dtype float16).  weight [H].
     Returns the normed rows, and with a residual also the sum x + residual in
     x's type: (normed, sum)."""
-    dt, wdt, x2, xs, r2, rs, total, M, H = _norm_args(x, weight, residual)
+    dt, wdt, xs, res, rs, total, M, H, index = _norm_args(x, weight, residual)
     odt = _ROW_DTYPES.get(out_dtype)
     if odt is None:
         raise TypeError("out_dtype must be float16, bfloat16 or float32")
-    dev = x.device
-    out = torch.empty(x.shape, dtype=out_dtype, device=dev)
-    with _guard(dev):
-        st = load_library().rms_norm_rows(x2.data_ptr(), xs, None if r2 is None else r2.data_ptr(), rs, dt,
-                                          weight.data_ptr(), wdt, M, H, eps,
-                                          None if total is None else total.data_ptr(), out.data_ptr(), odt,
-                                          _raw_stream(dev))
+    out = (torch.empty_like(x, memory_format=torch.contiguous_format) if odt == dt
+           else x.new_empty(x.shape, dtype=out_dtype))
+    st = _on(index, load_library().rms_norm_rows, x.data_ptr(), xs, res, rs, dt, weight.data_ptr(), wdt, M, H, eps,
+             None if total is None else total.data_ptr(), out.data_ptr(), odt, _raw_stream(index))
     if st != OK:
         _raise(st, "rms_norm_rows")
     return out if total is None else (out, total)
@@ -732,21 +743,17 @@ def rms_norm_int8(x, weight, residual=None, *, channel_scales=None, eps: float =
     channel_scales (float16 [H]), the per-channel scales of the packed int4
     weights, are folded in.  Returns (codes int8 [..., H], row_scales float32
     [M]), and with a residual also the sum: (codes, row_scales, sum)."""
-    dt, wdt, x2, xs, r2, rs, total, M, H = _norm_args(x, weight, residual)
-    dev = x.device
+    dt, wdt, xs, res, rs, total, M, H, index = _norm_args(x, weight, residual)
+    cs = None
     if channel_scales is not None:
-        _check(channel_scales, "channel_scales", torch.float16, 1)
-        if channel_scales.shape[0] != H:
-            raise ValueError("channel_scales must hold H values")
-        _same_device(dev, channel_scales=channel_scales)
-    codes = torch.empty(x.shape, dtype=torch.int8, device=dev)
-    row_scales = torch.empty(M, dtype=torch.float32, device=dev)
-    with _guard(dev):
-        st = load_library().rms_norm_rows_int8(x2.data_ptr(), xs, None if r2 is None else r2.data_ptr(), rs, dt,
-                                               weight.data_ptr(), wdt,
-                                               None if channel_scales is None else channel_scales.data_ptr(), M, H,
-                                               eps, None if total is None else total.data_ptr(), codes.data_ptr(),
-                                               row_scales.data_ptr(), _raw_stream(dev))
+        _vector(channel_scales, "channel_scales", torch.float16, H)
+        _same_device(index, channel_scales=channel_scales)
+        cs = channel_scales.data_ptr()
+    codes = x.new_empty(x.shape, dtype=torch.int8)
+    row_scales = x.new_empty(M, dtype=torch.float32)
+    st = _on(index, load_library().rms_norm_rows_int8, x.data_ptr(), xs, res, rs, dt, weight.data_ptr(), wdt, cs, M,
+             H, eps, None if total is None else total.data_ptr(), codes.data_ptr(), row_scales.data_ptr(),
+             _raw_stream(index))
     if st != OK:
         _raise(st, "rms_norm_rows_int8")
     return (codes, row_scales) if total is None else (codes, row_scales, total)
@@ -757,20 +764,17 @@ def quantize_rows(x, *, channel_scales=None):
     activations of a linear_int4 whose input is no norm).  Returns (codes int8
     [..., H], row_scales float32 [M])."""
     dt = _row_code(x, "x")
-    x2, xs = _rows2d(x, "x")
-    M, H = x2.shape
-    dev = x.device
+    M, H, xs = _rows2d(x, "x")
+    index = x.get_device()
+    cs = None
     if channel_scales is not None:
-        _check(channel_scales, "channel_scales", torch.float16, 1)
-        if channel_scales.shape[0] != H:
-            raise ValueError("channel_scales must hold H values")
-        _same_device(dev, channel_scales=channel_scales)
-    codes = torch.empty(x.shape, dtype=torch.int8, device=dev)
-    row_scales = torch.empty(M, dtype=torch.float32, device=dev)
-    with _guard(dev):
-        st = load_library().quantize_rows_int8(x2.data_ptr(), xs, dt,
-                                               None if channel_scales is None else channel_scales.data_ptr(), M, H,
-                                               codes.data_ptr(), row_scales.data_ptr(), _raw_stream(dev))
+        _vector(channel_scales, "channel_scales", torch.float16, H)
+        _same_device(index, channel_scales=channel_scales)
+        cs = channel_scales.data_ptr()
+    codes = x.new_empty(x.shape, dtype=torch.int8)
+    row_scales = x.new_empty(M, dtype=torch.float32)
+    st = _on(index, load_library().quantize_rows_int8, x.data_ptr(), xs, dt, cs, M, H, codes.data_ptr(),
+             row_scales.data_ptr(), _raw_stream(index))
     if st != OK:
         _raise(st, "quantize_rows_int8")
     return codes, row_scales
@@ -795,54 +799,54 @@ def linear_int4(codes, row_scales, packed_w, *, out_scales=None, bias=None, acti
     tensor to write, which may be residual itself.  Returns it."""
     if not isinstance(codes, torch.Tensor) or not codes.is_cuda or codes.dtype != torch.int8:
         raise TypeError("codes must be a CUDA (HIP) int8 tensor")
-    c2, cs = _rows2d(codes, "codes")
-    M, K = c2.shape
-    _check(row_scales, "row_scales", torch.float32, 1)
+    M, K, cs = _rows2d(codes, "codes")
     _check(packed_w, "packed_w", torch.uint8, 2)
     N = packed_w.shape[0]
-    if row_scales.shape[0] != M or packed_w.shape[1] * 2 != K:
-        raise ValueError("shape mismatch between codes, row_scales and packed_w")
+    if packed_w.shape[1] * 2 != K:
+        raise ValueError("shape mismatch between codes and packed_w")
+    _vector(row_scales, "row_scales", torch.float32, M)
     dt = _ROW_DTYPES.get(out_dtype)
     if dt is None:
         raise TypeError("out_dtype must be float16, bfloat16 or float32")
-    if activation not in _ACTIVATIONS:
+    act = _ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError("activation must be None, 'relu', 'gelu' or 'silu'")
-    dev = codes.device
     if out_scales is not None:
-        _check(out_scales, "out_scales", torch.float32, 1)
-        if out_scales.shape[0] != N:
-            raise ValueError("out_scales must hold N values")
+        _vector(out_scales, "out_scales", torch.float32, N)
     if bias is not None:
-        _check(bias, "bias", out_dtype, 1)
-        if bias.shape[0] != N:
-            raise ValueError("bias must hold N values")
+        _vector(bias, "bias", out_dtype, N)
+    index = codes.get_device()
     rs, os_ = 0, N
     shape = codes.shape[:-1] + (N,)
     if residual is not None:
         if _row_code(residual, "residual") != dt or residual.shape != shape:
             raise ValueError("residual must be [M, N] of out_dtype")
-        residual, rs = _rows2d(residual, "residual")
+        rs = _rows2d(residual, "residual")[2]
     if out is None:
-        res = out = torch.empty(shape, dtype=out_dtype, device=dev)
+        out = row_scales.new_empty(shape, dtype=out_dtype)
     else:
         if _row_code(out, "out") != dt or out.shape != shape:
             raise ValueError("out must be [M, N] of out_dtype")
-        res = out
-        out, os_ = _rows2d(out, "out")
-    _same_device(dev, row_scales=row_scales, packed_w=packed_w, out_scales=out_scales, bias=bias, residual=residual,
+        os_ = _rows2d(out, "out")[2]
+    _same_device(index, row_scales=row_scales, packed_w=packed_w, out_scales=out_scales, bias=bias, residual=residual,
                  out=out)
-    L = load_library()
-    with _guard(dev):
-        need = L.linear_int4_rows_workspace_bytes(M, N, K)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        st = L.linear_int4_rows(c2.data_ptr(), cs, row_scales.data_ptr(), packed_w.data_ptr(),
-                                None if out_scales is None else out_scales.data_ptr(),
-                                None if bias is None else bias.data_ptr(), _ACTIVATIONS[activation],
-                                None if residual is None else residual.data_ptr(), rs, M, N, K, out.data_ptr(), os_,
-                                dt, None if ws is None else ws.data_ptr(), need, _raw_stream(dev))
+    st = _on(index, _launch_linear, index, codes.data_ptr(), cs, row_scales, packed_w.data_ptr(), _at(out_scales),
+             _at(bias), act, _at(residual), rs, M, N, K, out.data_ptr(), os_, dt)
     if st != OK:
         _raise(st, "linear_int4_rows")
-    return res
+    return out
+
+
+def _launch_linear(index, codes, cs, row_scales, packed_w, out_scales, bias, act, residual, rs, M, N, K, out, os_, dt):
+    L = load_library()
+    need = L.linear_int4_rows_workspace_bytes(M, N, K)
+    ws = row_scales.new_empty(need, dtype=torch.uint8) if need else None
+    return L.linear_int4_rows(codes, cs, row_scales.data_ptr(), packed_w, out_scales, bias, act, residual, rs, M, N, K,
+                              out, os_, dt, _at(ws), need, _raw_stream(index))
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 # ---------------------------------------------------------------- rules on logits
@@ -865,70 +869,75 @@ class LogitRules:
 
     def __init__(self, *, history=None, history_offsets=None, n_prompt=None, repetition=None, frequency=None,
                  presence=None, bias_ids=None, bias_values=None, bias_offsets=None, mask=None, mask_index=None):
-        self.device = self.requests = None
+        self.device = self.requests = self.n_index = None
         self.tensors = (history, history_offsets, n_prompt, repetition, frequency, presence, bias_ids, bias_values,
                         bias_offsets, mask, mask_index)
-        for t, name, dt, extra in ((history, "history", torch.int32, None),
-                                   (history_offsets, "history_offsets", torch.int64, 1),
-                                   (n_prompt, "n_prompt", torch.int32, 0),
-                                   (repetition, "repetition", torch.float32, 0),
-                                   (frequency, "frequency", torch.float32, 0),
-                                   (presence, "presence", torch.float32, 0),
-                                   (bias_ids, "bias_ids", torch.int32, None),
-                                   (bias_values, "bias_values", torch.float32, None),
-                                   (bias_offsets, "bias_offsets", torch.int64, 1),
-                                   (mask_index, "mask_index", torch.int32, None)):
-            if t is None:
-                continue
-            _check(t, name, dt, 1)
-            self._place(t, name)
-            if extra is not None:
-                if self.requests is None:
-                    self.requests = t.shape[0] - extra
-                elif self.requests != t.shape[0] - extra:
-                    raise ValueError(f"{name} is for {t.shape[0] - extra} requests, not {self.requests}")
-        if (history is None) != (history_offsets is None):
-            raise ValueError("history and history_offsets go together")
-        if n_prompt is not None and history is None:
-            raise ValueError("n_prompt needs a history")
-        if not ((bias_ids is None) == (bias_values is None) == (bias_offsets is None)):
+        place = self._place
+        n_history = n_bias = 0
+        p_history = p_offsets = p_prompt = p_rep = p_freq = p_pres = p_ids = p_values = p_boffsets = 0
+        if history is not None:
+            if history_offsets is None:
+                raise ValueError("history and history_offsets go together")
+            p_history, n_history = place(history, "history", torch.int32), history.shape[0]
+            p_offsets = place(history_offsets, "history_offsets", torch.int64, 1)
+        elif history_offsets is not None or n_prompt is not None:
+            raise ValueError("history_offsets and n_prompt need a history")
+        if n_prompt is not None:
+            p_prompt = place(n_prompt, "n_prompt", torch.int32, 0)
+        if repetition is not None:
+            p_rep = place(repetition, "repetition", torch.float32, 0)
+        if frequency is not None:
+            p_freq = place(frequency, "frequency", torch.float32, 0)
+        if presence is not None:
+            p_pres = place(presence, "presence", torch.float32, 0)
+        if bias_ids is not None and bias_values is not None and bias_offsets is not None:
+            p_ids, n_bias = place(bias_ids, "bias_ids", torch.int32), bias_ids.shape[0]
+            p_values = place(bias_values, "bias_values", torch.float32)
+            p_boffsets = place(bias_offsets, "bias_offsets", torch.int64, 1)
+            if bias_values.shape[0] != n_bias:
+                raise ValueError("bias_ids and bias_values must have one length")
+        elif bias_ids is not None or bias_values is not None or bias_offsets is not None:
             raise ValueError("bias_ids, bias_values and bias_offsets go together")
-        if bias_ids is not None and bias_ids.shape != bias_values.shape:
-            raise ValueError("bias_ids and bias_values must have one length")
-        stride = 0
+        stride = p_mask = p_index = 0
         self.mask_rows = self.mask_words = 0
-        self.n_index = None
         if mask is not None:
             if not isinstance(mask, torch.Tensor) or not mask.is_cuda or mask.dtype != torch.int32 or mask.dim() != 2:
                 raise TypeError("mask must be a 2-D int32 CUDA (HIP) tensor")
-            self._place(mask, "mask")
-            self.mask_rows, self.mask_words = mask.shape
-            if self.mask_rows < 1 or (self.mask_words > 1 and mask.stride(1) != 1):
-                raise ValueError("mask must hold a row at least, with contiguous words")
-            stride = mask.stride(0) if self.mask_rows > 1 else self.mask_words
-            if stride < self.mask_words:
-                raise ValueError("mask must not have overlapping rows")
+            self.mask_rows, self.mask_words, stride = _rows2d(mask, "mask")
+            self._on(mask, "mask")
+            p_mask = mask.data_ptr()
             if mask_index is not None:
-                self.n_index = mask_index.shape[0]
+                p_index, self.n_index = place(mask_index, "mask_index", torch.int32), mask_index.shape[0]
         elif mask_index is not None:
             raise ValueError("mask_index needs a mask")
+        self.packed = _RULES.pack(p_history, n_history, p_offsets, p_prompt, p_rep, p_freq, p_pres, p_ids, p_values,
+                                  n_bias, p_boffsets, p_mask, self.mask_rows, stride, p_index)
 
-        def at(t):
-            return 0 if t is None else t.data_ptr()
-        self.packed = _RULES.pack(at(history), 0 if history is None else history.shape[0], at(history_offsets),
-                                  at(n_prompt), at(repetition), at(frequency), at(presence), at(bias_ids),
-                                  at(bias_values), 0 if bias_ids is None else bias_ids.shape[0], at(bias_offsets),
-                                  at(mask), self.mask_rows, stride, at(mask_index))
+    def _place(self, t, name, dtype, extra=None):
+        """Checks a contiguous vector, one value per request (and `extra`) where
+        that is given, and returns its address."""
+        if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda or t.dim() != 1 or not t.is_contiguous():
+            _check(t, name, dtype, 1)
+        self._on(t, name)
+        if extra is not None:
+            n = t.shape[0] - extra
+            if self.requests is None:
+                self.requests = n
+            elif self.requests != n:
+                raise ValueError(f"{name} is for {n} requests, not {self.requests}")
+        return t.data_ptr()
 
-    def _place(self, t, name):
+    def _on(self, t, name):
+        index = t.get_device()
         if self.device is None:
-            self.device = t.device
-        elif t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, not on {self.device}")
+            self.device = index
+        elif index != self.device:
+            raise ValueError(f"{name} is on device {index}, not on {self.device}")
 
-    def check(self, dev, R, T, V):
-        if self.device is not None and self.device != dev:
-            raise ValueError(f"the rules are on {self.device}, not on {dev}")
+    def check(self, index, R, T, V):
+        """Raises unless the rules fit a call of these sizes on that device."""
+        if self.device is not None and self.device != index:
+            raise ValueError(f"the rules are on device {self.device}, not on {index}")
         if self.requests is not None and self.requests != R:
             raise ValueError(f"the rules are for {self.requests} requests, not {R}")
         if self.mask_rows:
@@ -941,8 +950,8 @@ class LogitRules:
 
 
 def _logit_rows(logits, R):
-    """(rows [R*T, V], their distance, type code, R, T, V) of logits [R, T, V],
-    or [R*T, V] with R."""
+    """(type code, rows' distance, R, T, V) of logits [R, T, V], or [R*T, V]
+    with R."""
     code = _row_code(logits, "logits")
     if logits.dim() == 3:
         if R is not None and R != logits.shape[0]:
@@ -952,30 +961,35 @@ def _logit_rows(logits, R):
         raise ValueError("logits must be [R, T, V], or [R*T, V] with R")
     elif R is None:
         raise ValueError("R is required for 2-D logits")
-    rows, stride = _rows2d(logits, "logits")
-    M, V = rows.shape
+    M, V, stride = _rows2d(logits, "logits")
     if R < 1 or M % R:
         raise ValueError("the logits' rows must be R*T")
-    return rows, stride, code, R, M // R, V
+    return code, stride, R, M // R, V
 
 
-def _drafts(dev, R, T, draft_ids, draft_probs=None, uniforms=None):
+def _drafted(t, name, dtype, n, index):
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        _check(t, name, dtype)
+    if t.numel() != n:
+        raise ValueError(f"{name} must hold R*(T-1) values")
+    if t.get_device() != index:
+        _same_device(index, **{name: t})
+    return t.data_ptr()
+
+
+def _drafts(index, R, T, draft_ids, draft_probs=None, uniforms=None):
     if T == 1:
         return None, None, None
     if draft_ids is None:
         raise ValueError("draft_ids is required when T > 1")
-    if (draft_probs is None) != (uniforms is None):
+    n = R * (T - 1)
+    ids = _drafted(draft_ids, "draft_ids", torch.int32, n, index)
+    if draft_probs is None and uniforms is None:
+        return ids, None, None
+    if draft_probs is None or uniforms is None:
         raise ValueError("draft_probs and uniforms go together")
-    for t, n, dt in ((draft_ids, "draft_ids", torch.int32), (draft_probs, "draft_probs", torch.float32),
-                     (uniforms, "uniforms", torch.float32)):
-        if t is not None:
-            _check(t, n, dt)
-            if t.numel() != R * (T - 1):
-                raise ValueError(f"{n} must hold R*(T-1) values")
-            if t.device != dev:
-                raise ValueError(f"{n} is on {t.device}, not on {dev}")
-    return (draft_ids.data_ptr(), None if draft_probs is None else draft_probs.data_ptr(),
-            None if uniforms is None else uniforms.data_ptr())
+    return (ids, _drafted(draft_probs, "draft_probs", torch.float32, n, index),
+            _drafted(uniforms, "uniforms", torch.float32, n, index))
 
 
 def apply_logit_rules(logits, rules, draft_ids=None, *, R: int | None = None, out=None):
@@ -984,39 +998,30 @@ def apply_logit_rules(logits, rules, draft_ids=None, *, R: int | None = None, ou
     strided); draft_ids int32 [R, T-1] (None when T == 1): row t counts drafts
     0 .. t-1 as generated.  out: the tensor to write, of the logits' shape and
     type, which may be the logits.  Returns it."""
-    rows, stride, code, R, T, V = _logit_rows(logits, R)
-    dev = logits.device
+    code, stride, R, T, V = _logit_rows(logits, R)
+    index = logits.get_device()
     if rules is not None:
-        rules.check(dev, R, T, V)
-    dr, _, _ = _drafts(dev, R, T, draft_ids)
+        rules.check(index, R, T, V)
+    dr = _drafts(index, R, T, draft_ids)[0]
+    os_ = V
     if out is None:
-        res = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
-        ptr, os_ = res.data_ptr(), V
+        out = torch.empty_like(logits, memory_format=torch.contiguous_format)
     else:
-        if not isinstance(out, torch.Tensor) or out.shape != logits.shape or out.dtype != logits.dtype or out.device != dev:
-            raise ValueError("out must have the shape, type and device of the logits")
-        res = out
-        o2, os_ = _rows2d(out, "out")
-        ptr = o2.data_ptr()
-    with _guard(dev):
-        st = load_library().logit_rules_apply(rows.data_ptr(), stride, code, dr, R, T, V,
-                                              None if rules is None else rules.packed, ptr, os_, _raw_stream(dev))
+        if not isinstance(out, torch.Tensor) or out.shape != logits.shape or out.dtype != logits.dtype:
+            raise ValueError("out must have the shape and type of the logits")
+        _same_device(index, out=out)
+        os_ = _rows2d(out, "out")[2]
+    st = _on(index, load_library().logit_rules_apply, logits.data_ptr(), stride, code, dr, R, T, V,
+             None if rules is None else rules.packed, out.data_ptr(), os_, _raw_stream(index))
     if st != OK:
         _raise(st, "logit_rules_apply")
-    return res
+    return out
 
 
-def _verify_outputs(dev, M, R, T, k, sampled, want_lse):
-    f, i = torch.float32, torch.int32
-    return (torch.empty(M, dtype=f, device=dev), torch.empty(M, dtype=i, device=dev),
-            torch.empty((M, k), dtype=i, device=dev) if k else None,
-            torch.empty((M, k), dtype=f, device=dev) if k else None,
-            torch.empty((R, T - 1), dtype=f, device=dev) if sampled else None,
-            torch.empty(R, dtype=i, device=dev), torch.empty(M, dtype=f, device=dev) if want_lse else None)
-
-
-def _at(t):
-    return None if t is None else t.data_ptr()
+def _verify_outputs(like, M, R, T, k, sampled, want_lse):
+    f, i, new = torch.float32, torch.int32, like.new_empty
+    return (new(M, dtype=f), new(M, dtype=i), new((M, k), dtype=i) if k else None, new((M, k), dtype=f) if k else None,
+            new((R, T - 1), dtype=f) if sampled else None, new(R, dtype=i), new(M, dtype=f) if want_lse else None)
 
 
 def verify_logits(logits, rules=None, draft_ids=None, draft_probs=None, uniforms=None, *, top_k: int = 0,
@@ -1030,23 +1035,21 @@ def verify_logits(logits, rules=None, draft_ids=None, draft_probs=None, uniforms
     [R*T, k], p_draft [R, T-1], n_accepted [R], lse [R*T]); the top-k outputs
     are None when top_k == 0, p_draft without draft_probs or when T == 1, lse
     unless want_lse.  A row whose mask leaves nothing has argmax -1."""
-    rows, stride, code, R, T, V = _logit_rows(logits, R)
-    dev = logits.device
+    code, stride, R, T, V = _logit_rows(logits, R)
+    index = logits.get_device()
     if rules is not None:
-        rules.check(dev, R, T, V)
-    dr, dp, un = _drafts(dev, R, T, draft_ids, draft_probs, uniforms)
+        rules.check(index, R, T, V)
+    dr, dp, un = _drafts(index, R, T, draft_ids, draft_probs, uniforms)
     M, k = R * T, int(top_k)
     L = load_library()
     need = L.logit_rules_verify_workspace_bytes(R, T, V, k)
     if need == 0:
         _raise(EINVAL, "logit_rules_verify")
-    out = lmax, amax, tids, tlog, pdr, nacc, lse = _verify_outputs(dev, M, R, T, k, dp is not None, want_lse)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    with _guard(dev):
-        st = L.logit_rules_verify(rows.data_ptr(), stride, code, dr, dp, un, R, T, V,
-                                  None if rules is None else rules.packed, k, temperature, lmax.data_ptr(),
-                                  amax.data_ptr(), _at(tids), _at(tlog), _at(lse), _at(pdr), nacc.data_ptr(),
-                                  ws.data_ptr(), need, _raw_stream(dev))
+    out = lmax, amax, tids, tlog, pdr, nacc, lse = _verify_outputs(logits, M, R, T, k, dp is not None, want_lse)
+    ws = logits.new_empty(need, dtype=torch.uint8)
+    st = _on(index, L.logit_rules_verify, logits.data_ptr(), stride, code, dr, dp, un, R, T, V,
+             None if rules is None else rules.packed, k, temperature, lmax.data_ptr(), amax.data_ptr(), _at(tids),
+             _at(tlog), _at(lse), _at(pdr), nacc.data_ptr(), ws.data_ptr(), need, _raw_stream(index))
     if st != OK:
         _raise(st, "logit_rules_verify")
     return out
@@ -1074,27 +1077,27 @@ def verify_ruled(hidden, packed_w, scales, rules, draft_ids=None, draft_probs=No
     V = packed_w.shape[0]
     if packed_w.shape[1] * 2 != H or scales.shape[0] != H or hidden.shape[0] != R * T:
         raise ValueError("shape mismatch between hidden, packed_w and scales")
-    dev = hidden.device
-    _same_device(dev, packed_w=packed_w, scales=scales)
+    index = hidden.get_device()
+    _same_device(index, packed_w=packed_w, scales=scales)
     if rules is not None:
-        rules.check(dev, R, T, V)
-    dr, dp, un = _drafts(dev, R, T, draft_ids, draft_probs, uniforms)
+        rules.check(index, R, T, V)
+    dr, dp, un = _drafts(index, R, T, draft_ids, draft_probs, uniforms)
     k = int(top_k)
     L = load_library()
     need = L.verify_lm_head_int4_ruled_workspace_bytes(R, T, V, H, k)
     if need == 0:
         _raise(EINVAL, "verify_lm_head_int4_ruled")
-    out = lmax, amax, tids, tlog, pdr, nacc, lse = _verify_outputs(dev, R * T, R, T, k, dp is not None, want_lse)
-    with _guard(dev):
-        if workspace is None:
-            # a graph keeps its own: the stream's may be replaced by a larger one
-            capturing = torch.cuda.is_current_stream_capturing()
-            workspace = Workspace(need, dev) if capturing else _default_workspace(dev, need)
-        st = L.verify_lm_head_int4_ruled(hidden.data_ptr(), packed_w.data_ptr(), scales.data_ptr(), dr, dp, un, R, T,
-                                         V, H, None if rules is None else rules.packed, k, temperature,
-                                         lmax.data_ptr(), amax.data_ptr(), _at(tids), _at(tlog), _at(lse), _at(pdr),
-                                         nacc.data_ptr(), workspace.tensor.data_ptr(), workspace.nbytes,
-                                         _raw_stream(dev))
+    out = lmax, amax, tids, tlog, pdr, nacc, lse = _verify_outputs(hidden, R * T, R, T, k, dp is not None, want_lse)
+    if workspace is None:
+        # a graph keeps its own: the stream's may be replaced by a larger one
+        capturing = torch.cuda.is_current_stream_capturing()
+        workspace = _on(index, Workspace if capturing else lambda n, d: _default_workspace(d, n), need, hidden.device)
+    else:
+        _same_device(index, workspace=workspace.tensor)
+    st = _on(index, L.verify_lm_head_int4_ruled, hidden.data_ptr(), packed_w.data_ptr(), scales.data_ptr(), dr, dp, un,
+             R, T, V, H, None if rules is None else rules.packed, k, temperature, lmax.data_ptr(), amax.data_ptr(),
+             _at(tids), _at(tlog), _at(lse), _at(pdr), nacc.data_ptr(), workspace.tensor.data_ptr(), workspace.nbytes,
+             _raw_stream(index))
     if st != OK:
         _raise(st, "verify_lm_head_int4_ruled")
     return out
