@@ -24,8 +24,8 @@
  * the verify calls do, they leave the weights pure integers.
  *
  * Numerics.  Everything is binary32, one rounding per operation in the order
- * written (the sum of squares in an order that depends on H and on M only
- * through the launch shape; it moves rstd by a few units in the last place).
+ * written (the sum of squares in an order that depends on H alone: a row gives
+ * the same bits in every batch).
  * The norm uses h before it is rounded to the rows' type.  The codes do not
  * depend on rstd.  A NaN or an infinity in a row makes that row's outputs NaN
  * or infinite as the formulas do; in 8 bits its codes are 0 and its row_scale
