@@ -239,8 +239,6 @@ __global__ void __launch_bounds__(kMaxThreads) norm_rows_kernel(NormArgs a)
             peak = i < n_waves ? s_peak[buf][i] : 0u;
             reduce<16, kNorm, kInt8>(ss, peak);
         }
-        const float rstd = kNorm ? 1.0f / sqrtf(ss / (float)H + a.eps) : 1.0f;
-
         if (kInt8) {
             const float pk = __uint_as_float(peak);
             const bool tiny = pk < kTinyPeak;
@@ -251,9 +249,12 @@ __global__ void __launch_bounds__(kMaxThreads) norm_rows_kernel(NormArgs a)
             for (int j = 0; j < 8; ++j)        // |t * inv| <= 127 (1 + 2^-23): rint never leaves [-127, 127]
                 q[j] = live ? (int)rintf(t[j] * inv) : 0;
             store_codes8(a.codes + (size_t)m * H, c, H, q);
-            if (tid == 0)
+            if (tid == 0) {
+                const float rstd = kNorm ? 1.0f / sqrtf(ss / (float)H + a.eps) : 1.0f;
                 a.row_scales[m] = tiny ? 0.0f : (pk * rstd) / 127.0f;
+            }
         } else {
+            const float rstd = 1.0f / sqrtf(ss / (float)H + a.eps);
             float y[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
