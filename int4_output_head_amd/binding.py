@@ -686,6 +686,8 @@ def _rows2d(t, name):
         M = t.numel() // H if H else 0
     if M < 1 or H < 1:
         raise ValueError(f"{name} must not be empty")
+    if M > 0x7FFFFFFF or H > 0x7FFFFFFF:
+        raise ValueError(f"{name} has too many rows or channels")
     if stride < H:
         raise ValueError(f"{name} must not have overlapping rows")
     return M, H, stride

@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_rows_kernel(NormArgs a)
     }
 
     int buf = 0;
-    for (int m = blockIdx.x; m < a.M; m += gridDim.x, buf ^= 1) {
+    for (unsigned m = blockIdx.x; m < (unsigned)a.M; m += gridDim.x, buf ^= 1) {
         float h[8];
         load8<kDtype>(static_cast<const char *>(a.x) + (size_t)m * a.x_stride * kSize, c, H, h);
         if (a.residual) {

@@ -175,6 +175,20 @@ def test_counts_and_entries_too_many_for_one_word(b, n, nb):
     same(b.apply_logit_rules(dev(logits), device_rules(b, rules), dev(drafts), R=R), want)
 
 
+def test_verify_with_the_longest_slices(b):
+    """Words apart, whole slices and top-k lists: the most LDS a call takes."""
+    R, T, V, nb = 60, 4, 20000, 3000
+    g = np.random.default_rng(5)
+    logits, rules, drafts = make(R, T, V, 2, history=100, bias=0)
+    rules["bias_ids"] = g.integers(0, V, nb).astype(np.int32)
+    rules["bias_values"] = g.normal(0, 4, nb).astype(np.float32)
+    rules["bias_offsets"] = np.linspace(0, nb, R + 1).astype(np.int64)
+    x = lr.ruled(logits, rules, drafts, R, T)
+    got = b.verify_logits(dev(logits), device_rules(b, rules), dev(drafts), R=R, top_k=16, want_lse=True)
+    check_verify(got, x, drafts, None, None, R, T, 16, 1.0, True)
+    same(b.apply_logit_rules(dev(logits), device_rules(b, rules), dev(drafts), R=R), x)
+
+
 def test_offsets_outside_are_clamped(b):
     logits, rules, drafts = make(2, 2, 500, 3)
     n, m = len(rules["history"]), len(rules["bias_ids"])
