@@ -304,23 +304,37 @@ __device__ __forceinline__ long long clamp64(long long v, long long lo, long lon
     return v < lo ? lo : v > hi ? hi : v;
 }
 
+// A request's part of the histories (generated from `made` on) and of the bias
+// entries.
+struct Spans {
+    long long hb, he, made, bb, be;
+};
+__device__ __forceinline__ Spans load_spans(const RulesArgs &a, int req)
+{
+    Spans s = {0, 0, 0, 0, 0};
+    if (a.has_penalty && a.r.history) {
+        const long long b = a.r.history_offsets[req], e = a.r.history_offsets[req + 1];
+        const int prompt = a.r.n_prompt ? a.r.n_prompt[req] : 0;
+        s.hb = clamp64(b, 0, a.r.n_history);
+        s.he = clamp64(e, 0, a.r.n_history);
+        s.made = s.hb + prompt;
+    }
+    if (a.has_bias) {
+        const long long b = a.r.bias_offsets[req], e = a.r.bias_offsets[req + 1];
+        s.bb = clamp64(b, 0, a.r.n_bias);
+        s.be = clamp64(e, 0, a.r.n_bias);
+    }
+    return s;
+}
+
 // The slice's tokens in one request's history and biases: the words of tokens
 // base .. base + S - 1, and the entries' where they lie apart.  Called by the
 // whole workgroup, which waits at the end.
-__device__ __forceinline__ void prepare_slice(const RulesArgs &a, int req, int base, int S, uint32_t *words,
+__device__ __forceinline__ void prepare_slice(const RulesArgs &a, const Spans &span, int base, int S, uint32_t *words,
                                               uint32_t *entries)
 {
     const int tid = threadIdx.x, nt = blockDim.x;
-    long long hb = 0, he = 0, made = 0, bb = 0, be = 0;
-    if (a.has_penalty && a.r.history) {
-        hb = clamp64(a.r.history_offsets[req], 0, a.r.n_history);
-        he = clamp64(a.r.history_offsets[req + 1], 0, a.r.n_history);
-        made = hb + (a.r.n_prompt ? a.r.n_prompt[req] : 0);
-    }
-    if (a.has_bias) {
-        bb = clamp64(a.r.bias_offsets[req], 0, a.r.n_bias);
-        be = clamp64(a.r.bias_offsets[req + 1], 0, a.r.n_bias);
-    }
+    const long long hb = span.hb, he = span.he, made = span.made, bb = span.bb, be = span.be;
     // Four tokens a load, kFly loads in flight per thread; loads past the end
     // take the last four tokens instead, whose earlier ones are not theirs.
     constexpr int kFly = 4;
@@ -412,6 +426,25 @@ __global__ void __launch_bounds__(64 * kMaxWaves) rules_kernel(RulesArgs a)
     constexpr size_t kSize = kDtype == INT4VH_ROWS_F32 ? 4 : 2;
     const char *lrow = static_cast<const char *>(a.logits) + (size_t)row * a.logits_stride * kSize;
 
+    // A chunk's logits, and its mask in the lanes below 32, a word each.
+    // Tokens past V load the row's last one and are struck out below.
+    struct Held {
+        float x[kPer];
+        uint32_t bits;
+    };
+    const uint32_t last = (uint32_t)(V - 1) * (uint32_t)kSize;
+    auto load_x = [&](int c, Held &h) {
+        const int t0 = begin + min(c, n_chunks - 1) * kChunk;
+        const uint32_t at = (uint32_t)(t0 + lane) * (uint32_t)kSize;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            h.x[i] = load_logit<kDtype>(lrow + min(at + (uint32_t)(64 * kSize) * i, last), 0);
+    };
+    Held ha, hb;
+    ha.bits = hb.bits = 0u;
+    if (n_chunks > 0)
+        load_x(0, ha);                        // on its way while the slice is counted
+    const Spans span = load_spans(a, req);
     const uint32_t *mask = nullptr;
     bool none = false;                        // nothing is allowed
     if (a.r.mask) {
@@ -422,36 +455,26 @@ __global__ void __launch_bounds__(64 * kMaxWaves) rules_kernel(RulesArgs a)
     }
     const int mask_words = (V + 31) / 32;
 
-    // A chunk's logits, and its mask in the lanes below 32, a word each.
-    // Tokens past V load the row's last one and are struck out below.
-    struct Held {
-        float x[kPer];
-        uint32_t bits;
-    };
-    const uint32_t last = (uint32_t)(V - 1) * (uint32_t)kSize;
-    auto load = [&](int c, Held &h) {
-        const int t0 = begin + min(c, n_chunks - 1) * kChunk;
-        const uint32_t at = (uint32_t)(t0 + lane) * (uint32_t)kSize;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            h.x[i] = load_logit<kDtype>(lrow + min(at + (uint32_t)(64 * kSize) * i, last), 0);
+    auto load_bits = [&](int c, Held &h) {
         if (mask)
-            h.bits = mask[min((t0 >> 5) + (lane & 31), mask_words - 1)];
+            h.bits = mask[min(((begin + min(c, n_chunks - 1) * kChunk) >> 5) + (lane & 31), mask_words - 1)];
     };
-    Held ha, hb;
-    ha.bits = hb.bits = 0u;
     if (n_chunks > 0)
-        load(0, ha);                          // on its way while the slice is counted
+        load_bits(0, ha);
+    auto load = [&](int c, Held &h) {
+        load_x(c, h);
+        load_bits(c, h);
+    };
 
     if (a.has_penalty || a.has_bias)
-        prepare_slice(a, req, base, S, words, entries);
+        prepare_slice(a, span, base, S, words, entries);
     if (t >= a.T || t >= (int)(blockIdx.z + 1) * a.row_group)
         return;                               // no barrier follows
 
     const float rep = a.r.repetition ? a.r.repetition[req] : 1.0f;
     const float freq = a.r.frequency ? a.r.frequency[req] : 0.0f;
     const float pres = a.r.presence ? a.r.presence[req] : 0.0f;
-    const float *bias = a.has_bias ? a.r.bias_values + clamp64(a.r.bias_offsets[req], 0, a.r.n_bias) : nullptr;
+    const float *bias = a.has_bias ? a.r.bias_values + span.bb : nullptr;
     // lane j holds draft j, for the rows behind it; the row's own draft
     int mine = -1, d = -1;
     if (a.T > 1) {
