@@ -373,6 +373,45 @@ def test_empty_rows_and_infinities(b):
     assert abs(lse[4].item() - want) <= 93 * U * abs(want)
 
 
+@pytest.mark.parametrize("R,T", [(1, 1), (2, 6)])
+def test_empty_history_and_biases_still_count_the_drafts(b, R, T):
+    V = 1100
+    logits, rules, drafts = make(R, T, V, 3, history=0, bias=0, mask=None)
+    drafts = drafts % 7 if T > 1 else drafts            # repeated drafts
+    none = dict(rules, history=np.zeros(0, np.int32), history_offsets=np.zeros(R + 1, np.int64),
+                n_prompt=np.zeros(R, np.int32), bias_ids=np.zeros(0, np.int32),
+                bias_values=np.zeros(0, np.float32), bias_offsets=np.zeros(R + 1, np.int64))
+    want = lr.ruled(logits, rules, drafts, R, T)
+    d = dev(drafts) if T > 1 else None
+    same(b.apply_logit_rules(dev(logits), device_rules(b, none), d, R=R), want)
+    check_verify(b.verify_logits(dev(logits), device_rules(b, none), d, R=R, top_k=4), want, drafts, None, None, R, T,
+                 4, 1.0, False)
+
+
+@pytest.mark.parametrize("k", [0, 9])
+@pytest.mark.parametrize("tau", [1e-42, 2e-38, 3e38])
+def test_temperatures_at_the_ends(b, tau, k):
+    # The scale log2(e) / tau overflows, is near the largest number, or is
+    # subnormal: the best token has all of the probability, or each its share.
+    R, T, V = 2, 3, 3001
+    logits, rules, drafts = make(R, T, V, 17, mask=None)
+    x = lr.ruled(logits, rules, drafts, R, T)
+    drafts = near_drafts(x, drafts, R, T, k)
+    x = lr.ruled(logits, rules, drafts, R, T)
+    g = np.random.default_rng(k)
+    dp, un = g.random((2, R, T - 1)).astype(np.float32)
+    got = b.verify_logits(dev(logits), device_rules(b, rules), dev(drafts), dev(dp), dev(un), R=R, top_k=k,
+                          temperature=tau, want_lse=True)
+    if tau < 1:                                          # 1/tau times a maximum above 1 is beyond binary32 or close
+        best = x.argmax(1)
+        for i in range(R):
+            for t in range(T - 1):
+                assert got[4][i, t].item() == float(drafts[i, t] == best[i * T + t])
+        assert not torch.isnan(got[6]).any()
+    else:
+        check_verify(got, x, drafts, dp, un, R, T, k, float(np.float32(tau)), True)
+
+
 def test_no_rules_equals_verify_sampled(b):
     """The same logits, once through the head's own sampled epilogue."""
     from int4_output_head_amd import synth
