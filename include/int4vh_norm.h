@@ -48,7 +48,8 @@
  * an unknown dtype, a stride below H (M > 1), eps negative or not finite, a
  * required pointer that is NULL, or a sum_out without a residual;
  * INT4VH_EALIGN for a pointer that is not aligned to its element;
- * INT4VH_EUNSUPPORTED for H > 8192; INT4VH_EHIP for a launch failure.
+ * INT4VH_EUNSUPPORTED for H > 8192 (quantize_rows_int8: 65536, the linear
+ * layers' limit); INT4VH_EHIP for a launch failure.
  */
 #ifndef INT4VH_NORM_H
 #define INT4VH_NORM_H

@@ -763,7 +763,7 @@ def rms_norm_int8(x, weight, residual=None, *, channel_scales=None, eps: float =
 
 def quantize_rows(x, *, channel_scales=None):
     """Rows x [..., H] in 8 bits with one scale per row, without a norm (the
-    activations of a linear_int4 whose input is no norm).  Returns (codes int8
+    activations of a linear_int4 whose input is no norm; H up to 65536).  Returns (codes int8
     [..., H], row_scales float32 [M])."""
     dt = _row_code(x, "x")
     M, H, xs = _rows2d(x, "x")

@@ -59,7 +59,7 @@ def test_norm8_refusals(lib, kw, status):
 @pytest.mark.parametrize("args,status", [
     ((0, 64, 0, A, 4, 64, A, A), EINVAL), ((A, 64, 5, A, 4, 64, A, A), EINVAL), ((A, 60, 0, A, 4, 64, A, A), EINVAL),
     ((A, 64, 0, A, 4, 64, 0, A), EINVAL), ((A, 64, 0, A, 4, 64, A, 0), EINVAL), ((A, 64, 0, A + 1, 4, 64, A, A), EALIGN),
-    ((A, 8193, 0, A, 4, 8193, A, A), EUNSUPPORTED),
+    ((A, 65537, 0, A, 4, 65537, A, A), EUNSUPPORTED),
 ])
 def test_quantize_refusals(lib, args, status):
     assert lib.quantize_rows_int8(*args, None) == status

@@ -101,6 +101,34 @@ def test_norm_int8(b, M, H, dt):
         close_codes(q[0], q[1], x, None, None, c, 0.0, norm=False)
 
 
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("M,H", [(1, 8193), (3, 9000), (2, 16384), (1, 16385), (5, 25600), (2, 32769), (1, 65536),
+                                 (1100, 8200)])
+def test_long_rows_in_8_bits(b, M, H, dt):
+    for channel in (True, False):
+        x, _, _, c = make(M, H, DT[dt], M + H, False)
+        x[:, -1] *= 50                                 # the peak in the overlapping chunks of some rows
+        c = c if channel else None
+        q, sc = b.quantize_rows(gpu(x), channel_scales=gpu(c))
+        close_codes(q, sc, x, None, None, c, 0.0, norm=False)
+        buf = torch.full((M, H + 3), 7, dtype=DT[dt])  # strided, unaligned rows
+        buf[:, 3:] = x
+        q2, sc2 = b.quantize_rows(gpu(buf)[:, 3:], channel_scales=gpu(c))
+        assert torch.equal(q, q2) and torch.equal(sc, sc2)
+
+
+def test_long_zero_tiny_and_non_finite_rows(b):
+    H = 20001
+    x = torch.ones(6, H)
+    x[0], x[1] = 0, 2.0 ** -110
+    x[2, 20000], x[3, 5], x[4, 12000] = float("inf"), float("nan"), -float("inf")
+    q, s = b.quantize_rows(x.cuda())
+    assert torch.equal(q[:5].cpu(), torch.zeros(5, H, dtype=torch.int8))
+    s = s.cpu()
+    assert s[0] == 0 and s[1] == 0 and torch.isinf(s[2]) and torch.isnan(s[3]) and torch.isinf(s[4])
+    assert torch.equal(q[5].cpu(), torch.full((H,), 127, dtype=torch.int8))
+
+
 def test_weights_of_another_type(b):
     x, r, w, c = make(9, 1000, torch.bfloat16, 5)
     for wd in DT.values():
