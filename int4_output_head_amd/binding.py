@@ -144,7 +144,10 @@ def sampled_workspace_bytes(R: int, T: int, V: int, H: int) -> int:
 
 class Workspace:
     """A device workspace for verify calls, initialised on creation.  Calls
-    that share a Workspace must not be in flight at the same time."""
+    that share a Workspace must not be in flight at the same time, replays of
+    graphs that were captured with it among them; a graph does not keep it
+    alive.  Calls without one use one per stream, or under capture one per
+    call, which is part of the graph."""
 
     def __init__(self, nbytes: int, device):
         self.nbytes = int(nbytes)
@@ -159,6 +162,12 @@ _ws_cache: dict = {}
 
 
 def _default_workspace(device, nbytes: int) -> Workspace:
+    # A graph keeps the addresses it was captured with, while an eager call may
+    # replace the stream's workspace by a larger one, and a replay may run
+    # beside the stream's eager calls: a call under capture gets its own, from
+    # the graph's memory, which the graph initialises itself.
+    if _on(device.index, torch.cuda.is_current_stream_capturing):
+        return Workspace(nbytes, device)
     # one per (device, current stream): calls on one stream are ordered
     key = (device.index, torch.cuda.current_stream(device).cuda_stream)
     ws = _ws_cache.get(key)
@@ -1063,8 +1072,9 @@ def verify_ruled(hidden, packed_w, scales, rules, draft_ids=None, draft_probs=No
     """Verification through the head under rules (LogitRules): verify_batch's
     logits through verify_logits, in one call.  hidden: float16 [R, T, H] (or
     [R*T, H] with R); the other arguments and the outputs as verify_logits.
-    The workspace also holds the call's logits
-    (verify_lm_head_int4_ruled_workspace_bytes)."""
+    The workspace also holds the call's logits, R*T*V*4 bytes
+    (verify_lm_head_int4_ruled_workspace_bytes); without one of the caller's,
+    the stream's own grows to that size and is kept for later calls."""
     if hidden.dim() == 3:
         R, T, H = hidden.shape
         hidden = hidden.reshape(R * T, H)
@@ -1091,9 +1101,7 @@ def verify_ruled(hidden, packed_w, scales, rules, draft_ids=None, draft_probs=No
         _raise(EINVAL, "verify_lm_head_int4_ruled")
     out = lmax, amax, tids, tlog, pdr, nacc, lse = _verify_outputs(hidden, R * T, R, T, k, dp is not None, want_lse)
     if workspace is None:
-        # a graph keeps its own: the stream's may be replaced by a larger one
-        capturing = torch.cuda.is_current_stream_capturing()
-        workspace = _on(index, Workspace if capturing else lambda n, d: _default_workspace(d, n), need, hidden.device)
+        workspace = _on(index, _default_workspace, hidden.device, need)
     else:
         _same_device(index, workspace=workspace.tensor)
     st = _on(index, L.verify_lm_head_int4_ruled, hidden.data_ptr(), packed_w.data_ptr(), scales.data_ptr(), dr, dp, un,
