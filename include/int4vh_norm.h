@@ -30,8 +30,9 @@
  * depend on rstd.  A NaN or an infinity in a row makes that row's outputs NaN
  * or infinite as the formulas do; in 8 bits its codes are 0 and its row_scale
  * is NaN or infinite.  A row whose peak is below 2^-100 has codes 0 and
- * row_scale 0.  The sum of squares overflows for rows beyond about 1e18
- * (out of reach for binary16).
+ * row_scale 0.  Rows of any finite size are normed as the formulas say: where
+ * mean h^2 + eps overflows or is below 2^-80, the squares are summed at a scale
+ * of another power of two, which rounds nothing.
  *
  * Layout.  x and residual: [M, H] of `dtype`, rows x_stride / residual_stride
  * elements apart (at least H, or any value when M == 1), channels contiguous.

@@ -36,6 +36,12 @@ using namespace int4vh_detail;
 constexpr int kMaxThreads = 1024;
 constexpr int kMaxLong = 65536;           // channels of a row in 8 bits without a norm
 constexpr float kTinyPeak = 0x1p-100f;    // rows below it have no finite 127 / peak worth using
+// Rows whose mean square + eps would overflow (from an rms of 2^57.5 on, for
+// 8192 channels) or is below kLowMean, where squares get lost to subnormal
+// numbers, are summed once more at another scale: kDown, at which squares
+// reach 2^96 and their sum 2^109, or kUp, at which the smallest subnormal
+// number squares to 2^-118 and a sum stays below 2^113.
+constexpr float kLowMean = 0x1p-80f, kDown = 0x1p-80f, kUp = 0x1p90f;
 
 struct NormArgs {
     const void *x;
@@ -182,6 +188,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_rows_kernel(NormArgs a)
 {
     __shared__ float s_sum[2][kMaxThreads / 64];
     __shared__ uint32_t s_peak[2][kMaxThreads / 64];
+    __shared__ float s_again[kMaxThreads / 64];
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 63, wave = tid >> 6, n_waves = nt >> 6;
     const int H = a.H;
     constexpr size_t kSize = kDtype == INT4VH_ROWS_F32 ? 4 : 2;
@@ -200,6 +207,10 @@ __global__ void __launch_bounds__(kMaxThreads) norm_rows_kernel(NormArgs a)
                 cs[j] = 1.0f;
         }
     }
+
+    // sums of squares that serve as they are
+    const float low_sum = a.eps < kLowMean ? kLowMean * (float)H : 0.0f;
+    const float high_sum = a.eps < 0x1p126f ? 0x1p127f : 0.0f;
 
     int buf = 0;
     for (unsigned m = blockIdx.x; m < (unsigned)a.M; m += gridDim.x, buf ^= 1) {
@@ -247,9 +258,9 @@ __global__ void __launch_bounds__(kMaxThreads) norm_rows_kernel(NormArgs a)
             peak = i < n_waves ? s_peak[buf][i] : 0u;
             reduce<16, kNorm, kInt8>(ss, peak);
         }
+        const float pk = __uint_as_float(peak);
+        const bool tiny = pk < kTinyPeak;
         if (kInt8) {
-            const float pk = __uint_as_float(peak);
-            const bool tiny = pk < kTinyPeak;
             const bool live = !tiny && peak < 0x7F800000u;
             const float inv = 127.0f / pk;
             int q[8];
@@ -257,16 +268,52 @@ __global__ void __launch_bounds__(kMaxThreads) norm_rows_kernel(NormArgs a)
             for (int j = 0; j < 8; ++j)        // |t * inv| <= 127 (1 + 2^-23): rint never leaves [-127, 127]
                 q[j] = live ? (int)rintf(t[j] * inv) : 0;
             store_codes8(a.codes + (size_t)m * H, c, H, q);
+        }
+        // before and behind: powers of two that make up for another scale
+        float eps = a.eps, before = 1.0f, behind = 1.0f;
+        // The same in every thread: a scalar, for a jump out of the usual way.
+        // binary16 rows stay inside by far (between 2^-48 and 2^47).
+        const bool again = kNorm && kDtype != INT4VH_ROWS_F16 &&
+                           __builtin_amdgcn_readfirstlane(ss < low_sum || ss > high_sum);
+        if (__builtin_expect(again, false)) {
+            const bool low = ss < low_sum;
+            const float f = low ? kUp : kDown;
+            ss = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                ss = __builtin_fmaf(h[j] * f, h[j] * f, ss);
+            uint32_t none = 0u;
+            reduce<64, true, false>(ss, none);
+            if (n_waves > 1) {
+                if (lane == 0)
+                    s_again[wave] = ss;        // the row before read it in front of this row's first barrier
+                __syncthreads();
+                ss = (lane & 15) < n_waves ? s_again[lane & 15] : 0.0f;
+                reduce<16, true, false>(ss, none);
+            }
+            eps = eps * f * f;
+            // small rows are scaled up front, large ones at the end: no
+            // product in between overflows or loses bits
+            before = low ? f : 1.0f;
+            behind = low ? 1.0f : f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                h[j] *= before;
+        }
+        if (kInt8) {
             if (tid == 0) {
-                const float rstd = kNorm ? 1.0f / sqrtf(ss / (float)H + a.eps) : 1.0f;
-                a.row_scales[m] = tiny ? 0.0f : (pk * rstd) / 127.0f;
+                const float rstd = kNorm ? 1.0f / sqrtf(ss / (float)H + eps) : 1.0f;
+                float top = pk * rstd;
+                if (__builtin_expect(again, false))    // exact in binary64, then the product's one rounding
+                    top = (float)((double)pk * rstd * before * behind);
+                a.row_scales[m] = tiny ? 0.0f : top / 127.0f;
             }
         } else {
-            const float rstd = 1.0f / sqrtf(ss / (float)H + a.eps);
+            const float rstd = 1.0f / sqrtf(ss / (float)H + eps);
             float y[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                y[j] = h[j] * rstd * w[j];
+                y[j] = h[j] * rstd * behind * w[j];
             store8(static_cast<char *>(a.out) + (size_t)m * H * out_size, a.out_dtype, c, H, y);
         }
     }
