@@ -62,7 +62,7 @@ def activate64(y, activation):
     if activation == "relu":
         return np.where(y < 0, 0.0, y)
     if activation == "gelu":
-        return 0.5 * y * (1.0 + np.vectorize(math.erf, otypes=[np.float64])(y * math.sqrt(0.5)))
+        return 0.5 * y * np.vectorize(math.erfc, otypes=[np.float64])(-y * math.sqrt(0.5))
     if activation == "silu":
         with np.errstate(over="ignore"):
             return y / (1.0 + np.exp(-y))
