@@ -14,8 +14,8 @@
  *   seen   = v occurs there or anywhere in the request's history
  *   l0     = f32(logit)
  *   l1     = seen ? (l0 > 0 ? l0 / repetition[i] : l0 * repetition[i]) : l0
- *   l2     = l1 - frequency[i] * count
- *   l3     = l2 - (count > 0 ? presence[i] : 0)
+ *   l2     = count > 0 ? l1 - frequency[i] * count : l1
+ *   l3     = count > 0 ? l2 - presence[i] : l2
  *   l4     = l3 + bias(i, v)
  *   ruled  = v is allowed in the row ? l4 : -infinity
  *
@@ -33,7 +33,9 @@
  *   n_prompt         int32 [R], leading tokens of each history that are the
  *                    prompt; NULL: 0, all of it is generated
  *   repetition, frequency, presence
- *                    float32 [R], each NULL for none; repetition > 0
+ *                    float32 [R], each NULL for none; repetition > 0; infinite
+ *                    ones hold too (a frequency or presence of infinity bans
+ *                    what was generated, and nothing else)
  *   bias_ids, bias_values
  *                    int32, float32 [n_bias], request i's entries in
  *                    [bias_offsets[i], bias_offsets[i+1]) (int64 [R+1], clamped);

@@ -408,9 +408,10 @@ __device__ __forceinline__ void prepare_slice(const RulesArgs &a, const Spans &s
 
 __device__ __forceinline__ float penalise(float l, uint32_t count, float rep, float freq, float pres)
 {
-    float x = l > 0.0f ? l / rep : l * rep;
-    x = x - freq * (float)count;
-    return x - (count ? pres : 0.0f);
+    const float x = l > 0.0f ? l / rep : l * rep;
+    // tokens of the prompt alone keep x, whatever the other two are (an
+    // infinite frequency times a count of 0 would be NaN)
+    return count ? x - freq * (float)count - pres : x;
 }
 
 // Grid (slices of the vocabulary, requests, row groups); wave w takes row w /
