@@ -55,8 +55,9 @@
  * 1), a required pointer that is NULL (draft_ids when T > 1; the offsets with
  * a history or biases; a mask's words below ceil(V/32) or n_masks < 1, or below
  * R*T without mask_index; negative n_history or n_bias); INT4VH_EALIGN for a
- * pointer not aligned to its element; INT4VH_EUNSUPPORTED for V > 2^24;
- * INT4VH_EWORKSPACE, INT4VH_EHIP as in int4vh.h.
+ * pointer not aligned to its element; INT4VH_EUNSUPPORTED for V > 2^24,
+ * n_history > 2^31 - 17 or n_bias > 2^31 - 1; INT4VH_EWORKSPACE, INT4VH_EHIP as
+ * in int4vh.h.
  */
 #ifndef INT4VH_LOGITS_H
 #define INT4VH_LOGITS_H

@@ -68,6 +68,7 @@ constexpr WordLayout kShared = {(1u << 20) - 1u, 1u << 20, 21};
 constexpr WordLayout kApart = {0x7FFFFFFFu, 0x80000000u, 0};
 constexpr long long kSharedHistory = (1ll << 20) - 32;   // generated tokens, drafts on top
 constexpr long long kSharedEntries = (1 << 11) - 1;
+constexpr long long kMaxHistory = (1ll << 31) - 1 - INT4VH_MAX_T, kMaxEntries = (1ll << 31) - 1;   // kApart's
 
 struct RulesArgs {
     const void *logits;
@@ -903,6 +904,8 @@ int check(const void *logits, int64_t stride, int dtype, const int32_t *draft, i
               !rows_aligned(r->bias_ids, 4) || !rows_aligned(r->bias_values, 4) || !rows_aligned(r->bias_offsets, 8) ||
               !rows_aligned(r->mask, 4) || !rows_aligned(r->mask_index, 4)))
         return INT4VH_EALIGN;
+    if (r && (r->n_history > kMaxHistory || r->n_bias > kMaxEntries))
+        return INT4VH_EUNSUPPORTED;
     return V > kMaxV ? INT4VH_EUNSUPPORTED : INT4VH_OK;
 }
 
