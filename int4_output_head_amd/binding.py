@@ -652,8 +652,12 @@ def stream_read(buf, mode: int = 0, *, out=None, events=None):
 
 ROWS_F16, ROWS_BF16, ROWS_F32 = 0, 1, 2
 _ROW_DTYPES = {torch.float16: ROWS_F16, torch.bfloat16: ROWS_BF16, torch.float32: ROWS_F32}
-_raw_stream = torch._C._cuda_getCurrentRawStream     # by device index
-_current_device = torch._C._cuda_getDevice
+# A device's current stream by its index, and the current device.  The calls
+# behind torch.cuda's take 0.06 us (instead of 1.1) and 0.12 (0.23); where a
+# build of torch has not got them, the public ones serve.
+_raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+               or (lambda index: torch.cuda.current_stream(index).cuda_stream))
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
 
 
 def _row_code(t, name):
