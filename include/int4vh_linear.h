@@ -19,7 +19,10 @@
  * on how the sum over k is split: a row gives the same bits alone and in a
  * batch.  The epilogue is binary32 in the order written, without fused
  * multiply-adds; the gelu as a whole is within (1.5 y^2 + 14) 2^-24 of its
- * value, in its lower tail too.  A row_scale that is NaN or infinite makes its row NaN.
+ * value, in its lower tail too, and the silu is -0 where exp(-y) overflows (y
+ * below -88.7).  A row_scale that is NaN makes its row NaN; an infinite one
+ * makes products infinite, and NaN where acc is 0, before the bias and the
+ * activation.
  *
  * Layout (device memory owned by the caller): codes int8 [M, K], rows
  * codes_stride elements apart, 16-byte aligned rows; row_scales float32 [M];
