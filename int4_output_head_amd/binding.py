@@ -123,6 +123,8 @@ def _raise(status: int, what: str):
     msg = L.verify_lm_head_int4_status_string(status).decode()
     if status == EHIP:
         msg += ": " + L.verify_lm_head_int4_last_error().decode()
+        # a workspace has to be initialised again after such an error
+        _ws_cache.clear()
     raise RuntimeError(f"{what}: {msg} (status {status})")
 
 

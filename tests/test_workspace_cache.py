@@ -53,3 +53,15 @@ def test_a_capture_leaves_nothing_for_eager_calls(state):
     g = binding._default_workspace(DEV, 100)
     state.capturing = False
     assert binding._default_workspace(DEV, 100) is not g
+
+
+def test_a_failed_launch_drops_the_shared_ones(state):
+    """A call of several kernels that fails between them leaves its control
+    words set: the next call has to get an initialised workspace."""
+    a = binding._default_workspace(DEV, 100)
+    with pytest.raises(RuntimeError):
+        binding._raise(binding.EINVAL, "call")
+    assert binding._default_workspace(DEV, 100) is a
+    with pytest.raises(RuntimeError):
+        binding._raise(binding.EHIP, "call")
+    assert binding._default_workspace(DEV, 100) is not a
