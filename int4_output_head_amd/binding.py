@@ -171,7 +171,7 @@ def _default_workspace(device, nbytes: int) -> Workspace:
     if _on(device.index, torch.cuda.is_current_stream_capturing):
         return Workspace(nbytes, device)
     # one per (device, current stream): calls on one stream are ordered
-    key = (device.index, torch.cuda.current_stream(device).cuda_stream)
+    key = (device.index, _raw_stream(device.index))
     ws = _ws_cache.get(key)
     if ws is None or ws.nbytes < nbytes:
         ws = Workspace(nbytes, device)

@@ -21,7 +21,7 @@ def state(monkeypatch):
     monkeypatch.setattr(binding, "Workspace", Made)
     monkeypatch.setattr(binding, "_ws_cache", {})
     monkeypatch.setattr(binding, "_current_device", lambda: 0)
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: types.SimpleNamespace(cuda_stream=s.stream))
+    monkeypatch.setattr(binding, "_raw_stream", lambda index: s.stream)
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: s.capturing)
     return s
 
