@@ -20,11 +20,12 @@
 // int8 tile.  Where a product has too few tiles to fill the card, its sum over
 // K is split and the int32 parts are added by linear_join_kernel.
 //
-// Measured (graph-timed): 4096 x 5120 x 8192 in 190 us, 1.8 POP/s, where a
-// library int8 product of 8192^3 reaches 2.1 on this card (counters: matrix
-// cores busy 48 % of the cycles, vector instructions 48 %, LDS 39 %, of its
-// cycles 1.4 % bank conflicts); 256 x 18992 x 5120 in 50 us (34, 38 and 41 %:
-// 596 tiles on 256 compute units); 16 x 5120 x 5120 in 9.4 us.
+// Measured (graph-timed, operands from HBM): 4096 x 5120 x 8192 in 190 us, 1.8
+// POP/s, where a library int8 product of 8192^3 reaches 2.1 on this card
+// (counters: matrix cores busy 48 % of the cycles, vector instructions 48 %, LDS
+// 39 %, of its cycles 1.4 % bank conflicts); 256 x 18992 x 5120 in 50 us (34, 38
+// and 41 %: 596 tiles on 256 compute units; 39 us where the operands stay in the
+// last-level cache); 16 x 5120 x 5120 in 9.4 us.
 #include <hip/hip_runtime.h>
 
 #include <cmath>

@@ -25,7 +25,7 @@
 // rules written out in 70 us (4.4 TB/s; a large copy reaches 4.7), without any
 // rule in 67; verified greedily in 44.5 us and with top-16 in 61.5, without
 // rules in 31 and 47.5 us (5.0 and 3.3 TB/s).  Of the 61.5 the penalties are 7,
-// the mask 2, the bias 1, the merge 5.6; vector instructions take 64 % of the busy
+// the mask 2, the bias 1, the merge 5.4; vector instructions take 62 % of the busy
 // cycles.  One request's 16 rows, top-16, with a history of 25000 tokens take
 // 25 us (with 1000: 20), the merge 7.7 of them.
 #include <hip/hip_runtime.h>

@@ -10,7 +10,8 @@
 // and the largest |t| of the row come out of one reduction, because t = (h *
 // weight) * channel_scale does not depend on rstd -- the factor rstd is common
 // to the row and goes into its scale alone.  Workgroups walk over rows with a
-// stride of the grid and keep their channels' weights.  (Two chunks of 8 per
+// stride of the grid and keep their channels' weights.  Rows whose squares
+// leave binary32 are summed a second time at another scale.  (Two chunks of 8 per
 // thread, half the waves: 47.3 us against 43.6 for 4096 x 8192 bfloat16 rows
 // with residual, graph-timed, and 5.1 against 3.9 for one row in 8 bits.)
 //
@@ -40,7 +41,8 @@ constexpr float kTinyPeak = 0x1p-100f;    // rows below it have no finite 127 / 
 // 8192 channels) or is below kLowMean, where squares get lost to subnormal
 // numbers, are summed once more at another scale: kDown, at which squares
 // reach 2^96 and their sum 2^109, or kUp, at which the smallest subnormal
-// number squares to 2^-118 and a sum stays below 2^113.
+// number squares to 2^-118 and a sum stays below 2^113.  Looking for them costs
+// 0.1 us at 16 rows of 5120 bfloat16 channels (3.7 us) and 0.3 at 1021 (10.0).
 constexpr float kLowMean = 0x1p-80f, kDown = 0x1p-80f, kUp = 0x1p90f;
 
 struct NormArgs {
