@@ -18,9 +18,10 @@
  * exact in 32 bits, so the results do not depend on the launch shape, on M or
  * on how the sum over k is split: a row gives the same bits alone and in a
  * batch.  The epilogue is binary32 in the order written, without fused
- * multiply-adds; the gelu as a whole is within (1.5 y^2 + 14) 2^-24 of its
- * value, in its lower tail too, and the silu is -0 where exp(-y) overflows (y
- * below -88.7).  A row_scale that is NaN makes its row NaN; an infinite one
+ * multiply-adds; the gelu as a whole has a relative error below (1.5 y^2 + 14)
+ * 2^-24, in its lower tail too (where exp(-y^2 / 2) is subnormal, an error below
+ * (|y| + 1) 2^-150 more), and the silu is -0 where exp(-y) overflows (y below
+ * -88.7).  A row_scale that is NaN makes its row NaN; an infinite one
  * makes products infinite, and NaN where acc is 0, before the bias and the
  * activation.
  *

@@ -148,8 +148,8 @@ class Workspace:
     """A device workspace for verify calls, initialised on creation.  Calls
     that share a Workspace must not be in flight at the same time, replays of
     graphs that were captured with it among them; a graph does not keep it
-    alive.  Calls without one use one per stream, or under capture one per
-    call, which is part of the graph."""
+    alive.  Calls without one use one per stream, or under torch's capture one
+    per call, which is part of the graph's memory."""
 
     def __init__(self, nbytes: int, device):
         self.nbytes = int(nbytes)
