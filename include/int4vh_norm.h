@@ -83,6 +83,41 @@ int rms_norm_rows_int8(const void *x, int64_t x_stride, const void *residual, in
 int quantize_rows_int8(const void *x, int64_t x_stride, int dtype, const void *channel_scales, int M, int H,
                        int8_t *codes, float *row_scales, void *stream);
 
+/* Between two blocks: the norm behind the first (post_weight, NULL for none),
+ * its gate and scale, the residual's addition, and the norm in front of the
+ * second (pre_weight) in one pass.  For each of M rows:
+ *
+ *   u[i]    = f32(x[i]) * rstd(x) * f32(post_weight[i])      (u = f32(x) without one)
+ *   v[i]    = u[i] * g(f32(gate[i]))                         (optional)
+ *   h[i]    = f32(residual[i]) + v[i] * scale
+ *   sum[i]  = h[i], rounded to the rows' type
+ *   out[i]  = h[i] * rstd(h) * f32(pre_weight[i]), rounded to out_dtype, or the
+ *             codes and row_scales of rms_norm_rows_int8
+ *
+ * with rstd as above, the products from left to right, and g(z) = z or 1 / (1 +
+ * exp(-z)).  gate: [H] of `dtype` (gate_stride 0), or rows of their own
+ * gate_stride >= H elements apart (also when M == 1).  Numerics, layout and
+ * errors as above, except that the residual and sum_out are required (sum_out
+ * may be x, residual or a gate of rows itself where those are contiguous), and
+ * out comes with pre_weight: both NULL write the sum alone.  INT4VH_EINVAL also for an
+ * unknown gate_activation, a gate_stride without a gate or below H other than
+ * 0, and a scale that is not finite. */
+enum {
+    INT4VH_GATE_NONE = 0,
+    INT4VH_GATE_SIGMOID = 1
+};
+
+int rms_norm_block_rows(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                        const void *gate, int64_t gate_stride, int gate_activation, int dtype,
+                        const void *post_weight, const void *pre_weight, int weight_dtype, float scale, int M, int H,
+                        float eps, void *sum_out, void *out, int out_dtype, void *stream);
+
+int rms_norm_block_rows_int8(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                             const void *gate, int64_t gate_stride, int gate_activation, int dtype,
+                             const void *post_weight, const void *pre_weight, int weight_dtype,
+                             const void *channel_scales, float scale, int M, int H, float eps, void *sum_out,
+                             int8_t *codes, float *row_scales, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -96,6 +96,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         L.rms_norm_rows_int8.restype = i32
         L.quantize_rows_int8.argtypes = [P, i64, i32, P, i32, i32, P, P, P]
         L.quantize_rows_int8.restype = i32
+        L.rms_norm_block_rows.argtypes = [P, i64, P, i64, P, i64, i32, i32, P, P, i32, f32, i32, i32, f32, P, P, i32,
+                                          P]
+        L.rms_norm_block_rows.restype = i32
+        L.rms_norm_block_rows_int8.argtypes = [P, i64, P, i64, P, i64, i32, i32, P, P, i32, P, f32, i32, i32, f32, P,
+                                               P, P, P]
+        L.rms_norm_block_rows_int8.restype = i32
         # linear layers on packed int4 weights (include/int4vh_linear.h)
         L.linear_int4_rows_workspace_bytes.argtypes = [i32, i32, i32]
         L.linear_int4_rows_workspace_bytes.restype = sz
@@ -795,6 +801,88 @@ def quantize_rows(x, *, channel_scales=None):
     if st != OK:
         _raise(st, "quantize_rows_int8")
     return codes, row_scales
+
+
+_GATES = {None: 0, "sigmoid": 1}
+
+
+def _block_args(x, residual, post_weight, pre_weight, gate, gate_activation):
+    """The leading arguments of both block norms, and (M, H, device index, sum)."""
+    dt = _row_code(x, "x")
+    M, H, xs = _rows2d(x, "x")
+    index = x.get_device()
+    if _row_code(residual, "residual") != dt or residual.shape != x.shape:
+        raise ValueError("residual must have the type and shape of x")
+    rs = _rows2d(residual, "residual")[2]
+    wdt = None
+    for w, name in ((post_weight, "post_weight"), (pre_weight, "pre_weight")):
+        if w is not None:
+            code = _row_code(w, name)
+            if w.shape != (H,) or not w.is_contiguous():
+                raise ValueError(f"{name} must be contiguous [H]")
+            if wdt is not None and wdt != code:
+                raise TypeError("post_weight and pre_weight must have one type")
+            wdt = code
+    act = _GATES.get(gate_activation)
+    if act is None:
+        raise ValueError("gate_activation must be None or 'sigmoid'")
+    gs = 0
+    if gate is not None:
+        if _row_code(gate, "gate") != dt:
+            raise TypeError("gate must have the type of x")
+        if gate.shape == x.shape and gate.dim() > 1:
+            gs = _rows2d(gate, "gate")[2]
+        elif gate.shape != (H,) or not gate.is_contiguous():
+            raise ValueError("gate must be contiguous [H], or of the shape of x")
+    elif act:
+        raise ValueError("gate_activation needs a gate")
+    _same_device(index, residual=residual, post_weight=post_weight, pre_weight=pre_weight, gate=gate)
+    total = torch.empty_like(x, memory_format=torch.contiguous_format)
+    return ((x.data_ptr(), xs, residual.data_ptr(), rs, _at(gate), gs, act, dt, _at(post_weight), _at(pre_weight),
+             wdt or 0), M, H, index, total)
+
+
+def rms_norm_block(x, residual, post_weight=None, pre_weight=None, *, gate=None, gate_activation=None,
+                   scale: float = 1.0, eps: float = 1e-6, out_dtype=torch.float16):
+    """Between two blocks, in one pass: the norm behind the first (post_weight
+    [H], or None), its gate and scale, the residual's addition, and the norm in
+    front of the second (pre_weight [H], or None):
+    sum = residual + x * rstd(x) * post_weight * gate * scale, normed = sum *
+    rstd(sum) * pre_weight (from the sum before it is rounded).  x and residual
+    [..., H] as in rms_norm; gate: [H], or of the shape of x; gate_activation:
+    None or "sigmoid".  Returns (normed of out_dtype, sum in x's type); normed
+    is None without pre_weight."""
+    args, M, H, index, total = _block_args(x, residual, post_weight, pre_weight, gate, gate_activation)
+    odt = _ROW_DTYPES.get(out_dtype)
+    if odt is None:
+        raise TypeError("out_dtype must be float16, bfloat16 or float32")
+    out = None if pre_weight is None else x.new_empty(x.shape, dtype=out_dtype)
+    st = _on(index, load_library().rms_norm_block_rows, *args, scale, M, H, eps, total.data_ptr(), _at(out), odt,
+             _raw_stream(index))
+    if st != OK:
+        _raise(st, "rms_norm_block_rows")
+    return out, total
+
+
+def rms_norm_block_int8(x, residual, post_weight, pre_weight, *, gate=None, gate_activation=None, scale: float = 1.0,
+                        channel_scales=None, eps: float = 1e-6):
+    """rms_norm_block with its output in 8 bits, as rms_norm_int8 gives it:
+    (codes int8 [..., H], row_scales float32 [M], sum)."""
+    if pre_weight is None:
+        raise ValueError("pre_weight is required")
+    args, M, H, index, total = _block_args(x, residual, post_weight, pre_weight, gate, gate_activation)
+    cs = None
+    if channel_scales is not None:
+        _vector(channel_scales, "channel_scales", torch.float16, H)
+        _same_device(index, channel_scales=channel_scales)
+        cs = channel_scales.data_ptr()
+    codes = x.new_empty(x.shape, dtype=torch.int8)
+    row_scales = x.new_empty(M, dtype=torch.float32)
+    st = _on(index, load_library().rms_norm_block_rows_int8, *args, cs, scale, M, H, eps, total.data_ptr(),
+             codes.data_ptr(), row_scales.data_ptr(), _raw_stream(index))
+    if st != OK:
+        _raise(st, "rms_norm_block_rows_int8")
+    return codes, row_scales, total
 
 
 # ---------------------------------------------------------------- linear layers on packed int4 weights

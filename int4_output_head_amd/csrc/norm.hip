@@ -432,6 +432,217 @@ int launch(const NormArgs &a, int dtype, hipStream_t s)
     return launch_rows<INT4VH_ROWS_F32, kInt8, kNorm>(a, s);
 }
 
+struct BlockArgs {
+    const void *x, *residual, *gate;   // gate: null, [H] (gate_stride 0) or rows
+    long long x_stride, residual_stride, gate_stride;
+    const void *post, *pre;    // [H] of weight_dtype, either may be null
+    const uint16_t *channel;   // binary16 [H], or null
+    void *sum_out;
+    void *out;                 // [M, H] of out_dtype, with pre
+    int8_t *codes;             // [M, H] (8 bits)
+    float *row_scales;         // [M]
+    int M, H;
+    int weight_dtype, out_dtype;
+    int gate_activation;
+    float scale, eps;
+};
+
+__device__ __forceinline__ void gate_values(float (&g)[8], int activation)
+{
+    if (activation == INT4VH_GATE_SIGMOID)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            g[j] = 1.0f / (1.0f + expf(-g[j]));
+}
+
+// The norm behind a block, its gate and scale, the residual's addition and the
+// next block's norm: norm_rows_kernel with a second reduction in front.  The
+// block's output is normed in registers, so that the row is still read and
+// written once; the two reductions have LDS of their own and a barrier each.
+template <int kDtype, bool kInt8>
+__global__ void __launch_bounds__(kMaxThreads) norm_block_kernel(BlockArgs a)
+{
+    __shared__ float s_post[2][kMaxThreads / 64];
+    __shared__ float s_sum[2][kMaxThreads / 64];
+    __shared__ uint32_t s_peak[2][kMaxThreads / 64];
+    __shared__ float s_again[2][kMaxThreads / 64];
+    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 63, wave = tid >> 6, n_waves = nt >> 6;
+    const int H = a.H;
+    constexpr size_t kSize = kDtype == INT4VH_ROWS_F32 ? 4 : 2;
+    const size_t out_size = a.out_dtype == INT4VH_ROWS_F32 ? 4 : 2;
+
+    const int c = 8 * tid;                     // this thread's first channel
+    float post[8], pre[8], gate[8], cs[8];
+    if (a.post)
+        load8_any(a.post, a.weight_dtype, c, H, post);
+    if (a.pre)
+        load8_any(a.pre, a.weight_dtype, c, H, pre);
+    if (a.gate && a.gate_stride == 0) {
+        load8<kDtype>(a.gate, c, H, gate);
+        gate_values(gate, a.gate_activation);
+    }
+    if (kInt8) {
+        if (a.channel) {
+            load8<INT4VH_ROWS_F16>(a.channel, c, H, cs);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                cs[j] = 1.0f;
+        }
+    }
+    // sums of squares that serve as they are
+    const float low_sum = a.eps < kLowMean ? kLowMean * (float)H : 0.0f;
+    const float high_sum = a.eps < 0x1p126f ? 0x1p127f : 0.0f;
+
+    // The factor 1 / rms of values v from the sum of their squares, and the
+    // power of two `behind` that goes with it; where the squares leave binary32
+    // v is scaled and they are summed again.  Whole workgroup.
+    auto factor = [&](float (&v)[8], float ss, float *s_more, float &before, float &behind) {
+        float eps = a.eps;
+        before = behind = 1.0f;
+        if (__builtin_expect(__builtin_amdgcn_readfirstlane(ss < low_sum || ss > high_sum), false)) {
+            const bool low = ss < low_sum;
+            const float f = low ? kUp : kDown;
+            ss = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                ss = __builtin_fmaf(v[j] * f, v[j] * f, ss);
+            uint32_t none = 0u;
+            reduce<64, true, false>(ss, none);
+            if (n_waves > 1) {
+                if (lane == 0)
+                    s_more[wave] = ss;
+                __syncthreads();
+                ss = (lane & 15) < n_waves ? s_more[lane & 15] : 0.0f;
+                reduce<16, true, false>(ss, none);
+            }
+            eps = eps * f * f;
+            before = low ? f : 1.0f;
+            behind = low ? 1.0f : f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] *= before;
+        }
+        return 1.0f / sqrtf(ss / (float)H + eps);
+    };
+
+    int buf = 0;
+    for (unsigned m = blockIdx.x; m < (unsigned)a.M; m += gridDim.x, buf ^= 1) {
+        float u[8], h[8];
+        load8<kDtype>(static_cast<const char *>(a.x) + (size_t)m * a.x_stride * kSize, c, H, u);
+        load8<kDtype>(static_cast<const char *>(a.residual) + (size_t)m * a.residual_stride * kSize, c, H, h);
+        if (a.gate_stride)
+            load8<kDtype>(static_cast<const char *>(a.gate) + (size_t)m * a.gate_stride * kSize, c, H, gate);
+        float before, behind;
+        uint32_t none = 0u;
+        if (a.post) {
+            float ss = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                ss = __builtin_fmaf(u[j], u[j], ss);
+            reduce<64, true, false>(ss, none);
+            if (n_waves > 1) {
+                if (lane == 0)
+                    s_post[buf][wave] = ss;
+                __syncthreads();               // the other half of the array is the next row's
+                ss = (lane & 15) < n_waves ? s_post[buf][lane & 15] : 0.0f;
+                reduce<16, true, false>(ss, none);
+            }
+            const float rstd = factor(u, ss, s_again[0], before, behind);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                u[j] = u[j] * rstd * behind * post[j];
+        }
+        if (a.gate_stride)
+            gate_values(gate, a.gate_activation);
+        if (a.gate)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                u[j] *= gate[j];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            h[j] += u[j] * a.scale;
+        store8(static_cast<char *>(a.sum_out) + (size_t)m * H * kSize, kDtype, c, H, h);
+        if (!a.pre)
+            continue;
+
+        float t[8];                            // what 8 bits stand for, up to rstd
+        float ss = 0.0f;
+        uint32_t peak = 0u;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            // channels past H hold 0 here: x, the residual and the gate do
+            ss = __builtin_fmaf(h[j], h[j], ss);
+            if (kInt8) {
+                t[j] = h[j] * pre[j] * cs[j];
+                const uint32_t w = __float_as_uint(t[j]) & 0x7FFFFFFFu;
+                peak = w > peak ? w : peak;
+            }
+        }
+        reduce<64, true, kInt8>(ss, peak);
+        if (n_waves > 1) {
+            if (lane == 0) {
+                s_sum[buf][wave] = ss;
+                s_peak[buf][wave] = peak;
+            }
+            __syncthreads();
+            const int i = lane & 15;
+            ss = i < n_waves ? s_sum[buf][i] : 0.0f;
+            peak = i < n_waves ? s_peak[buf][i] : 0u;
+            reduce<16, true, kInt8>(ss, peak);
+        }
+        if (kInt8) {
+            const float pk = __uint_as_float(peak);
+            const bool tiny = pk < kTinyPeak, live = !tiny && peak < 0x7F800000u;
+            const float inv = 127.0f / pk;
+            int q[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                q[j] = live ? (int)rintf(t[j] * inv) : 0;
+            store_codes8(a.codes + (size_t)m * H, c, H, q);
+            const float rstd = factor(h, ss, s_again[1], before, behind);
+            if (tid == 0) {
+                float top = pk * rstd;
+                if (before != 1.0f || behind != 1.0f)  // exact in binary64, then the product's one rounding
+                    top = (float)((double)pk * rstd * before * behind);
+                a.row_scales[m] = tiny ? 0.0f : top / 127.0f;
+            }
+        } else {
+            const float rstd = factor(h, ss, s_again[1], before, behind);
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                y[j] = h[j] * rstd * behind * pre[j];
+            store8(static_cast<char *>(a.out) + (size_t)m * H * out_size, a.out_dtype, c, H, y);
+        }
+    }
+}
+
+template <int kDtype, bool kInt8>
+int launch_block_rows(const BlockArgs &a, hipStream_t s)
+{
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess)
+        return hip_fail(e, "hipGetDevice");
+    const int nt = (a.H + 511) / 512 * 64;
+    const int resident = cu_count(dev) * (2048 / nt);
+    const int grid = a.M < resident ? a.M : resident;
+    hipLaunchKernelGGL((norm_block_kernel<kDtype, kInt8>), dim3(grid), dim3(nt), 0, s, a);
+    e = hipGetLastError();
+    return e == hipSuccess ? INT4VH_OK : hip_fail(e, "block norm kernel launch");
+}
+
+template <bool kInt8>
+int launch_block(const BlockArgs &a, int dtype, hipStream_t s)
+{
+    if (dtype == INT4VH_ROWS_F16)
+        return launch_block_rows<INT4VH_ROWS_F16, kInt8>(a, s);
+    if (dtype == INT4VH_ROWS_BF16)
+        return launch_block_rows<INT4VH_ROWS_BF16, kInt8>(a, s);
+    return launch_block_rows<INT4VH_ROWS_F32, kInt8>(a, s);
+}
+
 // What every entry point checks of its rows.
 int check_rows(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride, int dtype, int M, int H,
                const void *sum_out, int max_h)
@@ -443,6 +654,26 @@ int check_rows(const void *x, int64_t x_stride, const void *residual, int64_t re
     if (!rows_aligned(x, rows_size(dtype)) || !rows_aligned(residual, rows_size(dtype)) || !rows_aligned(sum_out, rows_size(dtype)))
         return INT4VH_EALIGN;
     return H > max_h ? INT4VH_EUNSUPPORTED : INT4VH_OK;
+}
+
+// What both block norms check.
+int check_block(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride, const void *gate,
+                int64_t gate_stride, int gate_activation, int dtype, const void *post, const void *pre,
+                int weight_dtype, float scale, int M, int H, float eps, const void *sum_out)
+{
+    if (!residual || !sum_out || !rows_known(weight_dtype) || !(eps >= 0.0f) || !std::isfinite(eps) || !std::isfinite(scale))
+        return INT4VH_EINVAL;
+    if (gate_activation != INT4VH_GATE_NONE && gate_activation != INT4VH_GATE_SIGMOID)
+        return INT4VH_EINVAL;
+    if (gate ? gate_stride != 0 && gate_stride < H : gate_stride != 0)
+        return INT4VH_EINVAL;
+    const int st = check_rows(x, x_stride, residual, residual_stride, dtype, M, H, sum_out, INT4VH_MAX_H);
+    if (st == INT4VH_EINVAL)
+        return st;
+    if (!rows_aligned(gate, rows_size(dtype)) || !rows_aligned(post, rows_size(weight_dtype)) ||
+        !rows_aligned(pre, rows_size(weight_dtype)))
+        return INT4VH_EALIGN;
+    return st;
 }
 
 } // namespace
@@ -508,6 +739,49 @@ int quantize_rows_int8(const void *x, int64_t x_stride, int dtype, const void *c
     if (dtype == INT4VH_ROWS_F16)
         return launch_long_rows<INT4VH_ROWS_F16>(a, s);
     return dtype == INT4VH_ROWS_BF16 ? launch_long_rows<INT4VH_ROWS_BF16>(a, s) : launch_long_rows<INT4VH_ROWS_F32>(a, s);
+}
+
+int rms_norm_block_rows(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                        const void *gate, int64_t gate_stride, int gate_activation, int dtype,
+                        const void *post_weight, const void *pre_weight, int weight_dtype, float scale, int M, int H,
+                        float eps, void *sum_out, void *out, int out_dtype, void *stream)
+{
+    if (!rows_known(out_dtype) || (pre_weight == nullptr) != (out == nullptr))
+        return INT4VH_EINVAL;
+    const int st = check_block(x, x_stride, residual, residual_stride, gate, gate_stride, gate_activation, dtype,
+                               post_weight, pre_weight, weight_dtype, scale, M, H, eps, sum_out);
+    if (st == INT4VH_EINVAL)
+        return st;
+    if (!rows_aligned(out, rows_size(out_dtype)))
+        return INT4VH_EALIGN;
+    if (st != INT4VH_OK)
+        return st;
+    const BlockArgs a = {x,       residual,    gate, x_stride, residual_stride, gate_stride,  post_weight, pre_weight,
+                         nullptr, sum_out,     out,  nullptr,  nullptr,         M,            H,           weight_dtype,
+                         out_dtype, gate_activation, scale, eps};
+    return launch_block<false>(a, dtype, static_cast<hipStream_t>(stream));
+}
+
+int rms_norm_block_rows_int8(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                             const void *gate, int64_t gate_stride, int gate_activation, int dtype,
+                             const void *post_weight, const void *pre_weight, int weight_dtype,
+                             const void *channel_scales, float scale, int M, int H, float eps, void *sum_out,
+                             int8_t *codes, float *row_scales, void *stream)
+{
+    if (!pre_weight || !codes || !row_scales)
+        return INT4VH_EINVAL;
+    const int st = check_block(x, x_stride, residual, residual_stride, gate, gate_stride, gate_activation, dtype,
+                               post_weight, pre_weight, weight_dtype, scale, M, H, eps, sum_out);
+    if (st == INT4VH_EINVAL)
+        return st;
+    if (!rows_aligned(channel_scales, 2) || !rows_aligned(row_scales, 4))
+        return INT4VH_EALIGN;
+    if (st != INT4VH_OK)
+        return st;
+    const BlockArgs a = {x, residual, gate, x_stride, residual_stride, gate_stride, post_weight, pre_weight,
+                         static_cast<const uint16_t *>(channel_scales), sum_out, nullptr, codes, row_scales, M, H,
+                         weight_dtype, INT4VH_ROWS_F16, gate_activation, scale, eps};
+    return launch_block<true>(a, dtype, static_cast<hipStream_t>(stream));
 }
 
 } // extern "C"

@@ -81,3 +81,15 @@ def linear64(codes, row_scales, packed, out_scales=None, bias=None, activation=N
     if residual is not None:
         z = z + np.asarray(residual, np.float64)
     return z, y, s
+
+
+def block64(x, residual, post_weight=None, gate=None, gate_activation=None, scale=1.0, eps=1e-6):
+    """(h, the gated and scaled output v of the block) with h = residual + v."""
+    u = np.asarray(x, np.float64)
+    if post_weight is not None:
+        u = u * rstd64(u, eps) * np.asarray(post_weight, np.float64)
+    if gate is not None:
+        z = np.asarray(gate, np.float64)
+        u = u * (1.0 / (1.0 + np.exp(-z)) if gate_activation == "sigmoid" else z)
+    v = u * float(scale)
+    return np.asarray(residual, np.float64) + v, v
