@@ -107,6 +107,15 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         L.linear_int4_rows_workspace_bytes.restype = sz
         L.linear_int4_rows.argtypes = [P, i64, P, P, P, P, i32, P, i64, i32, i32, i32, P, i64, i32, P, sz, P]
         L.linear_int4_rows.restype = i32
+        # 4-bit floating point (include/int4vh_mxfp4.h)
+        L.quantize_rows_mxfp4.argtypes = [P, i64, i32, i32, i32, P, P, P]
+        L.quantize_rows_mxfp4.restype = i32
+        L.dequantize_rows_mxfp4.argtypes = [P, P, i32, i32, P, i32, P]
+        L.dequantize_rows_mxfp4.restype = i32
+        L.linear_mxfp4_rows_workspace_bytes.argtypes = [i32, i32, i32]
+        L.linear_mxfp4_rows_workspace_bytes.restype = sz
+        L.linear_mxfp4_rows.argtypes = [P, P, P, P, P, i32, P, i64, i32, i32, i32, P, i64, i32, P, sz, P]
+        L.linear_mxfp4_rows.restype = i32
         # rules on logits (include/int4vh_logits.h)
         L.logit_rules_apply.argtypes = [P, i64, i32, P, i32, i32, i32, P, P, i64, P]
         L.logit_rules_apply.restype = i32
@@ -952,6 +961,118 @@ def _launch_linear(index, codes, cs, row_scales, packed_w, out_scales, bias, act
 
 def _at(t):
     return None if t is None else t.data_ptr()
+
+
+# ---------------------------------------------------------------- 4-bit floating point
+
+def quantize_mxfp4(x):
+    """Rows x [..., H] (float16, bfloat16 or float32; H a multiple of 32 up to
+    65536) in microscaled 4-bit floating point, one power of two for 32
+    channels: activations and weights of linear_mxfp4 alike.  Returns (codes
+    uint8 [..., H/2], the even channel in the low half of a byte, and scales
+    uint8 [..., H/32], exponents + 127)."""
+    dt = _row_code(x, "x")
+    M, H, xs = _rows2d(x, "x")
+    if H % 32:
+        raise ValueError("the channels of x must be a multiple of 32")
+    index = x.get_device()
+    lead = x.shape[:-1]
+    codes = x.new_empty(lead + (H // 2,), dtype=torch.uint8)
+    scales = x.new_empty(lead + (H // 32,), dtype=torch.uint8)
+    st = _on(index, load_library().quantize_rows_mxfp4, x.data_ptr(), xs, dt, M, H, codes.data_ptr(),
+             scales.data_ptr(), _raw_stream(index))
+    if st != OK:
+        _raise(st, "quantize_rows_mxfp4")
+    return codes, scales
+
+
+def _mx_rows(codes, scales, names=("codes", "scales")):
+    """(M, K) of a matrix in 4-bit floating point."""
+    for t, name in ((codes, names[0]), (scales, names[1])):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.uint8:
+            raise TypeError(f"{name} must be a CUDA (HIP) uint8 tensor")
+        if not t.dim() or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous rows")
+    K = 2 * codes.shape[-1]
+    if K < 32 or K % 32 or scales.shape != codes.shape[:-1] + (K // 32,):
+        raise ValueError(f"{names[1]} must hold one byte for 32 channels of {names[0]}")
+    M = codes.numel() // (K // 2)
+    if M < 1 or M > 0x7FFFFFFF:
+        raise ValueError(f"{names[0]} must have between 1 and 2^31 - 1 rows")
+    return M, K
+
+
+def dequantize_mxfp4(codes, scales, *, out_dtype=torch.float16):
+    """The values of rows in 4-bit floating point (quantize_mxfp4): codes
+    [..., H/2], scales [..., H/32] -> [..., H] of out_dtype."""
+    M, H = _mx_rows(codes, scales)
+    dt = _ROW_DTYPES.get(out_dtype)
+    if dt is None:
+        raise TypeError("out_dtype must be float16, bfloat16 or float32")
+    index = codes.get_device()
+    if scales.get_device() != index:
+        _same_device(index, scales=scales)
+    out = codes.new_empty(codes.shape[:-1] + (H,), dtype=out_dtype)
+    st = _on(index, load_library().dequantize_rows_mxfp4, codes.data_ptr(), scales.data_ptr(), M, H, out.data_ptr(),
+             dt, _raw_stream(index))
+    if st != OK:
+        _raise(st, "dequantize_rows_mxfp4")
+    return out
+
+
+def linear_mxfp4_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(load_library().linear_mxfp4_rows_workspace_bytes(M, N, K))
+
+
+def linear_mxfp4(codes, scales, w_codes, w_scales, *, bias=None, activation=None, residual=None,
+                 out_dtype=torch.float16, out=None):
+    """Linear layer between two matrices in 4-bit floating point
+    (quantize_mxfp4): rows codes [..., K/2], scales [..., K/32] and weights
+    w_codes [N, K/2], w_scales [N, K/32]: activation(x @ w.T + bias) +
+    residual.  bias [N] and residual [..., N] of out_dtype; activation: None,
+    "relu", "gelu" or "silu".  out: the [..., N] tensor to write, which may be
+    residual itself.  Returns it."""
+    M, K = _mx_rows(codes, scales)
+    if w_codes.dim() != 2:
+        raise ValueError("w_codes must be [N, K/2]")
+    N, wk = _mx_rows(w_codes, w_scales, ("w_codes", "w_scales"))
+    if wk != K:
+        raise ValueError("shape mismatch between codes and w_codes")
+    dt = _ROW_DTYPES.get(out_dtype)
+    if dt is None:
+        raise TypeError("out_dtype must be float16, bfloat16 or float32")
+    act = _ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError("activation must be None, 'relu', 'gelu' or 'silu'")
+    if bias is not None:
+        _vector(bias, "bias", out_dtype, N)
+    index = codes.get_device()
+    rs, os_ = 0, N
+    shape = codes.shape[:-1] + (N,)
+    if residual is not None:
+        if _row_code(residual, "residual") != dt or residual.shape != shape:
+            raise ValueError("residual must be [..., N] of out_dtype")
+        rs = _rows2d(residual, "residual")[2]
+    if out is None:
+        out = codes.new_empty(shape, dtype=out_dtype)
+    else:
+        if _row_code(out, "out") != dt or out.shape != shape:
+            raise ValueError("out must be [..., N] of out_dtype")
+        os_ = _rows2d(out, "out")[2]
+    _same_device(index, scales=scales, w_codes=w_codes, w_scales=w_scales, bias=bias, residual=residual, out=out)
+    st = _on(index, _launch_linear_mxfp4, index, codes, scales.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
+             _at(bias), act, _at(residual), rs, M, N, K, out.data_ptr(), os_, dt)
+    if st != OK:
+        _raise(st, "linear_mxfp4_rows")
+    return out
+
+
+def _launch_linear_mxfp4(index, codes, scales, w_codes, w_scales, bias, act, residual, rs, M, N, K, out, os_, dt):
+    L = load_library()
+    need = L.linear_mxfp4_rows_workspace_bytes(M, N, K)
+    ws = codes.new_empty(need) if need else None
+    return L.linear_mxfp4_rows(codes.data_ptr(), scales, w_codes, w_scales, bias, act, residual, rs, M, N, K, out, os_,
+                               dt, _at(ws), need, _raw_stream(index))
 
 
 # ---------------------------------------------------------------- rules on logits
