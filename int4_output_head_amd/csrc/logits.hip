@@ -36,6 +36,7 @@
 #include "int4vh.h"
 #include "int4vh_internal.h"
 #include "int4vh_logits.h"
+#include "logits_common.h"
 #include "rows_common.h"
 
 #pragma clang fp contract(off)
@@ -44,134 +45,21 @@ namespace {
 
 using namespace int4vh_detail;
 
-typedef unsigned long long u64;
-
-constexpr int kChunk = 1024;              // tokens of a row that a wave holds at a time
-constexpr int kPer = kChunk / 64;         // tokens per lane, 64 apart
-constexpr int kMaxWaves = 8;
-constexpr int kMaxSlice = kMaxWaves * kChunk;   // tokens of a workgroup's slice
 constexpr int kMaxTopK = 16;
-constexpr int kMaxRows = 4096;
 constexpr int kBuf = 128;                 // candidate keys per wave
-constexpr float kNegInf = -__builtin_huge_valf();
 
-// A token's word in LDS: times generated, whether it is in the prompt, and the
-// number of its last bias entry (from 1; 0: none).  Where a call's histories
-// and biases are short enough all three share 32 bits, which halves the LDS of
-// a slice (three workgroups a compute unit instead of two); otherwise entries
-// have words of their own.
-struct WordLayout {
-    uint32_t count, seen;     // bits
-    int entry_shift;          // of the entry in a shared word; 0: not shared
-};
-constexpr WordLayout kShared = {(1u << 20) - 1u, 1u << 20, 21};
-constexpr WordLayout kApart = {0x7FFFFFFFu, 0x80000000u, 0};
-constexpr long long kSharedHistory = (1ll << 20) - 32;   // generated tokens, drafts on top
-constexpr long long kSharedEntries = (1 << 11) - 1;
-constexpr long long kMaxHistory = (1ll << 31) - 1 - INT4VH_MAX_T, kMaxEntries = (1ll << 31) - 1;   // kApart's
-
-struct RulesArgs {
-    const void *logits;
-    long long logits_stride;
-    const int32_t *draft;      // [R, T-1] or null
-    int R, T, V;
-    int4vh_logit_rules r;      // zeros for none
-    int has_penalty, has_bias;
-    WordLayout word;
-    int row_group;             // rows per workgroup
-    int ways;                  // waves per row
-    int slice;                 // tokens per workgroup: a multiple of ways * kChunk
+struct RowsArgs : RulesArgs {
     // apply
     void *out;
     long long out_stride;
     // verify
-    int top_k, n_lists;
+    int top_k;
     float lse_scale;           // log2(e) / temperature
     u64 *lists;                // [R*T, n_lists, max(top_k, 1)] best keys of each wave's tokens, best first, 0 past the last
     u64 *heads;                // [R*T, n_lists] the lists' first keys (top_k >= 1)
     float2 *sums;              // [R*T, n_lists] (max, sum of exp2((x - max) * lse_scale))
     float *draft_logit;        // [R*T] ruled logit of the row's draft, where it is in [0, V)
 };
-
-// Key of a (value, token) pair whose unsigned order is: larger value, then
-// lower token.  -0 is keyed as +0; key 0 is below every pair's.
-__device__ __forceinline__ uint32_t order_word(float v)
-{
-    const uint32_t u = __float_as_uint(v + 0.0f);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ u64 order_key(float v, int token)
-{
-    return ((u64)order_word(v) << 32) | (u64)(~(uint32_t)token);
-}
-__device__ __forceinline__ float word_value(uint32_t u)
-{
-    return __uint_as_float((u & 0x80000000u) ? (u & 0x7FFFFFFFu) : ~u);
-}
-__device__ __forceinline__ float key_value(u64 k)
-{
-    return word_value((uint32_t)(k >> 32));
-}
-__device__ __forceinline__ int key_token(u64 k)
-{
-    return (int)(~(uint32_t)k);
-}
-
-__device__ __forceinline__ u64 shfl_xor64(u64 k, int mask)
-{
-    const uint32_t lo = __shfl_xor((uint32_t)k, mask), hi = __shfl_xor((uint32_t)(k >> 32), mask);
-    return ((u64)hi << 32) | lo;
-}
-__device__ __forceinline__ u64 wave_max64(u64 k)
-{
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
-        const u64 o = shfl_xor64(k, off);
-        k = o > k ? o : k;
-    }
-    return k;
-}
-__device__ __forceinline__ float wave_max(float v)
-{
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1)
-        v = fmaxf(v, __shfl_xor(v, off));
-    return v;
-}
-__device__ __forceinline__ float wave_sum(float v)
-{
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1)
-        v += __shfl_xor(v, off);
-    return v;
-}
-
-// exp2((x - m) * scale) of a value at most m; 1 at the maximum itself, so that
-// infinities do not meet, and 0 for -infinity and NaN.
-__device__ __forceinline__ float exp2_below(float x, float m, float scale)
-{
-    return x == m ? 1.0f : x > kNegInf ? exp2f((x - m) * scale) : 0.0f;
-}
-
-// LDS written and read by one wave alone: its accesses execute in order, so
-// only the compiler has to be held back.
-__device__ __forceinline__ void wave_fence()
-{
-    __builtin_amdgcn_wave_barrier();
-    asm volatile("" ::: "memory");
-}
-
-__device__ __forceinline__ u64 readlane64(u64 k, int src)
-{
-    return (u64)(uint32_t)__builtin_amdgcn_readlane((uint32_t)(k >> 32), src) << 32 |
-           (uint32_t)__builtin_amdgcn_readlane((uint32_t)k, src);
-}
-
-// The number of lanes of m below this one.
-__device__ __forceinline__ int lane_rank(u64 m)
-{
-    return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
-}
 
 // Keeps the k best of the n (<= kBuf) distinct keys buf[0, n), best first, and
 // returns how many there are (min(n, k)).  A key's rank is the number of
@@ -266,232 +154,20 @@ __device__ __forceinline__ void push_some(u64 *buf, int &n, const u64 (&key)[kN]
     }
 }
 
-// A word th (at least 1) that at least k lanes' words reach, and where it can
-// be no more than k + 8; 1 where fewer than k lanes have a word, since then
-// lower values of the same lanes are wanted too.  Two bits at a time are set
-// from the top while enough lanes still reach the word.
-__device__ __forceinline__ uint32_t reach_threshold(uint32_t word, int k)
-{
-    uint32_t th = 0u;
-    if (__popcll(__ballot(word != 0u)) < k)
-        return 1u;
-#pragma nounroll
-    for (int shift = 30; shift >= 0; shift -= 2) {
-        const int c1 = __popcll(__ballot(word >= (th | 1u << shift)));
-        const int c2 = __popcll(__ballot(word >= (th | 2u << shift)));
-        const int c3 = __popcll(__ballot(word >= (th | 3u << shift)));
-        const uint32_t bits = c3 >= k ? 3u : c2 >= k ? 2u : c1 >= k ? 1u : 0u;
-        const int c = c3 >= k ? c3 : c2 >= k ? c2 : c1;
-        th |= bits << shift;
-        if (bits && c <= k + 8)
-            break;
-    }
-    return th ? th : 1u;
-}
-
-// Logit `token` of a row.
-template <int kDtype>
-__device__ __forceinline__ float load_logit(const void *row, int token)
-{
-    if constexpr (kDtype == INT4VH_ROWS_F32)
-        return static_cast<const float *>(row)[token];
-    else
-        return from_bits16(static_cast<const uint16_t *>(row)[token], kDtype);
-}
-
-template <int kDtype>
-__device__ __forceinline__ void store_logit(void *row, int token, float v)
-{
-    if constexpr (kDtype == INT4VH_ROWS_F32)
-        static_cast<float *>(row)[token] = v;
-    else
-        static_cast<uint16_t *>(row)[token] = (uint16_t)to_bits16(v, kDtype);
-}
-
-__device__ __forceinline__ long long clamp64(long long v, long long lo, long long hi)
-{
-    return v < lo ? lo : v > hi ? hi : v;
-}
-
-// A request's part of the histories (generated from `made` on) and of the bias
-// entries.
-struct Spans {
-    long long hb, he, made, bb, be;
-};
-__device__ __forceinline__ Spans load_spans(const RulesArgs &a, int req)
-{
-    Spans s = {0, 0, 0, 0, 0};
-    if (a.has_penalty && a.r.history) {
-        const long long b = a.r.history_offsets[req], e = a.r.history_offsets[req + 1];
-        const int prompt = a.r.n_prompt ? a.r.n_prompt[req] : 0;
-        s.hb = clamp64(b, 0, a.r.n_history);
-        s.he = clamp64(e, 0, a.r.n_history);
-        s.made = s.hb + prompt;
-    }
-    if (a.has_bias) {
-        const long long b = a.r.bias_offsets[req], e = a.r.bias_offsets[req + 1];
-        s.bb = clamp64(b, 0, a.r.n_bias);
-        s.be = clamp64(e, 0, a.r.n_bias);
-    }
-    return s;
-}
-
-// The slice's tokens in one request's history and biases: the words of tokens
-// base .. base + S - 1, and the entries' where they lie apart.  Called by the
-// whole workgroup, which waits at the end.
-__device__ __forceinline__ void prepare_slice(const RulesArgs &a, const Spans &span, int base, int S, uint32_t *words,
-                                              uint32_t *entries)
-{
-    const int tid = threadIdx.x, nt = blockDim.x;
-    const long long hb = span.hb, he = span.he, made = span.made, bb = span.bb, be = span.be;
-    // Four tokens a load, kFly loads in flight per thread; loads past the end
-    // take the last four tokens instead, whose earlier ones are not theirs.
-    constexpr int kFly = 4;
-    const bool few = he - hb < 4;
-    Words4 v[kFly];
-    auto load = [&](long long i0) {
-        if (few)
-            return;
-#pragma unroll
-        for (int u = 0; u < kFly; ++u) {
-            const long long i = i0 + 4ll * u * nt;
-            v[u] = *reinterpret_cast<const Words4 *>(a.r.history + (i < he - 4 ? i : he - 4));
-        }
-    };
-    load(hb + 4 * tid);
-    int32_t id = -1;
-    if (bb + tid < be)
-        id = a.r.bias_ids[bb + tid];
-    const int n_words = entries == words ? S : 2 * S;
-    uint4 *clear = reinterpret_cast<uint4 *>(words);
-    for (int i = tid; i < n_words / 4; i += nt)
-        clear[i] = make_uint4(0u, 0u, 0u, 0u);
-    __syncthreads();
-    if (a.has_bias) {
-        for (long long i = bb + tid; i < be; i += nt) {
-            if (i != bb + tid)
-                id = a.r.bias_ids[i];
-            const uint32_t at = (uint32_t)id - (uint32_t)base;
-            if (id >= 0 && at < (uint32_t)S)
-                atomicMax(&entries[at], ((uint32_t)(i - bb) + 1u) << a.word.entry_shift);
-        }
-        if (entries == words)
-            __syncthreads();                  // the maxima are taken before anything is added to them
-    }
-    auto count = [&](int32_t token, bool prompt) {
-        const uint32_t at = (uint32_t)token - (uint32_t)base;
-        if (token >= 0 && at < (uint32_t)S) {
-            if (prompt)
-                atomicOr(&words[at], a.word.seen);
-            else
-                atomicAdd(&words[at], 1u);
-        }
-    };
-    if (few) {
-        if (hb + tid < he)
-            count(a.r.history[hb + tid], hb + tid < made);
-    } else {
-        for (long long i0 = hb + 4 * tid; i0 < he; i0 += 4ll * nt * kFly) {
-            if (i0 != hb + 4 * tid)
-                load(i0);
-#pragma unroll
-            for (int u = 0; u < kFly; ++u) {
-                const long long i = i0 + 4ll * u * nt, from = i < he - 4 ? i : he - 4;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (from + j >= i)
-                        count((int32_t)v[u].w[j], from + j < made);
-            }
-        }
-    }
-    __syncthreads();
-}
-
-__device__ __forceinline__ float penalise(float l, uint32_t count, float rep, float freq, float pres)
-{
-    const float x = l > 0.0f ? l / rep : l * rep;
-    // tokens of the prompt alone keep x, whatever the other two are (an
-    // infinite frequency times a count of 0 would be NaN)
-    return count ? x - freq * (float)count - pres : x;
-}
-
-// Grid (slices of the vocabulary, requests, row groups); wave w takes row w /
-// ways of the group and the (w % ways)-th part of the slice.  kVerify: reduce
-// the rows; otherwise write them out.
+// The rows under the rules (SliceWalk).  kVerify: reduce the rows; otherwise
+// write them out.
 template <int kDtype, bool kVerify, bool kTopK, bool kLse>
-__global__ void __launch_bounds__(64 * kMaxWaves) rules_kernel(RulesArgs a)
+__global__ void __launch_bounds__(64 * kMaxWaves) rules_kernel(RowsArgs a)
 {
     extern __shared__ __attribute__((aligned(16))) uint32_t s_mem[];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int S = a.slice, V = a.V;
-    uint32_t *words = s_mem;
-    uint32_t *entries = s_mem + (a.has_penalty && a.has_bias && !a.word.entry_shift ? S : 0);
-    u64 *buf = reinterpret_cast<u64 *>(entries + (a.has_penalty || a.has_bias ? S : 0)) + wave * kBuf;
-    const int base = blockIdx.x * S;
-    const int req = blockIdx.y;
-    const int t = blockIdx.z * a.row_group + wave / a.ways, way = wave % a.ways;
-    const int part = S / a.ways, begin = base + way * part;        // this wave's tokens
-    const int n_chunks = begin < V ? (min(part, V - begin) + kChunk - 1) / kChunk : 0;
-    const int row = req * a.T + min(t, a.T - 1);
-    constexpr size_t kSize = kDtype == INT4VH_ROWS_F32 ? 4 : 2;
-    const char *lrow = static_cast<const char *>(a.logits) + (size_t)row * a.logits_stride * kSize;
-
-    // A chunk's logits, and its mask in the lanes below 32, a word each.
-    // Tokens past V load the row's last one and are struck out below.
-    struct Held {
-        float x[kPer];
-        uint32_t bits;
-    };
-    const uint32_t last = (uint32_t)(V - 1) * (uint32_t)kSize;
-    auto load_x = [&](int c, Held &h) {
-        const int t0 = begin + min(c, n_chunks - 1) * kChunk;
-        const uint32_t at = (uint32_t)(t0 + lane) * (uint32_t)kSize;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            h.x[i] = load_logit<kDtype>(lrow + min(at + (uint32_t)(64 * kSize) * i, last), 0);
-    };
-    Held ha, hb;
-    ha.bits = hb.bits = 0u;
-    if (n_chunks > 0)
-        load_x(0, ha);                        // on its way while the slice is counted
-    const Spans span = load_spans(a, req);
-    const uint32_t *mask = nullptr;
-    bool none = false;                        // nothing is allowed
-    if (a.r.mask) {
-        const long long mi = a.r.mask_index ? a.r.mask_index[row] : row;
-        none = mi >= a.r.n_masks;
-        if (mi >= 0 && !none)
-            mask = a.r.mask + (size_t)mi * a.r.mask_stride;
-    }
-    const int mask_words = (V + 31) / 32;
-
-    auto load_bits = [&](int c, Held &h) {
-        if (mask)
-            h.bits = mask[min(((begin + min(c, n_chunks - 1) * kChunk) >> 5) + (lane & 31), mask_words - 1)];
-    };
-    if (n_chunks > 0)
-        load_bits(0, ha);
-    auto load = [&](int c, Held &h) {
-        load_x(c, h);
-        load_bits(c, h);
-    };
-
-    if (a.has_penalty || a.has_bias)
-        prepare_slice(a, span, base, S, words, entries);
-    if (t >= a.T || t >= (int)(blockIdx.z + 1) * a.row_group)
+    SliceWalk<kDtype> walk(a, s_mem);
+    if (!walk.live())
         return;                               // no barrier follows
-
-    const float rep = a.r.repetition ? a.r.repetition[req] : 1.0f;
-    const float freq = a.r.frequency ? a.r.frequency[req] : 0.0f;
-    const float pres = a.r.presence ? a.r.presence[req] : 0.0f;
-    const float *bias = a.has_bias ? a.r.bias_values + span.bb : nullptr;
-    // lane j holds draft j, for the rows behind it; the row's own draft
-    int mine = -1, d = -1;
-    if (a.T > 1) {
-        const int32_t *dr = a.draft + (size_t)req * (a.T - 1);
-        mine = lane < t ? dr[lane] : -1;
-        d = t < a.T - 1 ? dr[t] : -1;
-    }
+    walk.load_request();
+    const int lane = walk.lane, row = walk.row, way = walk.way, d = walk.d, V = a.V;
+    constexpr size_t kSize = SliceWalk<kDtype>::kSize;
+    u64 *buf = reinterpret_cast<u64 *>(walk.entries + (a.has_penalty || a.has_bias ? a.slice : 0)) +
+               __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * kBuf;
 
     int n = 0;                                // keys in buf
     float above = kNegInf;                    // once k keys are held: a value has to be at least this
@@ -499,60 +175,7 @@ __global__ void __launch_bounds__(64 * kMaxWaves) rules_kernel(RulesArgs a)
     int bt = -1;
     float lm = kNegInf, ls = 0.0f;            // this lane's (max, sum)
 
-    auto process = [&](int c, Held &held) {
-        float (&x)[kPer] = held.x;
-        const int chunk0 = begin + c * kChunk;
-        const int at0 = chunk0 - base + lane;
-        if (a.has_penalty || a.has_bias) {
-            uint32_t w[kPer];
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                w[i] = words[at0 + 64 * i];
-            if (a.has_penalty) {
-                // the drafts in front of this row that lie in the chunk
-                for (u64 m = __ballot(mine >= 0 && (uint32_t)(mine - chunk0) < (uint32_t)kChunk); m; m &= m - 1) {
-                    const int at = __builtin_amdgcn_readlane(mine, __builtin_ctzll(m)) - chunk0 - lane;
-#pragma unroll
-                    for (int i = 0; i < kPer; ++i)
-                        w[i] += at == 64 * i ? 1u : 0u;
-                }
-            }
-            const uint32_t known = a.has_penalty ? a.word.count | a.word.seen : 0u;
-            const bool here = a.has_bias && entries == words;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (__ballot(w[i] != 0u)) {   // few groups of 64 tokens have any
-                    if (w[i] & known)
-                        x[i] = penalise(x[i], w[i] & a.word.count, rep, freq, pres);
-                    const uint32_t e = here ? w[i] >> a.word.entry_shift : 0u;
-                    if (e)
-                        x[i] = x[i] + bias[e - 1u];
-                }
-        }
-        if (a.has_bias && entries != words) {
-            uint32_t e[kPer];
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                e[i] = entries[at0 + 64 * i];
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (e[i])
-                    x[i] = x[i] + bias[e[i] - 1u];
-        }
-        if (mask || none) {
-            const uint32_t bits = none ? 0u : held.bits;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const u64 allowed = (u64)__builtin_amdgcn_readlane(bits, 2 * i + 1) << 32 |
-                                    (uint32_t)__builtin_amdgcn_readlane(bits, 2 * i);
-                x[i] = __builtin_amdgcn_inverse_ballot_w64(allowed) ? x[i] : kNegInf;
-            }
-        }
-        if (chunk0 + kChunk > V)
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                x[i] = chunk0 + 64 * i + lane < V ? x[i] : kNegInf;
-
+    walk.run([&](int chunk0, float (&x)[kPer]) {
         if constexpr (!kVerify) {
             char *orow = static_cast<char *>(a.out) + (size_t)row * a.out_stride * kSize;
 #pragma unroll
@@ -640,15 +263,7 @@ __global__ void __launch_bounds__(64 * kMaxWaves) rules_kernel(RulesArgs a)
             if ((int)(da & 63u) == lane)
                 a.draft_logit[row] = v;
         }
-    };
-    for (int c = 0; c < n_chunks; c += 2) {
-        load(c + 1, hb);
-        process(c, ha);
-        if (c + 1 < n_chunks) {
-            load(c + 2, ha);
-            process(c + 1, hb);
-        }
-    }
+    });
 
     if constexpr (kVerify) {
         const size_t slot = (size_t)row * a.n_lists + blockIdx.x * a.ways + way;
@@ -852,11 +467,6 @@ struct Layout {
     size_t lists, heads, sums, draft_logit, bytes;
 };
 
-size_t round256(size_t n)
-{
-    return (n + 255) / 256 * 256;
-}
-
 Layout layout_for(int R, int T, int V, int top_k)
 {
     Layout l;
@@ -871,109 +481,14 @@ Layout layout_for(int R, int T, int V, int top_k)
     return l;
 }
 
-bool sizes_ok(int R, int T, int V)
-{
-    return R >= 1 && T >= 1 && T <= INT4VH_MAX_T && V >= 1 && (long long)R * T <= kMaxRows;
-}
-
-constexpr int kMaxV = 1 << 24;
-
-int check(const void *logits, int64_t stride, int dtype, const int32_t *draft, int R, int T, int V,
-          const int4vh_logit_rules *r)
-{
-    if (!sizes_ok(R, T, V) || !rows_known(dtype) || !logits || (T > 1 && !draft))
-        return INT4VH_EINVAL;
-    if (R * T > 1 && stride < V)
-        return INT4VH_EINVAL;
-    if (r) {
-        if (r->n_history < 0 || r->n_bias < 0 || (r->n_history > 0 && !r->history) || (r->history && !r->history_offsets))
-            return INT4VH_EINVAL;
-        if (r->bias_ids && (!r->bias_values || !r->bias_offsets))
-            return INT4VH_EINVAL;
-        if (r->n_bias > 0 && !r->bias_ids)
-            return INT4VH_EINVAL;
-        if (r->mask && (r->n_masks < 1 || r->mask_stride < (V + 31) / 32 || (!r->mask_index && r->n_masks < R * T)))
-            return INT4VH_EINVAL;
-        if (!r->mask && r->mask_index)
-            return INT4VH_EINVAL;
-    }
-    if (!rows_aligned(logits, rows_size(dtype)) || !rows_aligned(draft, 4))
-        return INT4VH_EALIGN;
-    if (r && (!rows_aligned(r->history, 4) || !rows_aligned(r->history_offsets, 8) || !rows_aligned(r->n_prompt, 4) ||
-              !rows_aligned(r->repetition, 4) || !rows_aligned(r->frequency, 4) || !rows_aligned(r->presence, 4) ||
-              !rows_aligned(r->bias_ids, 4) || !rows_aligned(r->bias_values, 4) || !rows_aligned(r->bias_offsets, 8) ||
-              !rows_aligned(r->mask, 4) || !rows_aligned(r->mask_index, 4)))
-        return INT4VH_EALIGN;
-    if (r && (r->n_history > kMaxHistory || r->n_bias > kMaxEntries))
-        return INT4VH_EUNSUPPORTED;
-    return V > kMaxV ? INT4VH_EUNSUPPORTED : INT4VH_OK;
-}
-
-void fill_rules(RulesArgs &a, const int4vh_logit_rules *r, int T)
-{
-    a.r = r ? *r : int4vh_logit_rules{};
-    const bool any = a.r.repetition || a.r.frequency || a.r.presence;
-    a.has_penalty = any && (a.r.history || T > 1);
-    a.has_bias = a.r.bias_ids != nullptr;
-    // words are shared where both are there; alone, either has the plain ones
-    a.word = a.has_penalty && a.has_bias && a.r.n_history <= kSharedHistory && a.r.n_bias <= kSharedEntries ? kShared
-                                                                                                         : kApart;
-}
-
-struct Shape {
-    dim3 grid, block;
-    size_t lds;
-};
-
-// Slices as long as kMaxSlice spread the counting and a wave's threshold over
-// many tokens; shorter ones where there would be fewer than two workgroups a
-// compute unit (151936 logits, top-16: 16 requests x 4 rows 29.8 us against
-// 34.3 with a target of half a workgroup a unit, 4 x 4 17.3 against 20.5, one
-// request's 16 rows 25.3 against 27.7).  A wave has kChunk tokens of a row at
-// least.
-Shape shape_for(RulesArgs &a, bool topk, int cus)
-{
-    const int chunks = (a.V + kChunk - 1) / kChunk;
-    a.row_group = a.T < kMaxWaves ? a.T : kMaxWaves;
-    a.ways = kMaxWaves / a.row_group;
-    while (a.ways > chunks)
-        --a.ways;
-    const int groups = (a.T + a.row_group - 1) / a.row_group;
-    int per = kMaxWaves / a.ways;             // chunks per wave
-    while (per > 1 && (long long)((chunks + per * a.ways - 1) / (per * a.ways)) * a.R * groups < 2ll * cus)
-        per /= 2;
-    while (per > 1 && (per / 2) * a.ways >= chunks)
-        per /= 2;                             // no longer than the vocabulary
-    a.slice = per * a.ways * kChunk;
-    const int slices = (a.V + a.slice - 1) / a.slice;
-    a.n_lists = slices * a.ways;
-    const int waves = a.row_group * a.ways;
-    Shape s;
-    s.grid = dim3(slices, a.R, groups);
-    s.block = dim3(64 * waves);
-    const int arrays = a.word.entry_shift ? 1 : (a.has_penalty ? 1 : 0) + (a.has_bias ? 1 : 0);
-    s.lds = (size_t)a.slice * 4 * arrays + (topk ? (size_t)waves * kBuf * 8 : 0);
-    return s;
-}
-
 template <bool kVerify, bool kTopK, bool kLse>
-hipError_t launch_rules(const RulesArgs &a, int dtype, const Shape &sh, hipStream_t s)
+hipError_t launch_rules(const RowsArgs &a, int dtype, const Shape &sh, hipStream_t s)
 {
-    void (*k)(RulesArgs) = dtype == INT4VH_ROWS_F32   ? rules_kernel<INT4VH_ROWS_F32, kVerify, kTopK, kLse>
+    void (*k)(RowsArgs) = dtype == INT4VH_ROWS_F32   ? rules_kernel<INT4VH_ROWS_F32, kVerify, kTopK, kLse>
                            : dtype == INT4VH_ROWS_F16 ? rules_kernel<INT4VH_ROWS_F16, kVerify, kTopK, kLse>
                                                       : rules_kernel<INT4VH_ROWS_BF16, kVerify, kTopK, kLse>;
     hipLaunchKernelGGL(k, sh.grid, sh.block, sh.lds, s, a);
     return hipGetLastError();
-}
-
-int current_cus(int *cus)
-{
-    int dev = 0;
-    const hipError_t e = hipGetDevice(&dev);
-    if (e != hipSuccess)
-        return hip_fail(e, "hipGetDevice");
-    *cus = cu_count(dev);
-    return INT4VH_OK;
 }
 
 int check_verify(const float *draft_probs, const float *uniforms, int T, int V, int top_k, float temperature,
@@ -1002,7 +517,7 @@ int logit_rules_apply(const void *logits, int64_t logits_stride, int dtype, cons
 {
     if (!out || (sizes_ok(R, T, V) && R * T > 1 && out_stride < V))
         return INT4VH_EINVAL;
-    int st = check(logits, logits_stride, dtype, draft_ids, R, T, V, rules);
+    int st = check_rules(logits, logits_stride, dtype, draft_ids, R, T, V, rules);
     if (st != INT4VH_OK)
         return st;
     if (!rows_aligned(out, rows_size(dtype)))
@@ -1010,7 +525,7 @@ int logit_rules_apply(const void *logits, int64_t logits_stride, int dtype, cons
     int cus = 0;
     if ((st = current_cus(&cus)) != INT4VH_OK)
         return st;
-    RulesArgs a = {};
+    RowsArgs a = {};
     a.logits = logits;
     a.logits_stride = logits_stride;
     a.draft = draft_ids;
@@ -1020,7 +535,7 @@ int logit_rules_apply(const void *logits, int64_t logits_stride, int dtype, cons
     a.out = out;
     a.out_stride = out_stride;
     fill_rules(a, rules, T);
-    const Shape sh = shape_for(a, false, cus);
+    const Shape sh = shape_for(a, 0, cus);
     const hipError_t e = launch_rules<false, false, false>(a, dtype, sh, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? INT4VH_OK : hip_fail(e, "rules kernel launch");
 }
@@ -1038,7 +553,7 @@ int logit_rules_verify(const void *logits, int64_t logits_stride, int dtype, con
                        int32_t *argmax_ids, int32_t *topk_ids, float *topk_logits, float *lse, float *p_draft,
                        int32_t *n_accepted, void *workspace, size_t workspace_bytes, void *stream)
 {
-    int st = check(logits, logits_stride, dtype, draft_ids, R, T, V, rules);
+    int st = check_rules(logits, logits_stride, dtype, draft_ids, R, T, V, rules);
     if (st == INT4VH_EINVAL)
         return st;
     const int sv = check_verify(draft_probs, uniforms, T, V, top_k, temperature, logits_max, argmax_ids, topk_ids,
@@ -1061,7 +576,7 @@ int logit_rules_verify(const void *logits, int64_t logits_stride, int dtype, con
     char *ws = static_cast<char *>(workspace);
     const bool sampled = T > 1 && draft_probs;
     const bool want_lse = lse || (sampled && top_k == 0);
-    RulesArgs a = {};
+    RowsArgs a = {};
     a.logits = logits;
     a.logits_stride = logits_stride;
     a.draft = draft_ids;
@@ -1075,7 +590,7 @@ int logit_rules_verify(const void *logits, int64_t logits_stride, int dtype, con
     a.heads = reinterpret_cast<u64 *>(ws + l.heads);
     a.sums = reinterpret_cast<float2 *>(ws + l.sums);
     a.draft_logit = reinterpret_cast<float *>(ws + l.draft_logit);
-    const Shape sh = shape_for(a, top_k > 0, cus);
+    const Shape sh = shape_for(a, top_k > 0 ? kBuf * 8 : 0, cus);
     const hipStream_t s = static_cast<hipStream_t>(stream);
     hipError_t e;
     if (top_k)
@@ -1139,7 +654,7 @@ int verify_lm_head_int4_ruled(const void *hidden, const uint8_t *packed_w, const
         return INT4VH_EINVAL;
     // what the second half would refuse is refused before the first is launched
     char *ws = static_cast<char *>(workspace);
-    int st = check(ws, V, INT4VH_ROWS_F32, draft_ids, R, T, V, rules);
+    int st = check_rules(ws, V, INT4VH_ROWS_F32, draft_ids, R, T, V, rules);
     if (st == INT4VH_EINVAL)
         return st;
     const int sv = check_verify(draft_probs, uniforms, T, V, top_k, temperature, logits_max, argmax_ids, topk_ids,
