@@ -10,7 +10,8 @@ __all__ = ["verify", "verify_batch", "verify_batch_noalloc", "verify_mapped", "v
            "requant_amax", "requant_scales", "requant_pack", "requantize", "context_copy", "stream_read",
            "rms_norm", "rms_norm_int8", "rms_norm_block", "rms_norm_block_int8", "quantize_rows", "linear_int4", "linear_workspace_bytes",
            "quantize_mxfp4", "dequantize_mxfp4", "linear_mxfp4", "linear_mxfp4_workspace_bytes",
-           "LogitRules", "apply_logit_rules", "verify_logits", "verify_ruled"]
+           "LogitRules", "apply_logit_rules", "verify_logits", "verify_ruled",
+           "sample_logits", "sample_workspace_bytes"]
 
 
 def __getattr__(name):

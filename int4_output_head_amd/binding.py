@@ -129,6 +129,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         L.verify_lm_head_int4_ruled.argtypes = [P, P, P, P, P, P, i32, i32, i32, i32, P, i32, f32, P, P, P, P, P,
                                                 P, P, P, sz, P]
         L.verify_lm_head_int4_ruled.restype = i32
+        # tokens drawn from logits (include/int4vh_sample.h)
+        L.sample_logits_workspace_bytes.argtypes = [i32, i32, i32]
+        L.sample_logits_workspace_bytes.restype = sz
+        L.sample_logits_rows.argtypes = [P, i64, i32, P, i32, i32, i32, P, P, P, P, P, P, P, P, P, sz, P]
+        L.sample_logits_rows.restype = i32
         _lib = L
         return L
 
@@ -1326,3 +1331,79 @@ def verify_ruled(hidden, packed_w, scales, rules, draft_ids=None, draft_probs=No
     if st != OK:
         _raise(st, "verify_lm_head_int4_ruled")
     return out
+
+
+# ---------------------------------------------------------------- sampling
+
+_SAMPLING = struct.Struct("@PPPPfiff")     # int4vh_sampling
+
+
+def sample_workspace_bytes(R: int, T: int, V: int) -> int:
+    return int(load_library().sample_logits_workspace_bytes(R, T, V))
+
+
+def _setting(v, name, dtype, R, index):
+    """(device address or 0, scalar) of a setting: a number, or a tensor [R]."""
+    if isinstance(v, torch.Tensor):
+        if v.dtype != dtype or not v.is_cuda or v.shape != (R,) or not v.is_contiguous():
+            _vector(v, name, dtype, R)
+        if v.get_device() != index:
+            _same_device(index, **{name: v})
+        return v.data_ptr(), 0
+    return 0, v
+
+
+def sample_logits(logits, uniforms, rules=None, draft_ids=None, *, R: int | None = None, temperature=1.0, top_k=0,
+                  top_p=1.0, min_p=0.0, accept=None):
+    """A token of every row of logits [R, T, V] (or [R*T, V] with R; float32,
+    float16 or bfloat16), drawn by uniforms (float32, R*T numbers in [0, 1)) at
+    a temperature among the top_k best (0: all), of these the best that hold
+    top_p of the mass, and of these those with at least min_p of the best one's
+    mass, under rules (LogitRules, or None; draft_ids int32 [R, T-1] when T >
+    1, as in verify_logits).  temperature, top_p, min_p: numbers, or float32
+    [R], and top_k a number, or int32 [R], a value per request; a temperature of 0
+    takes the best token.  With accept (float32 [R, T-1], the drafts' own uniform
+    numbers) the drafts are verified as point masses: a draft is accepted where
+    accept < p_draft, and the tokens of rows with a draft are drawn from the
+    others, so that row n_accepted's is the token behind the accepted drafts.
+    Returns (token_ids int32 [R*T], -1 for a row that has none, token_probs
+    float32 [R*T], p_draft [R, T-1], n_accepted int32 [R]); the last two are
+    None without accept."""
+    code, stride, R, T, V = _logit_rows(logits, R)
+    index = logits.get_device()
+    if rules is not None:
+        rules.check(index, R, T, V)
+    dr = _drafts(index, R, T, draft_ids)[0]
+    M = R * T
+    if not isinstance(uniforms, torch.Tensor) or uniforms.dtype != torch.float32 or not uniforms.is_cuda:
+        _check(uniforms, "uniforms", torch.float32)
+    if uniforms.numel() != M or not uniforms.is_contiguous():
+        raise ValueError("uniforms must be contiguous and hold R*T values")
+    if uniforms.get_device() != index:
+        _same_device(index, uniforms=uniforms)
+    f, i = torch.float32, torch.int32
+    (pt, t), (pk, k), (pp, p), (pm, m) = (_setting(temperature, "temperature", f, R, index),
+                                          _setting(top_k, "top_k", i, R, index), _setting(top_p, "top_p", f, R, index),
+                                          _setting(min_p, "min_p", f, R, index))
+    if not isinstance(k, int):
+        raise TypeError("top_k must be a whole number or an int32 tensor")
+    settings = _SAMPLING.pack(pt, pk, pp, pm, t, min(max(k, -1), V), p, m)
+    new = logits.new_empty
+    ids, probs = new(M, dtype=i), new(M, dtype=f)
+    ac = pdr = nacc = None
+    if accept is not None:
+        if T == 1:
+            raise ValueError("accept needs drafts")
+        ac = _drafted(accept, "accept", f, R * (T - 1), index)
+        pdr, nacc = new((R, T - 1), dtype=f), new(R, dtype=i)
+    L = load_library()
+    need = L.sample_logits_workspace_bytes(R, T, V)
+    if need == 0:
+        _raise(EINVAL, "sample_logits_rows")
+    ws = new(need, dtype=torch.uint8)
+    st = _on(index, L.sample_logits_rows, logits.data_ptr(), stride, code, dr, R, T, V,
+             None if rules is None else rules.packed, settings, uniforms.data_ptr(), ac, ids.data_ptr(),
+             probs.data_ptr(), _at(pdr), _at(nacc), ws.data_ptr(), need, _raw_stream(index))
+    if st != OK:
+        _raise(st, "sample_logits_rows")
+    return ids, probs, pdr, nacc

@@ -8,7 +8,7 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = ("int4vh.hip", "requant.hip", "context_copy.hip", "stream_probe.hip", "norm.hip", "linear.hip",
-           "logits.hip", "mxfp4.hip")
+           "logits.hip", "mxfp4.hip", "sample.hip")
 SRCS = [os.path.join(HERE, "csrc", f) for f in SOURCES]
 OUT = os.path.join(HERE, "libint4vh.so")
 INCLUDE = os.path.join(ROOT, "include")

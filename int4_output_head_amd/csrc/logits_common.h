@@ -284,9 +284,9 @@ __device__ __forceinline__ float penalise(float l, uint32_t count, float rep, fl
     return count ? x - freq * (float)count - pres : x;
 }
 
-// A wave's walk over its part of a slice: wave w of a workgroup takes row w /
-// ways of the group and the (w % ways)-th part of the slice.  Grid (slices of
-// the vocabulary, requests, row groups).
+// A wave's walk over its part of a slice.  In a grid of (slices of the
+// vocabulary, requests, row groups) wave w of a workgroup takes row w / ways of
+// the group and the (w % ways)-th part of the slice.
 template <int kDtype>
 struct SliceWalk {
     static constexpr size_t kSize = kDtype == INT4VH_ROWS_F32 ? 4 : 2;
@@ -331,21 +331,31 @@ struct SliceWalk {
         load_bits(c, h);
     }
 
-    // s_mem: the slice's words, then its entries where they lie apart.  The
-    // whole workgroup counts the slice, whose first chunks are on their way
-    // meanwhile.
-    __device__ __forceinline__ SliceWalk(const RulesArgs &args, uint32_t *s_mem) : a(args)
+    // This wave's place in the grid.
+    __device__ __forceinline__ SliceWalk(const RulesArgs &args, uint32_t *s_mem)
+        : SliceWalk(args, s_mem, blockIdx.x * args.slice, args.slice, blockIdx.y,
+                    blockIdx.z * args.row_group + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / args.ways,
+                    __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % args.ways, args.ways)
+    {
+    }
+
+    // Part way_at of n_ways of the S tokens from `first` on, in row t_at of
+    // request req_at.  s_mem: the slice's words, then its entries where they lie
+    // apart.  The whole workgroup counts the slice, whose first chunks are on
+    // their way meanwhile.
+    __device__ __forceinline__ SliceWalk(const RulesArgs &args, uint32_t *s_mem, int first, int S, int req_at,
+                                         int t_at, int way_at, int n_ways)
+        : a(args)
     {
         lane = threadIdx.x & 63;
-        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        const int S = a.slice, V = a.V;
+        const int V = a.V;
         words = s_mem;
         entries = s_mem + (a.has_penalty && a.has_bias && !a.word.entry_shift ? S : 0);
-        base = blockIdx.x * S;
-        req = blockIdx.y;
-        t = blockIdx.z * a.row_group + wave / a.ways;
-        way = wave % a.ways;
-        const int part = S / a.ways;
+        base = first;
+        req = req_at;
+        t = t_at;
+        way = way_at;
+        const int part = S / n_ways;
         begin = base + way * part;
         n_chunks = begin < V ? (min(part, V - begin) + kChunk - 1) / kChunk : 0;
         row = req * a.T + min(t, a.T - 1);

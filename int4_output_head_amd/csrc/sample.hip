@@ -1,0 +1,721 @@
+// sample.hip -- tokens drawn from logits by given uniform numbers, for MI355X
+// (gfx950); definitions in int4vh_sample.h.
+//
+// Two kernels.  sample_scan_kernel walks the rows as the verification under
+// rules does (SliceWalk: the logits are read once, under their rules) and
+// leaves of each row either the sums of its chunks of 1024 tokens, or the
+// candidates that a filter may keep, or both.  What can be kept is bounded from
+// what a wave has seen: a value that lies more than temperature * ln(1 / min_p)
+// below its largest one has too little mass; under top_p, one that lies more
+// than temperature * ln(V / (1 - top_p)) below, because all tokens behind it
+// together would have less than 1 - top_p of the best one's mass; under top_k
+// up to 64, one below the k-th of the 64 lanes' largest values.
+// sample_draw_kernel, a workgroup per row, joins these: the borders of top_k
+// and top_p are found by histograms of counts and masses over the keys' range,
+// refined around the border, and the token by a sum over tokens in their order.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <stdint.h>
+
+#include "int4vh.h"
+#include "int4vh_internal.h"
+#include "int4vh_sample.h"
+#include "logits_common.h"
+#include "rows_common.h"
+
+#pragma clang fp contract(off)
+
+namespace {
+
+using namespace int4vh_detail;
+
+constexpr int kDrawThreads = 1024;
+constexpr int kCap = 8192;                // candidates that the drawing kernel holds in LDS
+constexpr int kBins = kDrawThreads;
+
+struct SampleArgs : RulesArgs {
+    int4vh_sampling s;
+    const float *uniforms;     // [R*T]
+    const float *accept;       // [R, T-1] or null
+    int bits;                  // masses are multiples of 2^-bits
+    u64 *cand;                 // [R*T, V] candidates' keys; a list begins at its wave's first token
+    int *counts;               // [R*T, n_lists + 1] candidates of each list, then where it begins
+    float *tops;               // [R*T, n_lists] largest value of each wave's tokens
+    double *sums;              // [R*T, chunks] mass of each chunk, less the row's draft where drafts are verified
+    float *maxes;              // [R*T, chunks] what it is relative to: the largest value
+    float *draft_logit;        // [R*T] ruled logit of the row's draft, where it is in [0, V)
+    uint32_t *tickets;         // [R] rows done
+    uint32_t *oks;             // [R*T] whether the row's draft is accepted
+    int32_t *token_ids;
+    float *token_probs, *p_draft;
+    int32_t *n_accepted;
+};
+
+// A request's settings: k = 0, p = 1 and mp = 0 keep all.
+struct Settings {
+    double inv_t;
+    float t;
+    int k;
+    float p, mp;
+    __device__ __forceinline__ bool filtered() const { return k > 0 || p < 1.0f || mp > 0.0f; }
+    // whether the sums of the chunks are wanted
+    __device__ __forceinline__ bool summed() const { return k == 0 && (p < 1.0f || mp <= 0.0f); }
+};
+__device__ __forceinline__ Settings load_settings(const SampleArgs &a, int req)
+{
+    Settings s;
+    s.t = a.s.temperatures ? a.s.temperatures[req] : a.s.temperature;
+    s.k = a.s.top_ks ? a.s.top_ks[req] : a.s.top_k;
+    s.p = a.s.top_ps ? a.s.top_ps[req] : a.s.top_p;
+    s.mp = a.s.min_ps ? a.s.min_ps[req] : a.s.min_p;
+    s.k = s.k <= 0 || s.k >= a.V ? 0 : s.k;
+    s.p = s.p < 1.0f ? fmaxf(s.p, 0.0f) : 1.0f;
+    s.mp = s.mp > 0.0f ? fminf(s.mp, 1.0f) : 0.0f;
+    if (!(s.t > 0.0f && s.t < __builtin_huge_valf())) {
+        s.t = 0.0f;
+        s.k = 1;
+        s.p = 1.0f;
+        s.mp = 0.0f;
+    }
+    s.inv_t = s.t > 0.0f ? 1.0 / (double)s.t : 0.0;
+    return s;
+}
+
+// The mass of a value x at most m, relative to that of m; 1 at m itself, so that
+// infinities do not meet, and 0 for -infinity and NaN.
+__device__ __forceinline__ double mass_below(float x, float m, double inv_t)
+{
+    return x == m ? 1.0 : x > kNegInf ? exp(((double)x - (double)m) * inv_t) : 0.0;
+}
+
+__device__ __forceinline__ double wave_sum_f64(double v)
+{
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1)
+        v += __shfl_xor(v, off);
+    return v;
+}
+
+template <int kDtype>
+__global__ void __launch_bounds__(64 * kMaxWaves) sample_scan_kernel(SampleArgs a)
+{
+    extern __shared__ __attribute__((aligned(16))) uint32_t s_mem[];
+    SliceWalk<kDtype> walk(a, s_mem);
+    if (blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0)
+        a.tickets[blockIdx.y] = 0u;
+    if (!walk.live())
+        return;                               // no barrier follows
+    walk.load_request();
+    const int lane = walk.lane, row = walk.row, d = walk.d, V = a.V;
+    const Settings set = load_settings(a, walk.req);
+    const bool filtered = set.filtered(), summed = set.summed();
+    const int n_all = (V + kChunk - 1) / kChunk;
+    // how far below the largest value a candidate may lie; slack for this
+    // bound's own roundings
+    float reach = __builtin_huge_valf();
+    if (set.t == 0.0f) {
+        reach = 0.0f;
+    } else {
+        if (set.mp > 0.0f && (set.k == 0 || set.p >= 1.0f))
+            reach = -set.t * logf(set.mp);
+        if (set.p < 1.0f && set.k == 0)
+            reach = fminf(reach, set.t * logf((float)V / (1.0f - set.p)));
+        reach = reach * (1.0f + 0x1p-18f) + set.t * 0x1p-18f;
+    }
+    u64 *list = a.cand + (size_t)row * V + walk.begin;
+    int n = 0;                                // candidates written
+    float top = kNegInf;                      // this lane's largest value
+    float from = -3.402823466e38f;            // candidates are at least this
+    walk.run([&](int chunk0, float (&x)[kPer]) {
+        float best = kNegInf;                 // fmaxf passes over NaN
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            best = fmaxf(best, x[i]);
+        const bool more = best > top;
+        top = fmaxf(top, best);
+        if (filtered && __ballot(best >= from)) {
+            if (__ballot(more)) {
+                const float m = wave_max(top);
+                const float bar = m - reach - fabsf(m) * 0x1p-20f;
+                from = bar > from ? bar : m == __builtin_huge_valf() && reach < m ? m : from;
+                if (set.k > 0 && set.k <= 64) {
+                    const uint32_t th = reach_threshold(top > kNegInf ? order_word(top) : 0u, set.k);
+                    if (th > 1u)
+                        from = fmaxf(from, word_value(th));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const u64 m = __ballot(x[i] >= from);
+                if (m) {
+                    if (x[i] >= from)
+                        list[n + lane_rank(m)] = order_key(x[i], chunk0 + 64 * i + lane);
+                    n += __popcll(m);
+                }
+            }
+        }
+        const uint32_t da = (uint32_t)d - (uint32_t)chunk0;
+        if (d >= 0 && d < V && da < (uint32_t)kChunk) {
+            float v = kNegInf;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const bool own = (int)(da >> 6) == i && (int)(da & 63u) == lane;
+                v = own ? x[i] : v;
+                if (a.accept && own)
+                    x[i] = kNegInf;           // apart from the sums
+            }
+            if ((int)(da & 63u) == lane)
+                a.draft_logit[row] = v;
+            best = kNegInf;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                best = fmaxf(best, x[i]);
+        }
+        if (summed) {
+            const float m = wave_max(best);
+            double s = 0.0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                s += mass_below(x[i], m, set.inv_t);
+            s = wave_sum_f64(s);
+            if (lane == 0) {
+                a.maxes[(size_t)row * n_all + chunk0 / kChunk] = m;
+                a.sums[(size_t)row * n_all + chunk0 / kChunk] = m > kNegInf ? s : 0.0;
+            }
+        }
+    });
+    const float m = wave_max(top);
+    if (lane == 0) {
+        const size_t slot = (size_t)row * a.n_lists + blockIdx.x * a.ways + walk.way;
+        a.counts[slot + row] = n;
+        a.tops[slot] = m;
+    }
+}
+
+// ---------------------------------------------------------------- drawing
+
+// Reductions and scans over the workgroup; all threads, `s` of 16 values per
+// use, free again after the next barrier.
+__device__ __forceinline__ float block_max(float v, float *s)
+{
+    v = wave_max(v);
+    if ((threadIdx.x & 63) == 0)
+        s[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = s[threadIdx.x & 15];
+#pragma unroll
+    for (int off = 8; off >= 1; off >>= 1)
+        v = fmaxf(v, __shfl_xor(v, off));
+    __syncthreads();
+    return v;
+}
+
+__device__ __forceinline__ u64 shfl_up64(u64 v, int off)
+{
+    const uint32_t lo = __shfl_up((uint32_t)v, off), hi = __shfl_up((uint32_t)(v >> 32), off);
+    return ((u64)hi << 32) | lo;
+}
+
+// The inclusive sum over the threads up to this one, and the whole sum.
+__device__ __forceinline__ u64 block_scan(u64 v, u64 *s, u64 &total)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const u64 o = shfl_up64(v, off);
+        v += lane >= off ? o : 0ull;
+    }
+    if (lane == 63)
+        s[wave] = v;
+    __syncthreads();
+    u64 before = 0ull;
+    total = 0ull;
+#pragma unroll
+    for (int w = 0; w < kDrawThreads / 64; ++w) {
+        before += w < wave ? s[w] : 0ull;
+        total += s[w];
+    }
+    __syncthreads();
+    return v + before;
+}
+
+struct DrawLds {
+    u64 keys[kCap];                           // candidates in the order of their tokens
+    u64 hist[kBins];
+    uint32_t hits[kBins];
+    __attribute__((aligned(16))) uint32_t words[2 * kChunk];   // the rules' words of one chunk
+    u64 scan[16];
+    float fl[16];
+    u64 found, rest;
+    int at, some;
+    float value;
+};
+
+// Keys by value, then token: 56 bits that are all in use.
+__device__ __forceinline__ u64 short_key(u64 key)
+{
+    return (key >> 32) << 24 | (key & 0xFFFFFFull);
+}
+
+// The smallest key whose larger keys together weigh less than `target` (at
+// least 1), or 0 where all keys together weigh less than that.
+template <class Weight>
+__device__ __forceinline__ u64 border(const u64 *keys, int n, u64 lo, u64 hi, u64 target, DrawLds &lds, Weight &&weight)
+{
+    u64 above = 0ull;
+    const int tid = threadIdx.x;
+    while (true) {
+        // bins of 2^shift keys, from hi down
+        const int width = hi > lo ? 64 - __builtin_clzll(hi - lo) : 1, shift = width > 10 ? width - 10 : 0;
+        lds.hist[tid] = 0ull;
+        lds.hits[tid] = 0u;
+        if (tid == 0)
+            lds.at = -1;
+        __syncthreads();
+        for (int i = tid; i < n; i += kDrawThreads) {
+            const u64 key = short_key(keys[i]);
+            if (key >= lo && key <= hi) {
+                const int bin = (int)((hi - key) >> shift);
+                atomicAdd(&lds.hist[bin], weight(keys[i]));
+                atomicAdd(&lds.hits[bin], 1u);
+            }
+        }
+        __syncthreads();
+        u64 total;
+        const u64 mine = lds.hist[tid], upto = block_scan(mine, lds.scan, total) + above;
+        if (upto - mine < target && upto >= target) {
+            lds.at = tid;
+            lds.rest = upto - mine;
+        }
+        __syncthreads();
+        const int bin = lds.at;
+        if (bin < 0)
+            return 0ull;
+        above = lds.rest;
+        const uint32_t hits = lds.hits[bin];
+        hi -= (u64)bin << shift;
+        const u64 below = hi - ((1ull << shift) - 1ull);
+        lo = below > lo && below <= hi ? below : lo;
+        if (hits == 1u)
+            break;
+        __syncthreads();
+    }
+    for (int i = tid; i < n; i += kDrawThreads) {
+        const u64 key = short_key(keys[i]);
+        if (key >= lo && key <= hi)
+            lds.found = key;
+    }
+    __syncthreads();
+    const u64 key = lds.found;
+    __syncthreads();
+    return key;
+}
+
+__device__ __forceinline__ u64 fixed(double mass, int bits)
+{
+    return (u64)llrint(ldexp(mass, bits));
+}
+__device__ __forceinline__ double floating(u64 sum, int bits)
+{
+    return ldexp((double)sum, -bits);
+}
+
+// The sum that a token's has to exceed.
+__device__ __forceinline__ u64 drawn(float u, u64 total)
+{
+    const double y = u > 0.0f ? floor((double)u * (double)total) : 0.0;
+    return y < (double)total ? min((u64)y, total - 1ull) : total - 1ull;
+}
+
+struct Draw {
+    int token;
+    float prob, p_draft;
+};
+
+// The row's token among the candidates keys[0, n).
+__device__ __forceinline__ Draw draw_filtered(const SampleArgs &a, const Settings &set, const u64 *keys, int n, float gm,
+                                              double others, int d, float u, DrawLds &lds)
+{
+    const int tid = threadIdx.x;
+    auto mass = [&](u64 key, float ref) { return set.t > 0.0f ? mass_below(key_value(key), ref, set.inv_t) : 1.0; };
+    auto units = [&](u64 key, float ref) { return fixed(mass(key, ref), a.bits); };
+    const u64 hi = (u64)order_word(gm) << 24 | 0xFFFFFFull;
+    u64 lo = 0ull;
+    if (set.k > 0 || set.p < 1.0f) {
+        // the smallest value among the candidates
+        float v = __builtin_huge_valf();
+        for (int i = tid; i < n; i += kDrawThreads)
+            v = fminf(v, key_value(keys[i]));
+        v = -block_max(-v, lds.fl);
+        lo = (u64)order_word(v) << 24;
+    }
+    u64 least = 0ull;
+    if (set.k > 0 && set.k < n)
+        least = border(keys, n, lo, hi, (u64)set.k, lds, [](u64) { return 1ull; });
+    if (set.p < 1.0f) {
+        u64 whole;
+        if (set.k > 0) {
+            u64 w = 0ull;
+            for (int i = tid; i < n; i += kDrawThreads)
+                if (short_key(keys[i]) >= least)
+                    w += units(keys[i], gm);
+            block_scan(w, lds.scan, whole);
+        } else {
+            whole = fixed(others, a.bits);
+        }
+        const double bar = ceil((double)set.p * (double)whole);
+        const u64 target = bar > 1.0 ? (u64)bar : 1ull;
+        const u64 last = border(keys, n, lo, hi, target, lds, [&](u64 key) { return units(key, gm); });
+        least = last > least ? last : least;
+    }
+    auto kept = [&](u64 key) {
+        return short_key(key) >= least && (set.mp <= 0.0f || mass(key, gm) >= (double)set.mp);
+    };
+    // the draft's share, and the largest value without it
+    Draw out = {-1, 0.0f, 0.0f};
+    float ref = gm;
+    if (a.accept) {
+        if (tid == 0)
+            lds.some = 0;
+        float v = kNegInf;
+        u64 w = 0ull;
+        __syncthreads();
+        for (int i = tid; i < n; i += kDrawThreads)
+            if (kept(keys[i])) {
+                w += units(keys[i], gm);
+                if (key_token(keys[i]) == d) {
+                    lds.some = 1;
+                    lds.value = key_value(keys[i]);
+                } else {
+                    v = fmaxf(v, key_value(keys[i]));
+                }
+            }
+        u64 whole;
+        block_scan(w, lds.scan, whole);
+        if (lds.some) {
+            const double md = set.t > 0.0f ? mass_below(lds.value, gm, set.inv_t) : 1.0;
+            out.p_draft = (float)(md / floating(whole, a.bits));
+        }
+        ref = block_max(v, lds.fl);
+        if (ref == kNegInf)
+            return out;
+    }
+    // the sums go by stretches of tokens, one a thread
+    const int each = (n + kDrawThreads - 1) / kDrawThreads, i0 = min(tid * each, n), i1 = min(i0 + each, n);
+    auto counts = [&](u64 key) { return kept(key) && !(a.accept && key_token(key) == d); };
+    u64 w = 0ull;
+    for (int i = i0; i < i1; ++i)
+        if (counts(keys[i]))
+            w += units(keys[i], ref);
+    u64 total;
+    const u64 upto = block_scan(w, lds.scan, total);
+    const u64 target = drawn(u, total);
+    if (upto - w <= target && target < upto) {
+        u64 sum = upto - w;
+        for (int i = i0; i < i1; ++i)
+            if (counts(keys[i])) {
+                sum += units(keys[i], ref);
+                if (sum > target) {
+                    lds.at = key_token(keys[i]);
+                    lds.value = (float)(mass(keys[i], ref) / floating(total, a.bits));
+                    break;
+                }
+            }
+    }
+    __syncthreads();
+    out.token = lds.at;
+    out.prob = lds.value;
+    return out;
+}
+
+template <int kDtype>
+__global__ void __launch_bounds__(kDrawThreads) sample_draw_kernel(SampleArgs a)
+{
+    __shared__ DrawLds lds;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int row = blockIdx.x, req = row / a.T, t = row % a.T, V = a.V;
+    const Settings set = load_settings(a, req);
+    const int n_lists = a.n_lists, n_chunks = (V + kChunk - 1) / kChunk;
+    const float u = a.uniforms[row];
+    const bool drafted = a.accept && t < a.T - 1;
+    const int d = drafted ? a.draft[(size_t)req * (a.T - 1) + t] : -1;
+    const float xd = d >= 0 && d < V ? a.draft_logit[row] : kNegInf;
+
+    float gm = kNegInf;
+    for (int i = tid; i < n_lists; i += kDrawThreads)
+        gm = fmaxf(gm, a.tops[(size_t)row * n_lists + i]);
+    gm = block_max(gm, lds.fl);
+    Draw out = {-1, 0.0f, 0.0f};
+    if (gm > kNegInf) {
+        // the chunks' masses, the draft's apart
+        const float *maxes = a.maxes + (size_t)row * n_chunks;
+        const double *sums = a.sums + (size_t)row * n_chunks;
+        float ref = kNegInf;
+        u64 total = 0ull;
+        auto chunk_mass = [&](int c) { return fixed(sums[c] * mass_below(maxes[c], ref, set.inv_t), a.bits); };
+        double whole = 0.0;                   // relative to gm, with the draft
+        const double md = xd > kNegInf ? mass_below(xd, gm, set.inv_t) : 0.0;
+        if (set.summed()) {
+            for (int c = tid; c < n_chunks; c += kDrawThreads)
+                ref = fmaxf(ref, maxes[c]);
+            ref = block_max(ref, lds.fl);
+            u64 w = 0ull;
+            if (ref > kNegInf)
+                for (int c = tid; c < n_chunks; c += kDrawThreads)
+                    w += chunk_mass(c);
+            block_scan(w, lds.scan, total);
+            whole = md + floating(total, a.bits) * (ref > kNegInf ? mass_below(ref, gm, set.inv_t) : 0.0);
+        }
+        if (!set.filtered()) {
+            out.p_draft = (float)(md / whole);
+            if (total) {
+                const u64 target = drawn(u, total);
+                u64 before = 0ull;
+                for (int c0 = 0; c0 < n_chunks; c0 += kDrawThreads) {
+                    const u64 w = c0 + tid < n_chunks ? chunk_mass(c0 + tid) : 0ull;
+                    u64 part;
+                    const u64 upto = before + block_scan(w, lds.scan, part);
+                    if (upto - w <= target && target < upto) {
+                        lds.at = c0 + tid;
+                        lds.rest = target - (upto - w);
+                    }
+                    before += part;
+                }
+                __syncthreads();
+                const int chunk = lds.at;
+                const u64 rest = lds.rest;
+                // that chunk once more, under its rules
+                SliceWalk<kDtype> walk(a, lds.words, chunk * kChunk, kChunk, req, t, 0, 1);
+                if (wave == 0) {
+                    walk.load_request();
+                    walk.rule(chunk * kChunk, walk.ha);
+                    u64 sum = 0ull;
+                    int token = -1, last = -1;
+                    float value = 0.0f, last_value = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) {
+                        const int v = chunk * kChunk + 64 * i + lane;
+                        const float x = drafted && v == d ? kNegInf : walk.ha.x[i];
+                        const u64 own = x > kNegInf ? fixed(mass_below(x, ref, set.inv_t), a.bits) : 0ull;
+                        u64 w = own;
+#pragma unroll
+                        for (int off = 1; off < 64; off <<= 1) {
+                            const u64 o = shfl_up64(w, off);
+                            w += lane >= off ? o : 0ull;
+                        }
+                        const u64 past = __ballot(own && sum + w > rest);
+                        if (past && token < 0) {
+                            const int at = __builtin_ctzll(past);
+                            token = chunk * kChunk + 64 * i + at;
+                            value = __shfl(x, at);
+                        }
+                        const u64 some = __ballot(own != 0ull);
+                        if (some) {           // the chunk's own sum may be a rounding less
+                            const int at = 63 - __builtin_clzll(some);
+                            last = chunk * kChunk + 64 * i + at;
+                            last_value = __shfl(x, at);
+                        }
+                        sum += readlane64(w, 63);
+                    }
+                    if (token < 0) {
+                        token = last;
+                        value = last_value;
+                    }
+                    if (lane == 0) {
+                        lds.at = token;
+                        lds.value = (float)(mass_below(value, ref, set.inv_t) / floating(total, a.bits));
+                    }
+                }
+                __syncthreads();
+                out.token = lds.at;
+                out.prob = lds.value;
+            }
+        } else {
+            // the candidates' lists side by side, in LDS or at the front of their row
+            int *offsets = a.counts + (size_t)row * (n_lists + 1);
+            const int part = a.slice / a.ways;
+            u64 *cand = a.cand + (size_t)row * V;
+            u64 n64 = 0ull;
+            for (int c0 = 0; c0 < n_lists; c0 += kDrawThreads) {
+                const u64 c = c0 + tid < n_lists ? (u64)offsets[c0 + tid] : 0ull;
+                u64 some;
+                const u64 upto = n64 + block_scan(c, lds.scan, some);
+                if (c0 + tid < n_lists)
+                    offsets[c0 + tid] = (int)(upto - c);
+                n64 += some;
+            }
+            const int n = (int)n64;
+            if (tid == 0)
+                offsets[n_lists] = n;
+            __syncthreads();
+            if (n <= kCap) {
+                for (int l = wave; l < n_lists; l += kDrawThreads / 64) {
+                    const int o = offsets[l], c = offsets[l + 1] - o;
+                    const u64 *from = cand + (size_t)l * part;
+                    for (int i = lane; i < c; i += 64)
+                        lds.keys[o + i] = from[i];
+                }
+                __syncthreads();
+                out = draw_filtered(a, set, lds.keys, n, gm, whole, d, u, lds);
+            } else {
+                // a key never moves up: what a round writes, no later one reads
+                for (int i0 = 0; i0 < n; i0 += kDrawThreads) {
+                    const int i = i0 + tid;
+                    u64 key = 0ull;
+                    if (i < n) {
+                        int l = 0, r = n_lists - 1;    // the last list that begins at i or before
+                        while (l < r) {
+                            const int m = (l + r + 1) / 2;
+                            if (offsets[m] <= i)
+                                l = m;
+                            else
+                                r = m - 1;
+                        }
+                        key = cand[(size_t)l * part + (i - offsets[l])];
+                    }
+                    __syncthreads();
+                    if (i < n)
+                        cand[i] = key;
+                    __syncthreads();
+                }
+                out = draw_filtered(a, set, cand, n, gm, whole, d, u, lds);
+            }
+        }
+    }
+    if (tid == 0) {
+        a.token_ids[row] = out.token;
+        a.token_probs[row] = out.prob;
+        if (a.accept) {
+            if (drafted) {
+                const size_t di = (size_t)req * (a.T - 1) + t;
+                a.p_draft[di] = out.p_draft;
+                __hip_atomic_store(&a.oks[row], a.accept[di] < out.p_draft ? 1u : 0u, __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
+            }
+            // the request's last row counts
+            const uint32_t done = __hip_atomic_fetch_add(&a.tickets[req], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+            if (done == (uint32_t)a.T - 1u) {
+                int k = 0;
+                while (k < a.T - 1 && __hip_atomic_load(&a.oks[(size_t)req * a.T + k], __ATOMIC_RELAXED,
+                                                        __HIP_MEMORY_SCOPE_AGENT))
+                    ++k;
+                a.n_accepted[req] = k;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+struct Layout {
+    size_t cand, counts, tops, sums, maxes, draft_logit, tickets, oks, bytes;
+};
+
+Layout layout_for(int R, int T, int V)
+{
+    Layout l;
+    const size_t M = (size_t)R * T, chunks = (V + kChunk - 1) / kChunk;
+    const size_t lists = chunks + kMaxWaves;   // with one more, at most
+    l.cand = 0;
+    l.counts = l.cand + round256(M * V * 8);
+    l.tops = l.counts + round256(M * lists * 4);
+    l.sums = l.tops + round256(M * lists * 4);
+    l.maxes = l.sums + round256(M * chunks * 8);
+    l.draft_logit = l.maxes + round256(M * chunks * 4);
+    l.tickets = l.draft_logit + round256(M * 4);
+    l.oks = l.tickets + round256((size_t)R * 4);
+    l.bytes = l.oks + round256(M * 4);
+    return l;
+}
+
+template <int kDtype>
+hipError_t launch(const SampleArgs &a, const Shape &sh, hipStream_t s)
+{
+    hipLaunchKernelGGL(sample_scan_kernel<kDtype>, sh.grid, sh.block, sh.lds, s, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+        return e;
+    hipLaunchKernelGGL(sample_draw_kernel<kDtype>, dim3(a.R * a.T), dim3(kDrawThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+} // namespace
+
+extern "C" {
+
+size_t sample_logits_workspace_bytes(int R, int T, int V)
+{
+    if (!sizes_ok(R, T, V) || V > kMaxV)
+        return 0;
+    return layout_for(R, T, V).bytes;
+}
+
+int sample_logits_rows(const void *logits, int64_t logits_stride, int dtype, const int32_t *draft_ids, int R, int T,
+                       int V, const int4vh_logit_rules *rules, const int4vh_sampling *sampling, const float *uniforms,
+                       const float *accept, int32_t *token_ids, float *token_probs, float *p_draft,
+                       int32_t *n_accepted, void *workspace, size_t workspace_bytes, void *stream)
+{
+    int st = check_rules(logits, logits_stride, dtype, draft_ids, R, T, V, rules);
+    if (st == INT4VH_EINVAL)
+        return st;
+    if (!sampling || !uniforms || !token_ids || !token_probs || !workspace)
+        return INT4VH_EINVAL;
+    if (accept && (T == 1 || !p_draft || !n_accepted))
+        return INT4VH_EINVAL;
+    if (!sampling->temperatures && (!(sampling->temperature >= 0.0f) || !std::isfinite(sampling->temperature)))
+        return INT4VH_EINVAL;
+    if ((!sampling->top_ks && sampling->top_k < 0) ||
+        (!sampling->top_ps && !(sampling->top_p >= 0.0f && sampling->top_p <= 1.0f)) ||
+        (!sampling->min_ps && !(sampling->min_p >= 0.0f && sampling->min_p <= 1.0f)))
+        return INT4VH_EINVAL;
+    if (!rows_aligned(sampling->temperatures, 4) || !rows_aligned(sampling->top_ks, 4) ||
+        !rows_aligned(sampling->top_ps, 4) || !rows_aligned(sampling->min_ps, 4) || !rows_aligned(uniforms, 4) ||
+        !rows_aligned(accept, 4) || !rows_aligned(token_ids, 4) || !rows_aligned(token_probs, 4) ||
+        !rows_aligned(p_draft, 4) || !rows_aligned(n_accepted, 4) || !rows_aligned(workspace, 256))
+        return INT4VH_EALIGN;
+    if (st != INT4VH_OK)
+        return st;
+    const Layout l = layout_for(R, T, V);
+    if (workspace_bytes < l.bytes)
+        return INT4VH_EWORKSPACE;
+    int cus = 0;
+    if ((st = current_cus(&cus)) != INT4VH_OK)
+        return st;
+
+    char *ws = static_cast<char *>(workspace);
+    SampleArgs a = {};
+    a.logits = logits;
+    a.logits_stride = logits_stride;
+    a.draft = draft_ids;
+    a.R = R;
+    a.T = T;
+    a.V = V;
+    fill_rules(a, rules, T);
+    a.s = *sampling;
+    a.uniforms = uniforms;
+    a.accept = accept;
+    a.bits = 62;
+    while ((1 << (62 - a.bits)) < V)
+        --a.bits;
+    a.cand = reinterpret_cast<u64 *>(ws + l.cand);
+    a.counts = reinterpret_cast<int *>(ws + l.counts);
+    a.tops = reinterpret_cast<float *>(ws + l.tops);
+    a.sums = reinterpret_cast<double *>(ws + l.sums);
+    a.maxes = reinterpret_cast<float *>(ws + l.maxes);
+    a.draft_logit = reinterpret_cast<float *>(ws + l.draft_logit);
+    a.tickets = reinterpret_cast<uint32_t *>(ws + l.tickets);
+    a.oks = reinterpret_cast<uint32_t *>(ws + l.oks);
+    a.token_ids = token_ids;
+    a.token_probs = token_probs;
+    a.p_draft = p_draft;
+    a.n_accepted = n_accepted;
+    const Shape sh = shape_for(a, 0, cus);
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const hipError_t e = dtype == INT4VH_ROWS_F32   ? launch<INT4VH_ROWS_F32>(a, sh, s)
+                         : dtype == INT4VH_ROWS_F16 ? launch<INT4VH_ROWS_F16>(a, sh, s)
+                                                    : launch<INT4VH_ROWS_BF16>(a, sh, s);
+    return e == hipSuccess ? INT4VH_OK : hip_fail(e, "sampling kernel launch");
+}
+
+} // extern "C"
