@@ -31,7 +31,8 @@ namespace {
 using namespace int4vh_detail;
 
 constexpr int kDrawThreads = 1024;
-constexpr int kCap = 8192;                // candidates that the drawing kernel holds in LDS
+constexpr int kCap = 4096;                // candidates that the drawing kernel holds in LDS
+constexpr int kFew = 512;                 // and those that it compares with each other
 constexpr int kBins = kDrawThreads;
 
 struct SampleArgs : RulesArgs {
@@ -40,8 +41,9 @@ struct SampleArgs : RulesArgs {
     const float *accept;       // [R, T-1] or null
     int bits;                  // masses are multiples of 2^-bits
     u64 *cand;                 // [R*T, V] candidates' keys; a list begins at its wave's first token
-    int *counts;               // [R*T, n_lists + 1] candidates of each list, then where it begins
+    int *counts;               // [R*T, n_lists] candidates of each list
     float *tops;               // [R*T, n_lists] largest value of each wave's tokens
+    float *bars;               // [R*T, n_lists] what it knows that a kept token reaches
     double *sums;              // [R*T, chunks] mass of each chunk, less the row's draft where drafts are verified
     float *maxes;              // [R*T, chunks] what it is relative to: the largest value
     float *draft_logit;        // [R*T] ruled logit of the row's draft, where it is in [0, V)
@@ -89,6 +91,23 @@ __device__ __forceinline__ double mass_below(float x, float m, double inv_t)
     return x == m ? 1.0 : x > kNegInf ? exp(((double)x - (double)m) * inv_t) : 0.0;
 }
 
+// How far below a row's largest value m a kept token may lie, with slack for the
+// roundings of this bound.  Infinite where the settings do not bound it, and 0
+// below an infinite m, as long as they do.
+__device__ __forceinline__ float reach_of(const Settings &set, int V, float m)
+{
+    float reach = __builtin_huge_valf();
+    if (set.t == 0.0f)
+        return 0.0f;
+    if (set.mp > 0.0f && (set.k == 0 || set.p >= 1.0f))
+        reach = -set.t * logf(set.mp);
+    if (set.p < 1.0f && set.k == 0)
+        reach = fminf(reach, set.t * logf((float)V / (1.0f - set.p)));
+    if (reach == __builtin_huge_valf())
+        return reach;
+    return m == __builtin_huge_valf() ? 0.0f : reach * (1.0f + 0x1p-18f) + set.t * 0x1p-18f + fabsf(m) * 0x1p-20f;
+}
+
 __device__ __forceinline__ double wave_sum_f64(double v)
 {
 #pragma unroll
@@ -111,18 +130,6 @@ __global__ void __launch_bounds__(64 * kMaxWaves) sample_scan_kernel(SampleArgs 
     const Settings set = load_settings(a, walk.req);
     const bool filtered = set.filtered(), summed = set.summed();
     const int n_all = (V + kChunk - 1) / kChunk;
-    // how far below the largest value a candidate may lie; slack for this
-    // bound's own roundings
-    float reach = __builtin_huge_valf();
-    if (set.t == 0.0f) {
-        reach = 0.0f;
-    } else {
-        if (set.mp > 0.0f && (set.k == 0 || set.p >= 1.0f))
-            reach = -set.t * logf(set.mp);
-        if (set.p < 1.0f && set.k == 0)
-            reach = fminf(reach, set.t * logf((float)V / (1.0f - set.p)));
-        reach = reach * (1.0f + 0x1p-18f) + set.t * 0x1p-18f;
-    }
     u64 *list = a.cand + (size_t)row * V + walk.begin;
     int n = 0;                                // candidates written
     float top = kNegInf;                      // this lane's largest value
@@ -137,8 +144,7 @@ __global__ void __launch_bounds__(64 * kMaxWaves) sample_scan_kernel(SampleArgs 
         if (filtered && __ballot(best >= from)) {
             if (__ballot(more)) {
                 const float m = wave_max(top);
-                const float bar = m - reach - fabsf(m) * 0x1p-20f;
-                from = bar > from ? bar : m == __builtin_huge_valf() && reach < m ? m : from;
+                from = fmaxf(from, m - reach_of(set, V, m));
                 if (set.k > 0 && set.k <= 64) {
                     const uint32_t th = reach_threshold(top > kNegInf ? order_word(top) : 0u, set.k);
                     if (th > 1u)
@@ -188,8 +194,9 @@ __global__ void __launch_bounds__(64 * kMaxWaves) sample_scan_kernel(SampleArgs 
     const float m = wave_max(top);
     if (lane == 0) {
         const size_t slot = (size_t)row * a.n_lists + blockIdx.x * a.ways + walk.way;
-        a.counts[slot + row] = n;
+        a.counts[slot] = n;
         a.tops[slot] = m;
+        a.bars[slot] = from;
     }
 }
 
@@ -241,76 +248,17 @@ __device__ __forceinline__ u64 block_scan(u64 v, u64 *s, u64 &total)
 }
 
 struct DrawLds {
-    u64 keys[kCap];                           // candidates in the order of their tokens
+    u64 keys[kCap];                           // candidates, in any order
+    u64 units[kFew];                          // and masses of few
     u64 hist[kBins];
     uint32_t hits[kBins];
     __attribute__((aligned(16))) uint32_t words[2 * kChunk];   // the rules' words of one chunk
     u64 scan[16];
     float fl[16];
     u64 found, rest;
-    int at, some;
+    int at, n, some;
     float value;
 };
-
-// Keys by value, then token: 56 bits that are all in use.
-__device__ __forceinline__ u64 short_key(u64 key)
-{
-    return (key >> 32) << 24 | (key & 0xFFFFFFull);
-}
-
-// The smallest key whose larger keys together weigh less than `target` (at
-// least 1), or 0 where all keys together weigh less than that.
-template <class Weight>
-__device__ __forceinline__ u64 border(const u64 *keys, int n, u64 lo, u64 hi, u64 target, DrawLds &lds, Weight &&weight)
-{
-    u64 above = 0ull;
-    const int tid = threadIdx.x;
-    while (true) {
-        // bins of 2^shift keys, from hi down
-        const int width = hi > lo ? 64 - __builtin_clzll(hi - lo) : 1, shift = width > 10 ? width - 10 : 0;
-        lds.hist[tid] = 0ull;
-        lds.hits[tid] = 0u;
-        if (tid == 0)
-            lds.at = -1;
-        __syncthreads();
-        for (int i = tid; i < n; i += kDrawThreads) {
-            const u64 key = short_key(keys[i]);
-            if (key >= lo && key <= hi) {
-                const int bin = (int)((hi - key) >> shift);
-                atomicAdd(&lds.hist[bin], weight(keys[i]));
-                atomicAdd(&lds.hits[bin], 1u);
-            }
-        }
-        __syncthreads();
-        u64 total;
-        const u64 mine = lds.hist[tid], upto = block_scan(mine, lds.scan, total) + above;
-        if (upto - mine < target && upto >= target) {
-            lds.at = tid;
-            lds.rest = upto - mine;
-        }
-        __syncthreads();
-        const int bin = lds.at;
-        if (bin < 0)
-            return 0ull;
-        above = lds.rest;
-        const uint32_t hits = lds.hits[bin];
-        hi -= (u64)bin << shift;
-        const u64 below = hi - ((1ull << shift) - 1ull);
-        lo = below > lo && below <= hi ? below : lo;
-        if (hits == 1u)
-            break;
-        __syncthreads();
-    }
-    for (int i = tid; i < n; i += kDrawThreads) {
-        const u64 key = short_key(keys[i]);
-        if (key >= lo && key <= hi)
-            lds.found = key;
-    }
-    __syncthreads();
-    const u64 key = lds.found;
-    __syncthreads();
-    return key;
-}
 
 __device__ __forceinline__ u64 fixed(double mass, int bits)
 {
@@ -328,103 +276,263 @@ __device__ __forceinline__ u64 drawn(float u, u64 total)
     return y < (double)total ? min((u64)y, total - 1ull) : total - 1ull;
 }
 
+// Keys by value, then token: 56 bits that are all in use; and by token alone,
+// the lowest first.
+__device__ __forceinline__ u64 value_key(u64 key)
+{
+    return (key >> 32) << 24 | (key & 0xFFFFFFull);
+}
+__device__ __forceinline__ u64 token_key(u64 key)
+{
+    return key & 0xFFFFFFull;
+}
+
+// The bin, of lds.hist as the threads have filled it from the top, in which the
+// sum from the top on reaches `target` (-1: none does); lds.rest is the sum
+// above it.
+__device__ __forceinline__ int border_bin(u64 above, u64 target, DrawLds &lds)
+{
+    u64 total;
+    const u64 mine = lds.hist[threadIdx.x], upto = block_scan(mine, lds.scan, total) + above;
+    if (upto - mine < target && upto >= target) {
+        lds.at = threadIdx.x;
+        lds.rest = upto - mine;
+    }
+    __syncthreads();
+    return lds.at;
+}
+
+// The key (by `order`) of the last candidate whose predecessors, those of
+// larger keys, weigh less than `target` (at least 1) together; 0 where all
+// candidates weigh less than that.  each(f) calls f with every candidate once;
+// keys lie in [lo, hi].
+template <class Each, class Order, class Weight>
+__device__ __forceinline__ u64 border(Each &&each, u64 lo, u64 hi, u64 target, DrawLds &lds, Order &&order,
+                                      Weight &&weight)
+{
+    u64 above = 0ull;
+    const int tid = threadIdx.x;
+    while (true) {
+        // bins of 2^shift keys, from hi down
+        const int width = hi > lo ? 64 - __builtin_clzll(hi - lo) : 1, shift = width > 10 ? width - 10 : 0;
+        lds.hist[tid] = 0ull;
+        lds.hits[tid] = 0u;
+        if (tid == 0)
+            lds.at = -1;
+        __syncthreads();
+        each([&](u64 key) {
+            const u64 o = order(key);
+            if (o >= lo && o <= hi) {
+                const u64 w = weight(key);
+                if (w) {
+                    const int bin = (int)((hi - o) >> shift);
+                    atomicAdd(&lds.hist[bin], w);
+                    atomicAdd(&lds.hits[bin], 1u);
+                }
+            }
+        });
+        __syncthreads();
+        const int bin = border_bin(above, target, lds);
+        if (bin < 0)
+            return 0ull;
+        above = lds.rest;
+        const uint32_t hits = lds.hits[bin];
+        hi -= (u64)bin << shift;
+        const u64 below = hi - ((1ull << shift) - 1ull);
+        lo = below > lo && below <= hi ? below : lo;
+        if (hits == 1u)
+            break;
+        __syncthreads();
+    }
+    each([&](u64 key) {
+        const u64 o = order(key);
+        if (o >= lo && o <= hi && weight(key))
+            lds.found = o;
+    });
+    __syncthreads();
+    const u64 key = lds.found;
+    __syncthreads();
+    return key;
+}
+
 struct Draw {
     int token;
     float prob, p_draft;
 };
 
-// The row's token among the candidates keys[0, n).
-__device__ __forceinline__ Draw draw_filtered(const SampleArgs &a, const Settings &set, const u64 *keys, int n, float gm,
-                                              double others, int d, float u, DrawLds &lds)
+// A row's candidates and what they are drawn with.
+struct Row {
+    const SampleArgs &a;
+    const Settings &set;
+    float gm;                                 // the largest value
+    double whole;                             // mass of the row, where top_p applies to all of it
+    int d;                                    // the draft that is left out, or -1
+    float u;
+
+    __device__ __forceinline__ double mass(u64 key, float ref) const
+    {
+        return set.t > 0.0f ? mass_below(key_value(key), ref, set.inv_t) : 1.0;
+    }
+    __device__ __forceinline__ u64 units(u64 key, float ref) const { return fixed(mass(key, ref), a.bits); }
+    // what a sum has to reach to hold top_p of `all`; at least 1, for the best token
+    __device__ __forceinline__ u64 share(u64 all) const
+    {
+        const double bar = ceil((double)set.p * (double)all);
+        return bar > 1.0 ? (u64)bar : 1ull;
+    }
+};
+
+// Few candidates, n <= kFew of lds.keys: each is compared with all others, by a
+// group of threads, which gives its rank and the mass in front of it; once
+// more by token for the sum that draws.
+__device__ __forceinline__ Draw draw_few(const Row &r, int n, DrawLds &lds)
 {
     const int tid = threadIdx.x;
-    auto mass = [&](u64 key, float ref) { return set.t > 0.0f ? mass_below(key_value(key), ref, set.inv_t) : 1.0; };
-    auto units = [&](u64 key, float ref) { return fixed(mass(key, ref), a.bits); };
-    const u64 hi = (u64)order_word(gm) << 24 | 0xFFFFFFull;
-    u64 lo = 0ull;
+    int group = kDrawThreads / kFew;          // threads a key
+    while (group < 64 && 2 * group * n <= kDrawThreads)
+        group *= 2;
+    const int i = tid / group, sub = tid % group;
+    const bool mine = i < n;
+    const u64 key = mine ? lds.keys[i] : 0ull;
+    const u64 own = mine ? r.units(key, r.gm) : 0ull;
+    if (mine && sub == 0)
+        lds.units[i] = own;
+    if (tid == 0)
+        lds.some = 0;
+    __syncthreads();
+    int rank = 0;
+    u64 before = 0ull;
+    for (int j = sub; j < n; j += group) {
+        const bool more = lds.keys[j] > key;
+        rank += more;
+        before += more ? lds.units[j] : 0ull;
+    }
+    for (int off = 1; off < group; off <<= 1) {
+        rank += __shfl_xor(rank, off);
+        before += shfl_xor64(before, off);
+    }
+    const bool lead = mine && sub == 0;
+    bool kept = mine && (r.set.k == 0 || rank < r.set.k);
+    if (r.set.p < 1.0f) {
+        u64 all;
+        if (r.set.k > 0)
+            block_scan(lead && kept ? own : 0ull, lds.scan, all);
+        else
+            all = fixed(r.whole, r.a.bits);
+        kept = kept && before < r.share(all);
+    }
+    kept = kept && (r.set.mp <= 0.0f || r.mass(key, r.gm) >= (double)r.set.mp);
+    Draw out = {-1, 0.0f, 0.0f};
+    float ref = r.gm;
+    u64 w = kept ? own : 0ull;
+    if (r.d >= 0) {
+        u64 all;
+        block_scan(lead ? w : 0ull, lds.scan, all);
+        const bool draft = kept && key_token(key) == r.d;
+        if (draft && sub == 0) {
+            lds.some = 1;
+            lds.value = (float)(r.mass(key, r.gm) / floating(all, r.a.bits));
+        }
+        kept = kept && !draft;
+        ref = block_max(kept ? key_value(key) : kNegInf, lds.fl);
+        out.p_draft = lds.some ? lds.value : 0.0f;
+        if (ref == kNegInf)
+            return out;
+        w = kept ? r.units(key, ref) : 0ull;
+    }
+    u64 total;
+    block_scan(lead ? w : 0ull, lds.scan, total);
+    if (lead)
+        lds.units[i] = w;
+    __syncthreads();
+    before = 0ull;
+    for (int j = sub; j < n; j += group)
+        before += token_key(lds.keys[j]) > token_key(key) ? lds.units[j] : 0ull;
+    for (int off = 1; off < group; off <<= 1)
+        before += shfl_xor64(before, off);
+    const u64 target = drawn(r.u, total);
+    if (lead && before <= target && target < before + w) {
+        lds.at = key_token(key);
+        lds.value = (float)(r.mass(key, ref) / floating(total, r.a.bits));
+    }
+    __syncthreads();
+    out.token = lds.at;
+    out.prob = lds.value;
+    return out;
+}
+
+// Any number of them: the borders by histograms.  each(f): f with every
+// candidate once.
+template <class Each>
+__device__ __forceinline__ Draw draw_many(const Row &r, Each &&each, DrawLds &lds)
+{
+    const Settings &set = r.set;
+    const int tid = threadIdx.x, bits = r.a.bits;
+    u64 least = 0ull;
     if (set.k > 0 || set.p < 1.0f) {
         // the smallest value among the candidates
         float v = __builtin_huge_valf();
-        for (int i = tid; i < n; i += kDrawThreads)
-            v = fminf(v, key_value(keys[i]));
+        each([&](u64 key) { v = fminf(v, key_value(key)); });
         v = -block_max(-v, lds.fl);
-        lo = (u64)order_word(v) << 24;
-    }
-    u64 least = 0ull;
-    if (set.k > 0 && set.k < n)
-        least = border(keys, n, lo, hi, (u64)set.k, lds, [](u64) { return 1ull; });
-    if (set.p < 1.0f) {
-        u64 whole;
-        if (set.k > 0) {
-            u64 w = 0ull;
-            for (int i = tid; i < n; i += kDrawThreads)
-                if (short_key(keys[i]) >= least)
-                    w += units(keys[i], gm);
-            block_scan(w, lds.scan, whole);
-        } else {
-            whole = fixed(others, a.bits);
+        const u64 lo = (u64)order_word(v) << 24, hi = (u64)order_word(r.gm) << 24 | 0xFFFFFFull;
+        if (set.k > 0)
+            least = border(each, lo, hi, (u64)set.k, lds, value_key, [](u64) { return 1ull; });
+        if (set.p < 1.0f) {
+            u64 all;
+            if (set.k > 0) {
+                u64 w = 0ull;
+                each([&](u64 key) { w += value_key(key) >= least ? r.units(key, r.gm) : 0ull; });
+                block_scan(w, lds.scan, all);
+            } else {
+                all = fixed(r.whole, bits);
+            }
+            const u64 last = border(each, lo, hi, r.share(all), lds, value_key,
+                                    [&](u64 key) { return r.units(key, r.gm); });
+            least = last > least ? last : least;
         }
-        const double bar = ceil((double)set.p * (double)whole);
-        const u64 target = bar > 1.0 ? (u64)bar : 1ull;
-        const u64 last = border(keys, n, lo, hi, target, lds, [&](u64 key) { return units(key, gm); });
-        least = last > least ? last : least;
     }
     auto kept = [&](u64 key) {
-        return short_key(key) >= least && (set.mp <= 0.0f || mass(key, gm) >= (double)set.mp);
+        return value_key(key) >= least && (set.mp <= 0.0f || r.mass(key, r.gm) >= (double)set.mp);
     };
     // the draft's share, and the largest value without it
     Draw out = {-1, 0.0f, 0.0f};
-    float ref = gm;
-    if (a.accept) {
+    float ref = r.gm;
+    if (r.d >= 0) {
         if (tid == 0)
             lds.some = 0;
         float v = kNegInf;
         u64 w = 0ull;
         __syncthreads();
-        for (int i = tid; i < n; i += kDrawThreads)
-            if (kept(keys[i])) {
-                w += units(keys[i], gm);
-                if (key_token(keys[i]) == d) {
+        each([&](u64 key) {
+            if (kept(key)) {
+                w += r.units(key, r.gm);
+                if (key_token(key) == r.d) {
                     lds.some = 1;
-                    lds.value = key_value(keys[i]);
+                    lds.value = key_value(key);
                 } else {
-                    v = fmaxf(v, key_value(keys[i]));
+                    v = fmaxf(v, key_value(key));
                 }
             }
-        u64 whole;
-        block_scan(w, lds.scan, whole);
-        if (lds.some) {
-            const double md = set.t > 0.0f ? mass_below(lds.value, gm, set.inv_t) : 1.0;
-            out.p_draft = (float)(md / floating(whole, a.bits));
-        }
+        });
+        u64 all;
+        block_scan(w, lds.scan, all);
+        if (lds.some)
+            out.p_draft = (float)((set.t > 0.0f ? mass_below(lds.value, r.gm, set.inv_t) : 1.0) / floating(all, bits));
         ref = block_max(v, lds.fl);
         if (ref == kNegInf)
             return out;
     }
-    // the sums go by stretches of tokens, one a thread
-    const int each = (n + kDrawThreads - 1) / kDrawThreads, i0 = min(tid * each, n), i1 = min(i0 + each, n);
-    auto counts = [&](u64 key) { return kept(key) && !(a.accept && key_token(key) == d); };
-    u64 w = 0ull;
-    for (int i = i0; i < i1; ++i)
-        if (counts(keys[i]))
-            w += units(keys[i], ref);
-    u64 total;
-    const u64 upto = block_scan(w, lds.scan, total);
-    const u64 target = drawn(u, total);
-    if (upto - w <= target && target < upto) {
-        u64 sum = upto - w;
-        for (int i = i0; i < i1; ++i)
-            if (counts(keys[i])) {
-                sum += units(keys[i], ref);
-                if (sum > target) {
-                    lds.at = key_token(keys[i]);
-                    lds.value = (float)(mass(keys[i], ref) / floating(total, a.bits));
-                    break;
-                }
-            }
-    }
+    auto drawable = [&](u64 key) { return kept(key) && key_token(key) != r.d ? r.units(key, ref) : 0ull; };
+    u64 w = 0ull, total;
+    each([&](u64 key) { w += drawable(key); });
+    block_scan(w, lds.scan, total);
+    const u64 at = border(each, 0ull, 0xFFFFFFull, drawn(r.u, total) + 1ull, lds, token_key, drawable);
+    each([&](u64 key) {
+        if (token_key(key) == at)
+            lds.value = (float)(r.mass(key, ref) / floating(total, bits));
+    });
     __syncthreads();
-    out.token = lds.at;
+    out.token = (int)(0xFFFFFFull - at);
     out.prob = lds.value;
     return out;
 }
@@ -442,9 +550,14 @@ __global__ void __launch_bounds__(kDrawThreads) sample_draw_kernel(SampleArgs a)
     const int d = drafted ? a.draft[(size_t)req * (a.T - 1) + t] : -1;
     const float xd = d >= 0 && d < V ? a.draft_logit[row] : kNegInf;
 
-    float gm = kNegInf;
-    for (int i = tid; i < n_lists; i += kDrawThreads)
+    float gm = kNegInf, low = kNegInf;
+    u64 n_all = 0ull;
+    const int *counts = a.counts + (size_t)row * n_lists;
+    for (int i = tid; i < n_lists; i += kDrawThreads) {
         gm = fmaxf(gm, a.tops[(size_t)row * n_lists + i]);
+        low = fmaxf(low, a.bars[(size_t)row * n_lists + i]);
+        n_all += (u64)counts[i];
+    }
     gm = block_max(gm, lds.fl);
     Draw out = {-1, 0.0f, 0.0f};
     if (gm > kNegInf) {
@@ -532,55 +645,76 @@ __global__ void __launch_bounds__(kDrawThreads) sample_draw_kernel(SampleArgs a)
                 out.prob = lds.value;
             }
         } else {
-            // the candidates' lists side by side, in LDS or at the front of their row
-            int *offsets = a.counts + (size_t)row * (n_lists + 1);
             const int part = a.slice / a.ways;
-            u64 *cand = a.cand + (size_t)row * V;
-            u64 n64 = 0ull;
-            for (int c0 = 0; c0 < n_lists; c0 += kDrawThreads) {
-                const u64 c = c0 + tid < n_lists ? (u64)offsets[c0 + tid] : 0ull;
-                u64 some;
-                const u64 upto = n64 + block_scan(c, lds.scan, some);
-                if (c0 + tid < n_lists)
-                    offsets[c0 + tid] = (int)(upto - c);
-                n64 += some;
-            }
-            const int n = (int)n64;
-            if (tid == 0)
-                offsets[n_lists] = n;
-            __syncthreads();
-            if (n <= kCap) {
+            const u64 *cand = a.cand + (size_t)row * V;
+            u64 whole_count;
+            block_scan(n_all, lds.scan, whole_count);
+            // Candidates from the row's largest value down to `low`, which all
+            // waves' bounds hold for, in bins by their distance from it; those
+            // behind bin `deepest` are out.
+            low = fmaxf(block_max(low, lds.fl), gm - reach_of(set, V, gm));
+            int deepest = kBins - 1;
+            float scale = 0.0f;
+            auto bin_of = [&](float x) { return x >= gm ? 0 : min((int)((gm - x) * scale), kBins - 1); };
+            auto listed = [&](auto &&f) {
                 for (int l = wave; l < n_lists; l += kDrawThreads / 64) {
-                    const int o = offsets[l], c = offsets[l + 1] - o;
+                    const int c = counts[l];
                     const u64 *from = cand + (size_t)l * part;
-                    for (int i = lane; i < c; i += 64)
-                        lds.keys[o + i] = from[i];
-                }
-                __syncthreads();
-                out = draw_filtered(a, set, lds.keys, n, gm, whole, d, u, lds);
-            } else {
-                // a key never moves up: what a round writes, no later one reads
-                for (int i0 = 0; i0 < n; i0 += kDrawThreads) {
-                    const int i = i0 + tid;
-                    u64 key = 0ull;
-                    if (i < n) {
-                        int l = 0, r = n_lists - 1;    // the last list that begins at i or before
-                        while (l < r) {
-                            const int m = (l + r + 1) / 2;
-                            if (offsets[m] <= i)
-                                l = m;
-                            else
-                                r = m - 1;
-                        }
-                        key = cand[(size_t)l * part + (i - offsets[l])];
+                    for (int i = lane; i < c; i += 64) {
+                        const u64 key = from[i];
+                        const float x = key_value(key);
+                        if (x >= low && bin_of(x) <= deepest)
+                            f(key);
                     }
-                    __syncthreads();
-                    if (i < n)
-                        cand[i] = key;
-                    __syncthreads();
                 }
-                out = draw_filtered(a, set, cand, n, gm, whole, d, u, lds);
+            };
+            const Row r = {a, set, gm, whole, d, u};
+            if (whole_count > (u64)kFew && (set.k > 0 || set.p < 1.0f)) {
+                // many: a histogram of all of them tells how deep the kept ones go
+                if (low <= -3.402823466e38f) {
+                    float v = __builtin_huge_valf();
+                    listed([&](u64 key) { v = fminf(v, key_value(key)); });
+                    low = -block_max(-v, lds.fl);
+                }
+                if (gm > low && gm - low < __builtin_huge_valf())
+                    scale = (float)kBins / (gm - low);
+                const bool by_count = set.k > 0;
+                const u64 target = by_count ? (u64)set.k : r.share(fixed(whole, a.bits));
+                lds.hist[tid] = 0ull;
+                if (tid == 0)
+                    lds.at = -1;
+                __syncthreads();
+                listed([&](u64 key) {
+                    atomicAdd(&lds.hist[bin_of(key_value(key))], by_count ? 1ull : r.units(key, gm));
+                });
+                __syncthreads();
+                const int bin = border_bin(0ull, target, lds);
+                deepest = bin >= 0 ? bin : deepest;
+                __syncthreads();
             }
+            if (tid == 0)
+                lds.n = 0;
+            __syncthreads();
+            listed([&](u64 key) {
+                const u64 m = __ballot(true);
+                int at = 0;
+                if (lane == __builtin_ctzll(m))
+                    at = atomicAdd(&lds.n, __popcll(m));
+                at = __shfl(at, __builtin_ctzll(m)) + lane_rank(m);
+                if (at < kCap)
+                    lds.keys[at] = key;
+            });
+            __syncthreads();
+            const int n = lds.n;
+            if (n <= kFew)
+                out = draw_few(r, n, lds);
+            else if (n <= kCap)
+                out = draw_many(r, [&](auto &&f) {
+                    for (int i = tid; i < n; i += kDrawThreads)
+                        f(lds.keys[i]);
+                }, lds);
+            else
+                out = draw_many(r, listed, lds);
         }
     }
     if (tid == 0) {
@@ -609,18 +743,19 @@ __global__ void __launch_bounds__(kDrawThreads) sample_draw_kernel(SampleArgs a)
 // ---------------------------------------------------------------- host side
 
 struct Layout {
-    size_t cand, counts, tops, sums, maxes, draft_logit, tickets, oks, bytes;
+    size_t cand, counts, tops, bars, sums, maxes, draft_logit, tickets, oks, bytes;
 };
 
 Layout layout_for(int R, int T, int V)
 {
     Layout l;
     const size_t M = (size_t)R * T, chunks = (V + kChunk - 1) / kChunk;
-    const size_t lists = chunks + kMaxWaves;   // with one more, at most
+    const size_t lists = chunks + kMaxWaves;   // at most
     l.cand = 0;
     l.counts = l.cand + round256(M * V * 8);
     l.tops = l.counts + round256(M * lists * 4);
-    l.sums = l.tops + round256(M * lists * 4);
+    l.bars = l.tops + round256(M * lists * 4);
+    l.sums = l.bars + round256(M * lists * 4);
     l.maxes = l.sums + round256(M * chunks * 8);
     l.draft_logit = l.maxes + round256(M * chunks * 4);
     l.tickets = l.draft_logit + round256(M * 4);
@@ -701,6 +836,7 @@ int sample_logits_rows(const void *logits, int64_t logits_stride, int dtype, con
     a.cand = reinterpret_cast<u64 *>(ws + l.cand);
     a.counts = reinterpret_cast<int *>(ws + l.counts);
     a.tops = reinterpret_cast<float *>(ws + l.tops);
+    a.bars = reinterpret_cast<float *>(ws + l.bars);
     a.sums = reinterpret_cast<double *>(ws + l.sums);
     a.maxes = reinterpret_cast<float *>(ws + l.maxes);
     a.draft_logit = reinterpret_cast<float *>(ws + l.draft_logit);
