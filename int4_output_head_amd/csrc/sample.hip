@@ -34,6 +34,7 @@ constexpr int kDrawThreads = 1024;
 constexpr int kCap = 4096;                // candidates that the drawing kernel holds in LDS
 constexpr int kFew = 512;                 // and those that it compares with each other
 constexpr int kBins = kDrawThreads;
+constexpr int kHeld = 1024;
 
 struct SampleArgs : RulesArgs {
     int4vh_sampling s;
@@ -84,11 +85,32 @@ __device__ __forceinline__ Settings load_settings(const SampleArgs &a, int req)
     return s;
 }
 
+// exp(z) for z <= 0, of relative error below 2^-42: z = n ln 2 + r with |r| <=
+// ln(2) / 2, and the power series of exp(r) to the tenth power, whose rest is at
+// most 0.3466^11 / 11! * 1.05 = 2.4e-13.  0 where it is below 2^-1022 by far.
+__device__ __forceinline__ double exp_below(double z)
+{
+    const double n = rint(z * 1.4426950408889634);
+    const double r = __builtin_fma(n, -1.9082149292705877e-10, __builtin_fma(n, -6.93147180369123816490e-01, z));
+    double p = 2.7557319223985893e-07;        // 1 / 10!
+    p = __builtin_fma(p, r, 2.7557319223985888e-06);
+    p = __builtin_fma(p, r, 2.4801587301587302e-05);
+    p = __builtin_fma(p, r, 1.9841269841269841e-04);
+    p = __builtin_fma(p, r, 1.3888888888888889e-03);
+    p = __builtin_fma(p, r, 8.3333333333333332e-03);
+    p = __builtin_fma(p, r, 4.1666666666666664e-02);
+    p = __builtin_fma(p, r, 1.6666666666666666e-01);
+    p = __builtin_fma(p, r, 0.5);
+    p = __builtin_fma(p, r, 1.0);
+    p = __builtin_fma(p, r, 1.0);
+    return z > -1000.0 ? __builtin_amdgcn_ldexp(p, (int)n) : 0.0;
+}
+
 // The mass of a value x at most m, relative to that of m; 1 at m itself, so that
 // infinities do not meet, and 0 for -infinity and NaN.
 __device__ __forceinline__ double mass_below(float x, float m, double inv_t)
 {
-    return x == m ? 1.0 : x > kNegInf ? exp(((double)x - (double)m) * inv_t) : 0.0;
+    return x == m ? 1.0 : x > kNegInf ? exp_below(((double)x - (double)m) * inv_t) : 0.0;
 }
 
 // How far below a row's largest value m a kept token may lie, with slack for the
@@ -249,9 +271,11 @@ __device__ __forceinline__ u64 block_scan(u64 v, u64 *s, u64 &total)
 
 struct DrawLds {
     u64 keys[kCap];                           // candidates, in any order
-    u64 units[kFew];                          // and masses of few
+    u64 few[kFew];                            // few of them that are compared with each other,
+    u64 units[kFew];                          // and their masses
     u64 hist[kBins];
     uint32_t hits[kBins];
+    int counts[kHeld];                        // of the first lists
     __attribute__((aligned(16))) uint32_t words[2 * kChunk];   // the rules' words of one chunk
     u64 scan[16];
     float fl[16];
@@ -287,13 +311,27 @@ __device__ __forceinline__ u64 token_key(u64 key)
     return key & 0xFFFFFFull;
 }
 
-// The bin, of lds.hist as the threads have filled it from the top, in which the
-// sum from the top on reaches `target` (-1: none does); lds.rest is the sum
-// above it.
-__device__ __forceinline__ int border_bin(u64 above, u64 target, DrawLds &lds)
+// lds.hist emptied, and no bin found.
+__device__ __forceinline__ void clear_bins(DrawLds &lds)
 {
+    lds.hist[threadIdx.x] = 0ull;
+    if (threadIdx.x == 0) {
+        lds.at = -1;
+        lds.n = 0;
+    }
+    __syncthreads();
+}
+
+// The bin, of lds.hist as the threads have filled it, in which the sum from the
+// first on reaches target_of(sum of all) (-1: none does); lds.rest is the sum in
+// front of it.
+template <class Target>
+__device__ __forceinline__ int border_bin(u64 above, DrawLds &lds, Target &&target_of)
+{
+    __syncthreads();
     u64 total;
     const u64 mine = lds.hist[threadIdx.x], upto = block_scan(mine, lds.scan, total) + above;
+    const u64 target = target_of(total);
     if (upto - mine < target && upto >= target) {
         lds.at = threadIdx.x;
         lds.rest = upto - mine;
@@ -315,11 +353,8 @@ __device__ __forceinline__ u64 border(Each &&each, u64 lo, u64 hi, u64 target, D
     while (true) {
         // bins of 2^shift keys, from hi down
         const int width = hi > lo ? 64 - __builtin_clzll(hi - lo) : 1, shift = width > 10 ? width - 10 : 0;
-        lds.hist[tid] = 0ull;
         lds.hits[tid] = 0u;
-        if (tid == 0)
-            lds.at = -1;
-        __syncthreads();
+        clear_bins(lds);
         each([&](u64 key) {
             const u64 o = order(key);
             if (o >= lo && o <= hi) {
@@ -331,8 +366,7 @@ __device__ __forceinline__ u64 border(Each &&each, u64 lo, u64 hi, u64 target, D
                 }
             }
         });
-        __syncthreads();
-        const int bin = border_bin(above, target, lds);
+        const int bin = border_bin(above, lds, [&](u64) { return target; });
         if (bin < 0)
             return 0ull;
         above = lds.rest;
@@ -382,83 +416,249 @@ struct Row {
     }
 };
 
-// Few candidates, n <= kFew of lds.keys: each is compared with all others, by a
-// group of threads, which gives its rank and the mass in front of it; once
-// more by token for the sum that draws.
+// Appends to an array in LDS, at most kMost of them; the lanes that call it.
+template <int kMost>
+__device__ __forceinline__ void append(u64 key, u64 *to, int *n)
+{
+    const u64 m = __ballot(true);
+    const int first = __builtin_ctzll(m);
+    int at = 0;
+    if ((int)(threadIdx.x & 63) == first)
+        at = atomicAdd(n, __popcll(m));
+    at = __shfl(at, first) + lane_rank(m);
+    if (at < kMost)
+        to[at] = key;
+}
+
+// A group of threads for each of n <= kFew keys of lds.few, all of which it
+// compares with its own: the lead has the results.
+struct Ranked {
+    int i, rank;                              // rank: the number of larger keys
+    bool mine, lead;
+    u64 key, before;                          // before: what they weigh
+    int group;
+
+    __device__ __forceinline__ Ranked(int n, const DrawLds &lds)
+    {
+        group = kDrawThreads / kFew;
+        while (group < 64 && 2 * group * n <= kDrawThreads)
+            group *= 2;
+        i = threadIdx.x / group;
+        mine = i < n;
+        lead = mine && threadIdx.x % group == 0;
+        key = mine ? lds.few[i] : 0ull;
+    }
+    // with the masses in lds.units
+    template <class Order>
+    __device__ __forceinline__ void rank_by(int n, const DrawLds &lds, Order &&order)
+    {
+        rank = 0;
+        before = 0ull;
+        const u64 own = order(key);
+        for (int j = threadIdx.x % group; j < n; j += group) {
+            const bool more = order(lds.few[j]) > own;
+            rank += more;
+            before += more ? lds.units[j] : 0ull;
+        }
+        for (int off = 1; off < group; off <<= 1) {
+            rank += __shfl_xor(rank, off);
+            before += shfl_xor64(before, off);
+        }
+    }
+};
+
+// The token at which the sum of the masses by token exceeds `target`, less
+// `front` that lies before the n keys of lds.few with masses lds.units.
+__device__ __forceinline__ void draw_ranked(Ranked &k, int n, u64 w, u64 front, u64 target, double share, DrawLds &lds)
+{
+    k.rank_by(n, lds, token_key);
+    if (k.lead && front + k.before <= target && target < front + k.before + w) {
+        lds.at = key_token(k.key);
+        lds.value = (float)share;
+    }
+    __syncthreads();
+}
+
+// Few candidates, n <= kFew, in lds.few.
 __device__ __forceinline__ Draw draw_few(const Row &r, int n, DrawLds &lds)
 {
-    const int tid = threadIdx.x;
-    int group = kDrawThreads / kFew;          // threads a key
-    while (group < 64 && 2 * group * n <= kDrawThreads)
-        group *= 2;
-    const int i = tid / group, sub = tid % group;
-    const bool mine = i < n;
-    const u64 key = mine ? lds.keys[i] : 0ull;
-    const u64 own = mine ? r.units(key, r.gm) : 0ull;
-    if (mine && sub == 0)
-        lds.units[i] = own;
-    if (tid == 0)
+    Ranked k(n, lds);
+    const u64 own = k.mine ? r.units(k.key, r.gm) : 0ull;
+    if (k.lead)
+        lds.units[k.i] = own;
+    if (threadIdx.x == 0)
         lds.some = 0;
     __syncthreads();
-    int rank = 0;
-    u64 before = 0ull;
-    for (int j = sub; j < n; j += group) {
-        const bool more = lds.keys[j] > key;
-        rank += more;
-        before += more ? lds.units[j] : 0ull;
-    }
-    for (int off = 1; off < group; off <<= 1) {
-        rank += __shfl_xor(rank, off);
-        before += shfl_xor64(before, off);
-    }
-    const bool lead = mine && sub == 0;
-    bool kept = mine && (r.set.k == 0 || rank < r.set.k);
+    k.rank_by(n, lds, [](u64 key) { return key; });
+    bool kept = k.mine && (r.set.k == 0 || k.rank < r.set.k);
     if (r.set.p < 1.0f) {
         u64 all;
         if (r.set.k > 0)
-            block_scan(lead && kept ? own : 0ull, lds.scan, all);
+            block_scan(k.lead && kept ? own : 0ull, lds.scan, all);
         else
             all = fixed(r.whole, r.a.bits);
-        kept = kept && before < r.share(all);
+        kept = kept && k.before < r.share(all);
     }
-    kept = kept && (r.set.mp <= 0.0f || r.mass(key, r.gm) >= (double)r.set.mp);
+    kept = kept && (r.set.mp <= 0.0f || r.mass(k.key, r.gm) >= (double)r.set.mp);
     Draw out = {-1, 0.0f, 0.0f};
     float ref = r.gm;
     u64 w = kept ? own : 0ull;
     if (r.d >= 0) {
         u64 all;
-        block_scan(lead ? w : 0ull, lds.scan, all);
-        const bool draft = kept && key_token(key) == r.d;
-        if (draft && sub == 0) {
+        block_scan(k.lead ? w : 0ull, lds.scan, all);
+        const bool draft = kept && key_token(k.key) == r.d;
+        if (draft && k.lead) {
             lds.some = 1;
-            lds.value = (float)(r.mass(key, r.gm) / floating(all, r.a.bits));
+            lds.value = (float)(r.mass(k.key, r.gm) / floating(all, r.a.bits));
         }
         kept = kept && !draft;
-        ref = block_max(kept ? key_value(key) : kNegInf, lds.fl);
+        ref = block_max(kept ? key_value(k.key) : kNegInf, lds.fl);
         out.p_draft = lds.some ? lds.value : 0.0f;
         if (ref == kNegInf)
             return out;
-        w = kept ? r.units(key, ref) : 0ull;
+        w = kept ? r.units(k.key, ref) : 0ull;
     }
     u64 total;
-    block_scan(lead ? w : 0ull, lds.scan, total);
-    if (lead)
-        lds.units[i] = w;
+    block_scan(k.lead ? w : 0ull, lds.scan, total);
+    if (k.lead)
+        lds.units[k.i] = w;
     __syncthreads();
-    before = 0ull;
-    for (int j = sub; j < n; j += group)
-        before += token_key(lds.keys[j]) > token_key(key) ? lds.units[j] : 0ull;
-    for (int off = 1; off < group; off <<= 1)
-        before += shfl_xor64(before, off);
-    const u64 target = drawn(r.u, total);
-    if (lead && before <= target && target < before + w) {
-        lds.at = key_token(key);
-        lds.value = (float)(r.mass(key, ref) / floating(total, r.a.bits));
-    }
-    __syncthreads();
+    draw_ranked(k, n, w, 0ull, drawn(r.u, total), w ? r.mass(k.key, ref) / floating(total, r.a.bits) : 0.0, lds);
     out.token = lds.at;
     out.prob = lds.value;
     return out;
+}
+
+// The keys of bin `bin` among the n of lds.keys, in lds.few; their number.
+template <class Bin>
+__device__ __forceinline__ int gather_bin(int n, int bin, DrawLds &lds, Bin &&bin_of)
+{
+    if (threadIdx.x == 0)
+        lds.n = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kDrawThreads)
+        if (bin_of(lds.keys[i]) == bin)
+            append<kFew>(lds.keys[i], lds.few, &lds.n);
+    __syncthreads();
+    return lds.n;
+}
+
+// The last key, by value, of bin `bin` whose predecessors weigh less than
+// `target` together, those in front of the bin `above`; false where the bin holds
+// too many.
+template <class Bin, class Weight>
+__device__ __forceinline__ bool border_of_bin(int n, int bin, u64 above, u64 target, DrawLds &lds, Bin &&bin_of,
+                                              Weight &&weight, u64 &least)
+{
+    const int m = gather_bin(n, bin, lds, bin_of);
+    if (m > kFew)
+        return false;
+    Ranked k(m, lds);
+    if (k.lead)
+        lds.units[k.i] = weight(k.key);
+    if (threadIdx.x == 0)
+        lds.found = ~0ull;
+    __syncthreads();
+    k.rank_by(m, lds, [](u64 key) { return key; });
+    if (k.lead && above + k.before < target)
+        atomicMin(&lds.found, value_key(k.key));
+    __syncthreads();
+    least = lds.found;
+    __syncthreads();
+    return true;
+}
+
+// n candidates in lds.keys, in bins by their value.  bin, above: the bin in which
+// the first filter's border lies and the weight in front of it (bin < 0: there is
+// none).  False where a bin holds too many.
+template <class Bin>
+__device__ __forceinline__ bool draw_held(const Row &r, int n, int bin, u64 above, u64 target, DrawLds &lds,
+                                          Bin &&bin_of, Draw &out)
+{
+    const Settings &set = r.set;
+    const int tid = threadIdx.x, bits = r.a.bits;
+    auto value_bin = [&](u64 key) { return bin_of(key_value(key)); };
+    auto units = [&](u64 key) { return r.units(key, r.gm); };
+    u64 least = 0ull;
+    if (set.k > 0) {
+        if (bin >= 0 && !border_of_bin(n, bin, above, target, lds, value_bin, [](u64) { return 1ull; }, least))
+            return false;
+        bin = -1;
+        if (set.p < 1.0f) {
+            clear_bins(lds);
+            for (int i = tid; i < n; i += kDrawThreads)
+                if (value_key(lds.keys[i]) >= least)
+                    atomicAdd(&lds.hist[value_bin(lds.keys[i])], units(lds.keys[i]));
+            bin = border_bin(0ull, lds, [&](u64 all) { return target = r.share(all); });
+            above = lds.rest;
+            __syncthreads();
+        }
+    }
+    if (bin >= 0) {
+        u64 last;
+        if (!border_of_bin(n, bin, above, target, lds, value_bin, units, last))
+            return false;
+        least = last > least ? last : least;
+    }
+    auto kept = [&](u64 key) {
+        return value_key(key) >= least && (set.mp <= 0.0f || r.mass(key, r.gm) >= (double)set.mp);
+    };
+    float ref = r.gm;
+    out.p_draft = 0.0f;
+    if (r.d >= 0) {
+        // the draft's share, and the largest value without it
+        if (tid == 0)
+            lds.some = 0;
+        float v = kNegInf;
+        u64 w = 0ull, all;
+        __syncthreads();
+        for (int i = tid; i < n; i += kDrawThreads) {
+            const u64 key = lds.keys[i];
+            if (kept(key)) {
+                w += units(key);
+                if (key_token(key) == r.d) {
+                    lds.some = 1;
+                    lds.value = key_value(key);
+                } else {
+                    v = fmaxf(v, key_value(key));
+                }
+            }
+        }
+        block_scan(w, lds.scan, all);
+        if (lds.some)
+            out.p_draft = (float)((set.t > 0.0f ? mass_below(lds.value, r.gm, set.inv_t) : 1.0) / floating(all, bits));
+        ref = block_max(v, lds.fl);
+        if (ref == kNegInf)
+            return true;
+    }
+    // by token: bins of 2^shift neighbours
+    const int shift = max(0, 32 - __builtin_clz(r.a.V) - 10);
+    auto drawable = [&](u64 key) { return kept(key) && key_token(key) != r.d ? r.units(key, ref) : 0ull; };
+    clear_bins(lds);
+    for (int i = tid; i < n; i += kDrawThreads) {
+        const u64 w = drawable(lds.keys[i]);
+        if (w)
+            atomicAdd(&lds.hist[key_token(lds.keys[i]) >> shift], w);
+    }
+    u64 total = 0ull;
+    bin = border_bin(0ull, lds, [&](u64 all) {
+        total = all;
+        return drawn(r.u, all) + 1ull;
+    });
+    above = lds.rest;
+    __syncthreads();
+    const int m = gather_bin(n, bin, lds, [&](u64 key) { return key_token(key) >> shift; });
+    if (m > kFew)
+        return false;
+    Ranked k(m, lds);
+    const u64 w = k.mine ? drawable(k.key) : 0ull;
+    if (k.lead)
+        lds.units[k.i] = w;
+    __syncthreads();
+    draw_ranked(k, m, w, above, drawn(r.u, total), w ? r.mass(k.key, ref) / floating(total, bits) : 0.0, lds);
+    out.token = lds.at;
+    out.prob = lds.value;
+    return true;
 }
 
 // Any number of them: the borders by histograms.  each(f): f with every
@@ -556,7 +756,10 @@ __global__ void __launch_bounds__(kDrawThreads) sample_draw_kernel(SampleArgs a)
     for (int i = tid; i < n_lists; i += kDrawThreads) {
         gm = fmaxf(gm, a.tops[(size_t)row * n_lists + i]);
         low = fmaxf(low, a.bars[(size_t)row * n_lists + i]);
-        n_all += (u64)counts[i];
+        const int c = counts[i];
+        n_all += (u64)c;
+        if (i < kHeld)
+            lds.counts[i] = c;
     }
     gm = block_max(gm, lds.fl);
     Draw out = {-1, 0.0f, 0.0f};
@@ -656,20 +859,40 @@ __global__ void __launch_bounds__(kDrawThreads) sample_draw_kernel(SampleArgs a)
             int deepest = kBins - 1;
             float scale = 0.0f;
             auto bin_of = [&](float x) { return x >= gm ? 0 : min((int)((gm - x) * scale), kBins - 1); };
+            // 4 lists and 2 keys of each lane at a time: the loads' latency counts
             auto listed = [&](auto &&f) {
-                for (int l = wave; l < n_lists; l += kDrawThreads / 64) {
-                    const int c = counts[l];
-                    const u64 *from = cand + (size_t)l * part;
-                    for (int i = lane; i < c; i += 64) {
-                        const u64 key = from[i];
-                        const float x = key_value(key);
-                        if (x >= low && bin_of(x) <= deepest)
-                            f(key);
+                constexpr int kLists = 4, kKeys = 2, kWaves = kDrawThreads / 64;
+                for (int l0 = wave; l0 < n_lists; l0 += kLists * kWaves) {
+                    int c[kLists], most = 0;
+#pragma unroll
+                    for (int j = 0; j < kLists; ++j) {
+                        const int l = l0 + j * kWaves;
+                        c[j] = l >= n_lists ? 0 : l < kHeld ? lds.counts[l] : counts[l];
+                        most = max(most, c[j]);
+                    }
+                    for (int i0 = lane; i0 - lane < most; i0 += 64 * kKeys) {
+                        u64 key[kLists][kKeys];
+#pragma unroll
+                        for (int j = 0; j < kLists; ++j)
+#pragma unroll
+                            for (int k = 0; k < kKeys; ++k)
+                                key[j][k] = i0 + 64 * k < c[j] ? cand[(size_t)(l0 + j * kWaves) * part + i0 + 64 * k] : 0ull;
+#pragma unroll
+                        for (int j = 0; j < kLists; ++j)
+#pragma unroll
+                            for (int k = 0; k < kKeys; ++k)
+                                if (key[j][k]) {
+                                    const float x = key_value(key[j][k]);
+                                    if (x >= low && bin_of(x) <= deepest)
+                                        f(key[j][k]);
+                                }
                     }
                 }
             };
             const Row r = {a, set, gm, whole, d, u};
-            if (whole_count > (u64)kFew && (set.k > 0 || set.p < 1.0f)) {
+            int bin = -1;
+            u64 above = 0ull, target = 0ull;
+            if (whole_count > (u64)kFew) {
                 // many: a histogram of all of them tells how deep the kept ones go
                 if (low <= -3.402823466e38f) {
                     float v = __builtin_huge_valf();
@@ -678,42 +901,41 @@ __global__ void __launch_bounds__(kDrawThreads) sample_draw_kernel(SampleArgs a)
                 }
                 if (gm > low && gm - low < __builtin_huge_valf())
                     scale = (float)kBins / (gm - low);
-                const bool by_count = set.k > 0;
-                const u64 target = by_count ? (u64)set.k : r.share(fixed(whole, a.bits));
-                lds.hist[tid] = 0ull;
-                if (tid == 0)
-                    lds.at = -1;
-                __syncthreads();
-                listed([&](u64 key) {
-                    atomicAdd(&lds.hist[bin_of(key_value(key))], by_count ? 1ull : r.units(key, gm));
-                });
-                __syncthreads();
-                const int bin = border_bin(0ull, target, lds);
-                deepest = bin >= 0 ? bin : deepest;
-                __syncthreads();
+                if (set.k > 0 || set.p < 1.0f) {
+                    const bool by_count = set.k > 0;
+                    target = by_count ? (u64)set.k : r.share(fixed(whole, a.bits));
+                    clear_bins(lds);
+                    listed([&](u64 key) {
+                        atomicAdd(&lds.hist[bin_of(key_value(key))], by_count ? 1ull : r.units(key, gm));
+                    });
+                    bin = border_bin(0ull, lds, [&](u64) { return target; });
+                    above = lds.rest;
+                    deepest = bin >= 0 ? bin : deepest;
+                    __syncthreads();
+                }
             }
             if (tid == 0)
                 lds.n = 0;
             __syncthreads();
-            listed([&](u64 key) {
-                const u64 m = __ballot(true);
-                int at = 0;
-                if (lane == __builtin_ctzll(m))
-                    at = atomicAdd(&lds.n, __popcll(m));
-                at = __shfl(at, __builtin_ctzll(m)) + lane_rank(m);
-                if (at < kCap)
-                    lds.keys[at] = key;
-            });
+            if (whole_count <= (u64)kFew)
+                listed([&](u64 key) { append<kFew>(key, lds.few, &lds.n); });
+            else
+                listed([&](u64 key) { append<kCap>(key, lds.keys, &lds.n); });
             __syncthreads();
             const int n = lds.n;
-            if (n <= kFew)
+            bool done = false;
+            if (n <= kFew) {
+                if (whole_count > (u64)kFew) {
+                    if (tid < n)
+                        lds.few[tid] = lds.keys[tid];
+                    __syncthreads();
+                }
                 out = draw_few(r, n, lds);
-            else if (n <= kCap)
-                out = draw_many(r, [&](auto &&f) {
-                    for (int i = tid; i < n; i += kDrawThreads)
-                        f(lds.keys[i]);
-                }, lds);
-            else
+                done = true;
+            } else if (n <= kCap) {
+                done = draw_held(r, n, bin, above, target, lds, bin_of, out);
+            }
+            if (!done)
                 out = draw_many(r, listed, lds);
         }
     }

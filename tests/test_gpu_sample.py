@@ -312,6 +312,18 @@ def test_longest_rows(b):
         check(got, x.double().numpy(), [s], u)
 
 
+@pytest.mark.parametrize("n", [300, 700, 5000])
+def test_fewer_tokens_than_top_k(b, n):
+    """A row that holds no top_k tokens above -infinity: top_p and min_p still hold."""
+    V = 9000
+    x = torch.full((4, V), -math.inf)
+    x[:, 1000:1000 + n] = torch.randn(4, n, generator=torch.Generator().manual_seed(n))
+    u = torch.tensor([0.1, 0.5, 0.9, 0.999])
+    for s in ((1.0, n + 50, 0.6, 0.0), (2.0, 8000, 0.9, 0.1), (1.0, n + 1, 1.0, 0.2), (1.0, n, 0.3, 0.0)):
+        got = b.sample_logits(x.cuda(), u.cuda(), R=4, temperature=s[0], top_k=s[1], top_p=s[2], min_p=s[3])
+        check(got, x.double().numpy(), [s] * 4, u)
+
+
 def test_binding_refusals(b):
     x, d, u, accept = (t.cuda() for t in speculative(2, 3, 100, 1))
     ok = dict(logits=x, uniforms=u, draft_ids=d, R=2)
