@@ -341,10 +341,10 @@ struct SliceWalk {
 
     // Part way_at of n_ways of the S tokens from `first` on, in row t_at of
     // request req_at.  s_mem: the slice's words, then its entries where they lie
-    // apart.  The whole workgroup counts the slice, whose first chunks are on
-    // their way meanwhile.
+    // apart.  The whole workgroup counts the slice, while each wave's chunk
+    // `begins` is on its way.
     __device__ __forceinline__ SliceWalk(const RulesArgs &args, uint32_t *s_mem, int first, int S, int req_at,
-                                         int t_at, int way_at, int n_ways)
+                                         int t_at, int way_at, int n_ways, int begins = 0)
         : a(args)
     {
         lane = threadIdx.x & 63;
@@ -362,7 +362,7 @@ struct SliceWalk {
         lrow = static_cast<const char *>(a.logits) + (size_t)row * a.logits_stride * kSize;
         ha.bits = hb.bits = 0u;
         if (n_chunks > 0)
-            load_x(0, ha);                    // on its way while the slice is counted
+            load_x(begins, ha);               // on its way while the slice is counted
         const Spans span = load_spans(a, req);
         mask = nullptr;
         none = false;
@@ -374,7 +374,7 @@ struct SliceWalk {
         }
         mask_words = (V + 31) / 32;
         if (n_chunks > 0)
-            load_bits(0, ha);
+            load_bits(begins, ha);
         if (a.has_penalty || a.has_bias)
             prepare_slice(a, span, base, S, words, entries);
         bias = a.has_bias ? a.r.bias_values + span.bb : nullptr;
@@ -470,6 +470,31 @@ struct SliceWalk {
                 rule(begin + (c + 1) * kChunk, hb);
                 use(begin + (c + 1) * kChunk, hb.x);
             }
+        }
+    }
+
+    // The same for the chunks of a mask, not 0, whose lowest is the one that the
+    // walk begins with.
+    template <class Use>
+    __device__ __forceinline__ void run_some(uint32_t chunks, Use &&use)
+    {
+        while (true) {
+            int c = __builtin_ctz(chunks);
+            chunks &= chunks - 1u;
+            if (chunks)
+                load(__builtin_ctz(chunks), hb);
+            rule(begin + c * kChunk, ha);
+            use(begin + c * kChunk, ha.x);
+            if (!chunks)
+                break;
+            c = __builtin_ctz(chunks);
+            chunks &= chunks - 1u;
+            if (chunks)
+                load(__builtin_ctz(chunks), ha);
+            rule(begin + c * kChunk, hb);
+            use(begin + c * kChunk, hb.x);
+            if (!chunks)
+                break;
         }
     }
 };

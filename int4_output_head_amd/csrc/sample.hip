@@ -1,18 +1,20 @@
 // sample.hip -- tokens drawn from logits by given uniform numbers, for MI355X
 // (gfx950); definitions in int4vh_sample.h.
 //
-// Two kernels.  sample_scan_kernel walks the rows as the verification under
+// Three kernels.  sample_scan_kernel walks the rows as the verification under
 // rules does (SliceWalk: the logits are read once, under their rules) and
-// leaves of each row either the sums of its chunks of 1024 tokens, or the
-// candidates that a filter may keep, or both.  What can be kept is bounded from
-// what a wave has seen: a value that lies more than temperature * ln(1 / min_p)
-// below its largest one has too little mass; under top_p, one that lies more
-// than temperature * ln(V / (1 - top_p)) below, because all tokens behind it
-// together would have less than 1 - top_p of the best one's mass; under top_k
-// up to 64, one below the k-th of the 64 lanes' largest values.
-// sample_draw_kernel, a workgroup per row, joins these: the borders of top_k
-// and top_p are found by histograms of counts and masses over the keys' range,
-// refined around the border, and the token by a sum over tokens in their order.
+// leaves of each chunk of 1024 tokens the largest value, and where a setting
+// asks for it the sum of the masses, or a value that several of its tokens
+// reach.  With no filter a token is drawn from these, and from one chunk that is
+// read again.  Otherwise they bound what can be kept: under min_p, nothing more
+// than temperature * ln(1 / min_p) below the largest value; under top_p, nothing
+// more than temperature * ln(V / (1 - top_p)) below, because all tokens behind it
+// together would have less than 1 - top_p of the best one's mass; under top_k,
+// nothing below a value that top_k tokens reach.  sample_collect_kernel reads the
+// chunks whose largest value passes, a few of them as a rule, and puts what
+// passes side by side; sample_draw_kernel, a workgroup per row, finds the
+// borders of top_k and top_p among that by histograms of counts and masses, and
+// the token by one over tokens.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -34,19 +36,19 @@ constexpr int kDrawThreads = 1024;
 constexpr int kCap = 4096;                // candidates that the drawing kernel holds in LDS
 constexpr int kFew = 512;                 // and those that it compares with each other
 constexpr int kBins = kDrawThreads;
-constexpr int kHeld = 1024;
 
 struct SampleArgs : RulesArgs {
     int4vh_sampling s;
     const float *uniforms;     // [R*T]
     const float *accept;       // [R, T-1] or null
     int bits;                  // masses are multiples of 2^-bits
-    u64 *cand;                 // [R*T, V] candidates' keys; a list begins at its wave's first token
-    int *counts;               // [R*T, n_lists] candidates of each list
-    float *tops;               // [R*T, n_lists] largest value of each wave's tokens
-    float *bars;               // [R*T, n_lists] what it knows that a kept token reaches
-    double *sums;              // [R*T, chunks] mass of each chunk, less the row's draft where drafts are verified
-    float *maxes;              // [R*T, chunks] what it is relative to: the largest value
+    float *tops;               // [R*T, chunks] largest value
+    float *bars;               // [R*T, chunks] value that each() of the chunk's tokens reach, under top_k
+    float *refs;               // [R*T, chunks] largest value, less the row's draft where drafts are verified,
+    double *sums;              // [R*T, chunks] and the masses' sum relative to it, likewise
+    u64 *cand;                 // [R*T, V] candidates' keys, in any order,
+    int *counts;               // [R*T] their number
+    float *lows;               // [R*T] and a value that all of them reach
     float *draft_logit;        // [R*T] ruled logit of the row's draft, where it is in [0, V)
     uint32_t *tickets;         // [R] rows done
     uint32_t *oks;             // [R*T] whether the row's draft is accepted
@@ -57,13 +59,21 @@ struct SampleArgs : RulesArgs {
 
 // A request's settings: k = 0, p = 1 and mp = 0 keep all.
 struct Settings {
-    double inv_t;
+    double inv_t;                             // log2(e) / temperature
     float t;
     int k;
     float p, mp;
     __device__ __forceinline__ bool filtered() const { return k > 0 || p < 1.0f || mp > 0.0f; }
     // whether the sums of the chunks are wanted
     __device__ __forceinline__ bool summed() const { return k == 0 && (p < 1.0f || mp <= 0.0f); }
+    // under top_k: tokens of each of n chunks, so that some of the chunks have top_k of them
+    __device__ __forceinline__ int each(int n) const
+    {
+        int j = 1;
+        while (j < 64 && (long long)j * n < 2ll * k)
+            j *= 2;
+        return j;
+    }
 };
 __device__ __forceinline__ Settings load_settings(const SampleArgs &a, int req)
 {
@@ -81,28 +91,25 @@ __device__ __forceinline__ Settings load_settings(const SampleArgs &a, int req)
         s.p = 1.0f;
         s.mp = 0.0f;
     }
-    s.inv_t = s.t > 0.0f ? 1.0 / (double)s.t : 0.0;
+    s.inv_t = s.t > 0.0f ? 1.4426950408889634 / (double)s.t : 0.0;
     return s;
 }
 
-// exp(z) for z <= 0, of relative error below 2^-42: z = n ln 2 + r with |r| <=
-// ln(2) / 2, and the power series of exp(r) to the tenth power, whose rest is at
-// most 0.3466^11 / 11! * 1.05 = 2.4e-13.  0 where it is below 2^-1022 by far.
-__device__ __forceinline__ double exp_below(double z)
+// 2^z for z <= 0, of relative error 2^-40: the whole part of z by ldexp, the rest,
+// |f| <= 1/2, by the polynomial of degree 8 whose largest relative error is least
+// (7.8e-13, by exchange of its extrema).  0 where it is below 2^-1022 by far.
+__device__ __forceinline__ double exp2_below(double z)
 {
-    const double n = rint(z * 1.4426950408889634);
-    const double r = __builtin_fma(n, -1.9082149292705877e-10, __builtin_fma(n, -6.93147180369123816490e-01, z));
-    double p = 2.7557319223985893e-07;        // 1 / 10!
-    p = __builtin_fma(p, r, 2.7557319223985888e-06);
-    p = __builtin_fma(p, r, 2.4801587301587302e-05);
-    p = __builtin_fma(p, r, 1.9841269841269841e-04);
-    p = __builtin_fma(p, r, 1.3888888888888889e-03);
-    p = __builtin_fma(p, r, 8.3333333333333332e-03);
-    p = __builtin_fma(p, r, 4.1666666666666664e-02);
-    p = __builtin_fma(p, r, 1.6666666666666666e-01);
-    p = __builtin_fma(p, r, 0.5);
-    p = __builtin_fma(p, r, 1.0);
-    p = __builtin_fma(p, r, 1.0);
+    const double n = rint(z), f = z - n;
+    double p = 1.3175858136257845e-06;
+    p = __builtin_fma(p, f, 1.5309737421323303e-05);
+    p = __builtin_fma(p, f, 1.540385174860361e-04);
+    p = __builtin_fma(p, f, 1.3333452062251618e-03);
+    p = __builtin_fma(p, f, 9.618128542862621e-03);
+    p = __builtin_fma(p, f, 5.550410939341707e-02);
+    p = __builtin_fma(p, f, 2.4022650698880368e-01);
+    p = __builtin_fma(p, f, 6.931471805465141e-01);
+    p = __builtin_fma(p, f, 9.999999999997623e-01);
     return z > -1000.0 ? __builtin_amdgcn_ldexp(p, (int)n) : 0.0;
 }
 
@@ -110,7 +117,7 @@ __device__ __forceinline__ double exp_below(double z)
 // infinities do not meet, and 0 for -infinity and NaN.
 __device__ __forceinline__ double mass_below(float x, float m, double inv_t)
 {
-    return x == m ? 1.0 : x > kNegInf ? exp_below(((double)x - (double)m) * inv_t) : 0.0;
+    return x == m ? 1.0 : x > kNegInf ? exp2_below(((double)x - (double)m) * inv_t) : 0.0;
 }
 
 // How far below a row's largest value m a kept token may lie, with slack for the
@@ -143,45 +150,31 @@ __global__ void __launch_bounds__(64 * kMaxWaves) sample_scan_kernel(SampleArgs 
 {
     extern __shared__ __attribute__((aligned(16))) uint32_t s_mem[];
     SliceWalk<kDtype> walk(a, s_mem);
-    if (blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0)
-        a.tickets[blockIdx.y] = 0u;
+    if (blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x < a.T) {
+        a.counts[blockIdx.y * a.T + threadIdx.x] = 0;
+        if (threadIdx.x == 0)
+            a.tickets[blockIdx.y] = 0u;
+    }
     if (!walk.live())
         return;                               // no barrier follows
     walk.load_request();
     const int lane = walk.lane, row = walk.row, d = walk.d, V = a.V;
     const Settings set = load_settings(a, walk.req);
-    const bool filtered = set.filtered(), summed = set.summed();
-    const int n_all = (V + kChunk - 1) / kChunk;
-    u64 *list = a.cand + (size_t)row * V + walk.begin;
-    int n = 0;                                // candidates written
-    float top = kNegInf;                      // this lane's largest value
-    float from = -3.402823466e38f;            // candidates are at least this
+    const bool summed = set.summed();
+    const int n_chunks = (V + kChunk - 1) / kChunk, each = set.k > 0 ? set.each(n_chunks) : 1;
     walk.run([&](int chunk0, float (&x)[kPer]) {
+        const size_t at = (size_t)row * n_chunks + chunk0 / kChunk;
         float best = kNegInf;                 // fmaxf passes over NaN
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
             best = fmaxf(best, x[i]);
-        const bool more = best > top;
-        top = fmaxf(top, best);
-        if (filtered && __ballot(best >= from)) {
-            if (__ballot(more)) {
-                const float m = wave_max(top);
-                from = fmaxf(from, m - reach_of(set, V, m));
-                if (set.k > 0 && set.k <= 64) {
-                    const uint32_t th = reach_threshold(top > kNegInf ? order_word(top) : 0u, set.k);
-                    if (th > 1u)
-                        from = fmaxf(from, word_value(th));
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const u64 m = __ballot(x[i] >= from);
-                if (m) {
-                    if (x[i] >= from)
-                        list[n + lane_rank(m)] = order_key(x[i], chunk0 + 64 * i + lane);
-                    n += __popcll(m);
-                }
-            }
+        float m = wave_max(best);
+        if (lane == 0)
+            a.tops[at] = m;
+        if (each > 1) {
+            const uint32_t th = reach_threshold(best > kNegInf ? order_word(best) : 0u, each);
+            if (lane == 0)
+                a.bars[at] = th > 1u ? word_value(th) : kNegInf;
         }
         const uint32_t da = (uint32_t)d - (uint32_t)chunk0;
         if (d >= 0 && d < V && da < (uint32_t)kChunk) {
@@ -199,27 +192,130 @@ __global__ void __launch_bounds__(64 * kMaxWaves) sample_scan_kernel(SampleArgs 
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
                 best = fmaxf(best, x[i]);
+            m = wave_max(best);
         }
         if (summed) {
-            const float m = wave_max(best);
             double s = 0.0;
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
                 s += mass_below(x[i], m, set.inv_t);
             s = wave_sum_f64(s);
             if (lane == 0) {
-                a.maxes[(size_t)row * n_all + chunk0 / kChunk] = m;
-                a.sums[(size_t)row * n_all + chunk0 / kChunk] = m > kNegInf ? s : 0.0;
+                a.refs[at] = m;
+                a.sums[at] = m > kNegInf ? s : 0.0;
             }
         }
     });
-    const float m = wave_max(top);
-    if (lane == 0) {
-        const size_t slot = (size_t)row * a.n_lists + blockIdx.x * a.ways + walk.way;
-        a.counts[slot] = n;
-        a.tops[slot] = m;
-        a.bars[slot] = from;
+}
+
+// The row's largest value, and one that nothing that is kept lies below, from
+// what the scan has left of its chunks.  A whole wave.
+constexpr int kGroups = 4;                    // groups of chunks per lane
+__device__ __forceinline__ float lowest_kept(const SampleArgs &a, const Settings &set, int row, int lane, float &gm)
+{
+    const int n = (a.V + kChunk - 1) / kChunk, each = set.k > 0 ? set.each(n) : 1;
+    const float *tops = a.tops + (size_t)row * n, *bars = each > 1 ? a.bars + (size_t)row * n : tops;
+    float most[kGroups], m = kNegInf;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g)
+        most[g] = kNegInf;
+    for (int c0 = 0; c0 < n; c0 += 64 * kGroups)
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+            if (c0 + 64 * g + lane < n) {
+                m = fmaxf(m, tops[c0 + 64 * g + lane]);
+                most[g] = fmaxf(most[g], bars[c0 + 64 * g + lane]);
+            }
+    gm = wave_max(m);
+    float low = gm - reach_of(set, a.V, gm);  // (NaN: no bound)
+    low = fmaxf(low, -3.402823466e38f);
+    const int want = set.k > 0 ? (set.k + each - 1) / each : 0;
+    if (want > 0 && want <= n && want <= 64 * kGroups) {
+        // a word that at least `want` groups reach, two bits at a time
+        uint32_t word[kGroups], th = 0u;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+            word[g] = most[g] > kNegInf ? order_word(most[g]) : 0u;
+        auto reach = [&](uint32_t w) {
+            int c = 0;
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g)
+                c += __popcll(__ballot(word[g] >= w));
+            return c;
+        };
+        if (reach(1u) >= want) {
+#pragma nounroll
+            for (int shift = 30; shift >= 0; shift -= 2) {
+                const uint32_t bits = reach(th | 3u << shift) >= want   ? 3u
+                                      : reach(th | 2u << shift) >= want ? 2u
+                                      : reach(th | 1u << shift) >= want ? 1u
+                                                                        : 0u;
+                th |= bits << shift;
+            }
+            low = fmaxf(low, word_value(th));
+        }
     }
+    return low;
+}
+
+// Grid and workgroups of the scan; chunks whose largest value is too low are not
+// read again.
+template <int kDtype>
+__global__ void __launch_bounds__(64 * kMaxWaves) sample_collect_kernel(SampleArgs a)
+{
+    extern __shared__ __attribute__((aligned(16))) uint32_t s_mem[];
+    __shared__ int s_any;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int req = blockIdx.y, t = blockIdx.z * a.row_group + wave / a.ways, way = wave % a.ways;
+    const Settings set = load_settings(a, req);
+    if (!set.filtered())
+        return;
+    if (threadIdx.x == 0)
+        s_any = 0;
+    __syncthreads();
+    const bool live = t < a.T && t < (int)(blockIdx.z + 1) * a.row_group;
+    const int V = a.V, n_chunks = (V + kChunk - 1) / kChunk, row = req * a.T + t;
+    const int part = a.slice / a.ways / kChunk, c0 = blockIdx.x * (a.slice / kChunk) + way * part;
+    float gm = kNegInf, low = kNegInf;
+    uint32_t chunks = 0u;
+    if (live) {
+        low = lowest_kept(a, set, row, lane, gm);
+        const bool more = lane < part && c0 + lane < n_chunks && a.tops[(size_t)row * n_chunks + c0 + lane] >= low;
+        chunks = (uint32_t)__ballot(more);
+        if (chunks && lane == 0)
+            s_any = 1;
+        if (blockIdx.x == 0 && way == 0 && lane == 0)
+            a.lows[row] = low;
+    }
+    __syncthreads();
+    if (!s_any)
+        return;
+    SliceWalk<kDtype> walk(a, s_mem, blockIdx.x * a.slice, a.slice, req, t, way, a.ways,
+                           chunks ? __builtin_ctz(chunks) : 0);
+    if (!chunks)
+        return;                               // no barrier follows
+    walk.load_request();
+    u64 *cand = a.cand + (size_t)row * V;
+    walk.run_some(chunks, [&](int chunk0, float (&x)[kPer]) {
+        u64 m[kPer];
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            m[i] = __ballot(x[i] >= low);
+            n += __popcll(m[i]);
+        }
+        int at = 0;
+        if (lane == 0)
+            at = atomicAdd(&a.counts[row], n);
+        at = __builtin_amdgcn_readfirstlane(at);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (m[i]) {
+                if (x[i] >= low)
+                    cand[at + lane_rank(m[i])] = order_key(x[i], chunk0 + 64 * i + lane);
+                at += __popcll(m[i]);
+            }
+    });
 }
 
 // ---------------------------------------------------------------- drawing
@@ -275,7 +371,6 @@ struct DrawLds {
     u64 units[kFew];                          // and their masses
     u64 hist[kBins];
     uint32_t hits[kBins];
-    int counts[kHeld];                        // of the first lists
     __attribute__((aligned(16))) uint32_t words[2 * kChunk];   // the rules' words of one chunk
     u64 scan[16];
     float fl[16];
@@ -482,6 +577,7 @@ __device__ __forceinline__ void draw_ranked(Ranked &k, int n, u64 w, u64 front, 
 // Few candidates, n <= kFew, in lds.few.
 __device__ __forceinline__ Draw draw_few(const Row &r, int n, DrawLds &lds)
 {
+    __syncthreads();
     Ranked k(n, lds);
     const u64 own = k.mine ? r.units(k.key, r.gm) : 0ull;
     if (k.lead)
@@ -744,37 +840,30 @@ __global__ void __launch_bounds__(kDrawThreads) sample_draw_kernel(SampleArgs a)
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int row = blockIdx.x, req = row / a.T, t = row % a.T, V = a.V;
     const Settings set = load_settings(a, req);
-    const int n_lists = a.n_lists, n_chunks = (V + kChunk - 1) / kChunk;
+    const int n_chunks = (V + kChunk - 1) / kChunk;
     const float u = a.uniforms[row];
     const bool drafted = a.accept && t < a.T - 1;
     const int d = drafted ? a.draft[(size_t)req * (a.T - 1) + t] : -1;
     const float xd = d >= 0 && d < V ? a.draft_logit[row] : kNegInf;
 
-    float gm = kNegInf, low = kNegInf;
-    u64 n_all = 0ull;
-    const int *counts = a.counts + (size_t)row * n_lists;
-    for (int i = tid; i < n_lists; i += kDrawThreads) {
-        gm = fmaxf(gm, a.tops[(size_t)row * n_lists + i]);
-        low = fmaxf(low, a.bars[(size_t)row * n_lists + i]);
-        const int c = counts[i];
-        n_all += (u64)c;
-        if (i < kHeld)
-            lds.counts[i] = c;
-    }
+    const float *tops = a.tops + (size_t)row * n_chunks;
+    float gm = kNegInf;
+    for (int c = tid; c < n_chunks; c += kDrawThreads)
+        gm = fmaxf(gm, tops[c]);
     gm = block_max(gm, lds.fl);
     Draw out = {-1, 0.0f, 0.0f};
     if (gm > kNegInf) {
         // the chunks' masses, the draft's apart
-        const float *maxes = a.maxes + (size_t)row * n_chunks;
+        const float *refs = a.refs + (size_t)row * n_chunks;
         const double *sums = a.sums + (size_t)row * n_chunks;
         float ref = kNegInf;
         u64 total = 0ull;
-        auto chunk_mass = [&](int c) { return fixed(sums[c] * mass_below(maxes[c], ref, set.inv_t), a.bits); };
+        auto chunk_mass = [&](int c) { return fixed(sums[c] * mass_below(refs[c], ref, set.inv_t), a.bits); };
         double whole = 0.0;                   // relative to gm, with the draft
         const double md = xd > kNegInf ? mass_below(xd, gm, set.inv_t) : 0.0;
         if (set.summed()) {
             for (int c = tid; c < n_chunks; c += kDrawThreads)
-                ref = fmaxf(ref, maxes[c]);
+                ref = fmaxf(ref, refs[c]);
             ref = block_max(ref, lds.fl);
             u64 w = 0ull;
             if (ref > kNegInf)
@@ -848,95 +937,59 @@ __global__ void __launch_bounds__(kDrawThreads) sample_draw_kernel(SampleArgs a)
                 out.prob = lds.value;
             }
         } else {
-            const int part = a.slice / a.ways;
             const u64 *cand = a.cand + (size_t)row * V;
-            u64 whole_count;
-            block_scan(n_all, lds.scan, whole_count);
-            // Candidates from the row's largest value down to `low`, which all
-            // waves' bounds hold for, in bins by their distance from it; those
-            // behind bin `deepest` are out.
-            low = fmaxf(block_max(low, lds.fl), gm - reach_of(set, V, gm));
-            int deepest = kBins - 1;
-            float scale = 0.0f;
-            auto bin_of = [&](float x) { return x >= gm ? 0 : min((int)((gm - x) * scale), kBins - 1); };
-            // 4 lists and 2 keys of each lane at a time: the loads' latency counts
-            auto listed = [&](auto &&f) {
-                constexpr int kLists = 4, kKeys = 2, kWaves = kDrawThreads / 64;
-                for (int l0 = wave; l0 < n_lists; l0 += kLists * kWaves) {
-                    int c[kLists], most = 0;
-#pragma unroll
-                    for (int j = 0; j < kLists; ++j) {
-                        const int l = l0 + j * kWaves;
-                        c[j] = l >= n_lists ? 0 : l < kHeld ? lds.counts[l] : counts[l];
-                        most = max(most, c[j]);
-                    }
-                    for (int i0 = lane; i0 - lane < most; i0 += 64 * kKeys) {
-                        u64 key[kLists][kKeys];
-#pragma unroll
-                        for (int j = 0; j < kLists; ++j)
-#pragma unroll
-                            for (int k = 0; k < kKeys; ++k)
-                                key[j][k] = i0 + 64 * k < c[j] ? cand[(size_t)(l0 + j * kWaves) * part + i0 + 64 * k] : 0ull;
-#pragma unroll
-                        for (int j = 0; j < kLists; ++j)
-#pragma unroll
-                            for (int k = 0; k < kKeys; ++k)
-                                if (key[j][k]) {
-                                    const float x = key_value(key[j][k]);
-                                    if (x >= low && bin_of(x) <= deepest)
-                                        f(key[j][k]);
-                                }
-                    }
-                }
-            };
+            const int n_cand = a.counts[row];
             const Row r = {a, set, gm, whole, d, u};
-            int bin = -1;
-            u64 above = 0ull, target = 0ull;
-            if (whole_count > (u64)kFew) {
-                // many: a histogram of all of them tells how deep the kept ones go
-                if (low <= -3.402823466e38f) {
-                    float v = __builtin_huge_valf();
-                    listed([&](u64 key) { v = fminf(v, key_value(key)); });
-                    low = -block_max(-v, lds.fl);
-                }
-                if (gm > low && gm - low < __builtin_huge_valf())
-                    scale = (float)kBins / (gm - low);
+            if (n_cand <= kFew) {
+                if (tid < n_cand)
+                    lds.few[tid] = cand[tid];
+                out = draw_few(r, n_cand, lds);
+            } else {
+                // many: a histogram, by their distance from the largest value, of
+                // all of them tells how deep the kept ones go
+                const float low = a.lows[row];
+                const float scale = gm > low && gm - low < __builtin_huge_valf() ? (float)kBins / (gm - low) : 0.0f;
+                auto bin_of = [&](float x) { return x >= gm ? 0 : min((int)((gm - x) * scale), kBins - 1); };
+                int bin = -1;
+                u64 above = 0ull, target = 0ull;
                 if (set.k > 0 || set.p < 1.0f) {
                     const bool by_count = set.k > 0;
                     target = by_count ? (u64)set.k : r.share(fixed(whole, a.bits));
                     clear_bins(lds);
-                    listed([&](u64 key) {
-                        atomicAdd(&lds.hist[bin_of(key_value(key))], by_count ? 1ull : r.units(key, gm));
-                    });
+#pragma unroll 4
+                    for (int i = tid; i < n_cand; i += kDrawThreads)
+                        atomicAdd(&lds.hist[bin_of(key_value(cand[i]))], by_count ? 1ull : r.units(cand[i], gm));
                     bin = border_bin(0ull, lds, [&](u64) { return target; });
                     above = lds.rest;
-                    deepest = bin >= 0 ? bin : deepest;
-                    __syncthreads();
                 }
-            }
-            if (tid == 0)
-                lds.n = 0;
-            __syncthreads();
-            if (whole_count <= (u64)kFew)
-                listed([&](u64 key) { append<kFew>(key, lds.few, &lds.n); });
-            else
-                listed([&](u64 key) { append<kCap>(key, lds.keys, &lds.n); });
-            __syncthreads();
-            const int n = lds.n;
-            bool done = false;
-            if (n <= kFew) {
-                if (whole_count > (u64)kFew) {
+                const int deepest = bin >= 0 ? bin : kBins - 1;
+                __syncthreads();
+                if (tid == 0)
+                    lds.n = 0;
+                __syncthreads();
+#pragma unroll 4
+                for (int i = tid; i < n_cand; i += kDrawThreads) {
+                    const u64 key = cand[i];
+                    if (bin_of(key_value(key)) <= deepest)
+                        append<kCap>(key, lds.keys, &lds.n);
+                }
+                __syncthreads();
+                const int n = lds.n;
+                bool done = false;
+                if (n <= kFew) {
                     if (tid < n)
                         lds.few[tid] = lds.keys[tid];
-                    __syncthreads();
+                    out = draw_few(r, n, lds);
+                    done = true;
+                } else if (n <= kCap) {
+                    done = draw_held(r, n, bin, above, target, lds, bin_of, out);
                 }
-                out = draw_few(r, n, lds);
-                done = true;
-            } else if (n <= kCap) {
-                done = draw_held(r, n, bin, above, target, lds, bin_of, out);
+                if (!done)
+                    out = draw_many(r, [&](auto &&f) {
+                        for (int i = tid; i < n_cand; i += kDrawThreads)
+                            f(cand[i]);
+                    }, lds);
             }
-            if (!done)
-                out = draw_many(r, listed, lds);
         }
     }
     if (tid == 0) {
@@ -965,25 +1018,32 @@ __global__ void __launch_bounds__(kDrawThreads) sample_draw_kernel(SampleArgs a)
 // ---------------------------------------------------------------- host side
 
 struct Layout {
-    size_t cand, counts, tops, bars, sums, maxes, draft_logit, tickets, oks, bytes;
+    size_t cand, tops, bars, refs, sums, counts, lows, draft_logit, tickets, oks, bytes;
 };
 
 Layout layout_for(int R, int T, int V)
 {
     Layout l;
     const size_t M = (size_t)R * T, chunks = (V + kChunk - 1) / kChunk;
-    const size_t lists = chunks + kMaxWaves;   // at most
     l.cand = 0;
-    l.counts = l.cand + round256(M * V * 8);
-    l.tops = l.counts + round256(M * lists * 4);
-    l.bars = l.tops + round256(M * lists * 4);
-    l.sums = l.bars + round256(M * lists * 4);
-    l.maxes = l.sums + round256(M * chunks * 8);
-    l.draft_logit = l.maxes + round256(M * chunks * 4);
+    l.tops = round256(M * V * 8);
+    l.bars = l.tops + round256(M * chunks * 4);
+    l.refs = l.bars + round256(M * chunks * 4);
+    l.sums = l.refs + round256(M * chunks * 4);
+    l.counts = l.sums + round256(M * chunks * 8);
+    l.lows = l.counts + round256(M * 4);
+    l.draft_logit = l.lows + round256(M * 4);
     l.tickets = l.draft_logit + round256(M * 4);
     l.oks = l.tickets + round256((size_t)R * 4);
     l.bytes = l.oks + round256(M * 4);
     return l;
+}
+
+// Whether a request may have a filter, as far as the host can tell.
+bool may_filter(const int4vh_sampling &s)
+{
+    return s.temperatures || s.top_ks || s.top_ps || s.min_ps || !(s.temperature > 0.0f) || s.top_k > 0 ||
+           s.top_p < 1.0f || s.min_p > 0.0f;
 }
 
 template <int kDtype>
@@ -993,6 +1053,11 @@ hipError_t launch(const SampleArgs &a, const Shape &sh, hipStream_t s)
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
+    if (may_filter(a.s)) {
+        hipLaunchKernelGGL(sample_collect_kernel<kDtype>, sh.grid, sh.block, sh.lds, s, a);
+        if ((e = hipGetLastError()) != hipSuccess)
+            return e;
+    }
     hipLaunchKernelGGL(sample_draw_kernel<kDtype>, dim3(a.R * a.T), dim3(kDrawThreads), 0, s, a);
     return hipGetLastError();
 }
@@ -1056,11 +1121,12 @@ int sample_logits_rows(const void *logits, int64_t logits_stride, int dtype, con
     while ((1 << (62 - a.bits)) < V)
         --a.bits;
     a.cand = reinterpret_cast<u64 *>(ws + l.cand);
-    a.counts = reinterpret_cast<int *>(ws + l.counts);
     a.tops = reinterpret_cast<float *>(ws + l.tops);
     a.bars = reinterpret_cast<float *>(ws + l.bars);
+    a.refs = reinterpret_cast<float *>(ws + l.refs);
     a.sums = reinterpret_cast<double *>(ws + l.sums);
-    a.maxes = reinterpret_cast<float *>(ws + l.maxes);
+    a.counts = reinterpret_cast<int *>(ws + l.counts);
+    a.lows = reinterpret_cast<float *>(ws + l.lows);
     a.draft_logit = reinterpret_cast<float *>(ws + l.draft_logit);
     a.tickets = reinterpret_cast<uint32_t *>(ws + l.tickets);
     a.oks = reinterpret_cast<uint32_t *>(ws + l.oks);
