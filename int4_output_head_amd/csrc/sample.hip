@@ -33,9 +33,12 @@ namespace {
 using namespace int4vh_detail;
 
 constexpr int kDrawThreads = 1024;
-constexpr int kCap = 4096;                // candidates that the drawing kernel holds in LDS
-constexpr int kFew = 512;                 // and those that it compares with each other
+constexpr int kFew = 512;                 // candidates that are compared with each other
 constexpr int kBins = kDrawThreads;
+
+// Words between counters that workgroups of all XCDs add to: a cache line each
+// (side by side, 256 rows' collection took 100 us instead of 30).
+constexpr int kPad = 32;
 
 struct SampleArgs : RulesArgs {
     int4vh_sampling s;
@@ -47,7 +50,7 @@ struct SampleArgs : RulesArgs {
     float *refs;               // [R*T, chunks] largest value, less the row's draft where drafts are verified,
     double *sums;              // [R*T, chunks] and the masses' sum relative to it, likewise
     u64 *cand;                 // [R*T, V] candidates' keys, in any order,
-    int *counts;               // [R*T] their number
+    int *counts;               // [R*T][kPad] their number
     float *lows;               // [R*T] and a value that all of them reach
     float *draft_logit;        // [R*T] ruled logit of the row's draft, where it is in [0, V)
     uint32_t *tickets;         // [R] rows done
@@ -95,12 +98,14 @@ __device__ __forceinline__ Settings load_settings(const SampleArgs &a, int req)
     return s;
 }
 
-// 2^z for z <= 0, of relative error 2^-40: the whole part of z by ldexp, the rest,
-// |f| <= 1/2, by the polynomial of degree 8 whose largest relative error is least
-// (7.8e-13, by exchange of its extrema).  0 where it is below 2^-1022 by far.
+// 2^z for z <= 0 (NaN and values below -1000 count as -1000), of relative error
+// 2^-40: the whole part of z goes into the exponent, the rest, |f| <= 1/2, through
+// the polynomial of degree 8 whose largest relative error is least (7.8e-13, by
+// exchange of its extrema).
 __device__ __forceinline__ double exp2_below(double z)
 {
-    const double n = rint(z), f = z - n;
+    z = fmax(z, -1000.0);
+    const double t = z + 0x1.8p52, f = z - (t - 0x1.8p52);     // t holds the whole part in its low word
     double p = 1.3175858136257845e-06;
     p = __builtin_fma(p, f, 1.5309737421323303e-05);
     p = __builtin_fma(p, f, 1.540385174860361e-04);
@@ -110,7 +115,7 @@ __device__ __forceinline__ double exp2_below(double z)
     p = __builtin_fma(p, f, 2.4022650698880368e-01);
     p = __builtin_fma(p, f, 6.931471805465141e-01);
     p = __builtin_fma(p, f, 9.999999999997623e-01);
-    return z > -1000.0 ? __builtin_amdgcn_ldexp(p, (int)n) : 0.0;
+    return __hiloint2double(__double2hiint(p) + (__double2loint(t) << 20), __double2loint(p));
 }
 
 // The mass of a value x at most m, relative to that of m; 1 at m itself, so that
@@ -151,7 +156,7 @@ __global__ void __launch_bounds__(64 * kMaxWaves) sample_scan_kernel(SampleArgs 
     extern __shared__ __attribute__((aligned(16))) uint32_t s_mem[];
     SliceWalk<kDtype> walk(a, s_mem);
     if (blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x < a.T) {
-        a.counts[blockIdx.y * a.T + threadIdx.x] = 0;
+        a.counts[(blockIdx.y * a.T + threadIdx.x) * kPad] = 0;
         if (threadIdx.x == 0)
             a.tickets[blockIdx.y] = 0u;
     }
@@ -196,9 +201,16 @@ __global__ void __launch_bounds__(64 * kMaxWaves) sample_scan_kernel(SampleArgs 
         }
         if (summed) {
             double s = 0.0;
+            if (fabsf(m) < __builtin_huge_valf()) {
+                // -infinity and NaN come out as 2^-1000
 #pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                s += mass_below(x[i], m, set.inv_t);
+                for (int i = 0; i < kPer; ++i)
+                    s += exp2_below(((double)x[i] - (double)m) * set.inv_t);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    s += x[i] == m ? 1.0 : 0.0;
+            }
             s = wave_sum_f64(s);
             if (lane == 0) {
                 a.refs[at] = m;
@@ -306,7 +318,7 @@ __global__ void __launch_bounds__(64 * kMaxWaves) sample_collect_kernel(SampleAr
         }
         int at = 0;
         if (lane == 0)
-            at = atomicAdd(&a.counts[row], n);
+            at = atomicAdd(&a.counts[row * kPad], n);
         at = __builtin_amdgcn_readfirstlane(at);
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
@@ -366,8 +378,7 @@ __device__ __forceinline__ u64 block_scan(u64 v, u64 *s, u64 &total)
 }
 
 struct DrawLds {
-    u64 keys[kCap];                           // candidates, in any order
-    u64 few[kFew];                            // few of them that are compared with each other,
+    u64 few[kFew];                            // few candidates that are compared with each other,
     u64 units[kFew];                          // and their masses
     u64 hist[kBins];
     uint32_t hits[kBins];
@@ -625,28 +636,50 @@ __device__ __forceinline__ Draw draw_few(const Row &r, int n, DrawLds &lds)
     return out;
 }
 
-// The keys of bin `bin` among the n of lds.keys, in lds.few; their number.
-template <class Bin>
-__device__ __forceinline__ int gather_bin(int n, int bin, DrawLds &lds, Bin &&bin_of)
+// f with each of the n candidates, some loads in flight.
+template <class F>
+__device__ __forceinline__ void each_of(const u64 *cand, int n, F &&f)
+{
+    constexpr int kFly = 4;
+    for (int i0 = threadIdx.x; i0 - (int)threadIdx.x < n; i0 += kFly * kDrawThreads) {
+        u64 key[kFly];
+#pragma unroll
+        for (int j = 0; j < kFly; ++j)
+            key[j] = i0 + j * kDrawThreads < n ? cand[i0 + j * kDrawThreads] : 0ull;
+#pragma nounroll
+        for (int j = 0; j < kFly; ++j) {       // one copy of f: the keys move down
+            if (key[0])
+                f(key[0]);
+#pragma unroll
+            for (int k = 0; k + 1 < kFly; ++k)
+                key[k] = key[k + 1];
+        }
+    }
+}
+
+// Those of the n candidates for which take() holds, in lds.few; their number.
+template <class Take>
+__device__ __forceinline__ int gather(const u64 *cand, int n, DrawLds &lds, Take &&take)
 {
     if (threadIdx.x == 0)
         lds.n = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kDrawThreads)
-        if (bin_of(lds.keys[i]) == bin)
-            append<kFew>(lds.keys[i], lds.few, &lds.n);
+    each_of(cand, n, [&](u64 key) {
+        if (take(key))
+            append<kFew>(key, lds.few, &lds.n);
+    });
     __syncthreads();
     return lds.n;
 }
 
-// The last key, by value, of bin `bin` whose predecessors weigh less than
-// `target` together, those in front of the bin `above`; false where the bin holds
-// too many.
-template <class Bin, class Weight>
-__device__ __forceinline__ bool border_of_bin(int n, int bin, u64 above, u64 target, DrawLds &lds, Bin &&bin_of,
-                                              Weight &&weight, u64 &least)
+// The last key, by value, of those that take() takes (a bin) whose predecessors
+// weigh less than `target` together, those in front of the bin `above`; false
+// where these are too many.
+template <class Take, class Weight>
+__device__ __forceinline__ bool border_among(const u64 *cand, int n, u64 above, u64 target, DrawLds &lds, Take &&take,
+                                             Weight &&weight, u64 &least)
 {
-    const int m = gather_bin(n, bin, lds, bin_of);
+    const int m = gather(cand, n, lds, take);
     if (m > kFew)
         return false;
     Ranked k(m, lds);
@@ -664,42 +697,52 @@ __device__ __forceinline__ bool border_of_bin(int n, int bin, u64 above, u64 tar
     return true;
 }
 
-// n candidates in lds.keys, in bins by their value.  bin, above: the bin in which
-// the first filter's border lies and the weight in front of it (bin < 0: there is
-// none).  False where a bin holds too many.
-template <class Bin>
-__device__ __forceinline__ bool draw_held(const Row &r, int n, int bin, u64 above, u64 target, DrawLds &lds,
-                                          Bin &&bin_of, Draw &out)
+// n candidates, from the largest value down to `low`.  False where a bin holds too
+// many of them.
+__device__ __forceinline__ bool draw_binned(const Row &r, const u64 *cand, int n, float low, DrawLds &lds, Draw &out)
 {
     const Settings &set = r.set;
     const int tid = threadIdx.x, bits = r.a.bits;
-    auto value_bin = [&](u64 key) { return bin_of(key_value(key)); };
-    auto units = [&](u64 key) { return r.units(key, r.gm); };
-    u64 least = 0ull;
+    // bins by the distance from the largest value
+    const float gm = r.gm, scale = gm > low && gm - low < __builtin_huge_valf() ? (float)kBins / (gm - low) : 0.0f;
+    auto bin_of = [&](u64 key) {
+        const float x = key_value(key);
+        return x >= gm ? 0 : min((int)((gm - x) * scale), kBins - 1);
+    };
+    auto units = [&](u64 key) { return r.units(key, gm); };
+    u64 least = 0ull, target = 0ull;
     if (set.k > 0) {
-        if (bin >= 0 && !border_of_bin(n, bin, above, target, lds, value_bin, [](u64) { return 1ull; }, least))
+        clear_bins(lds);
+        each_of(cand, n, [&](u64 key) { atomicAdd(&lds.hist[bin_of(key)], 1ull); });
+        const int bin = border_bin(0ull, lds, [&](u64) { return (u64)set.k; });
+        const u64 above = lds.rest;
+        __syncthreads();
+        if (bin >= 0 && !border_among(cand, n, above, (u64)set.k, lds, [&](u64 key) { return bin_of(key) == bin; },
+                                      [](u64) { return 1ull; }, least))
             return false;
-        bin = -1;
-        if (set.p < 1.0f) {
-            clear_bins(lds);
-            for (int i = tid; i < n; i += kDrawThreads)
-                if (value_key(lds.keys[i]) >= least)
-                    atomicAdd(&lds.hist[value_bin(lds.keys[i])], units(lds.keys[i]));
-            bin = border_bin(0ull, lds, [&](u64 all) { return target = r.share(all); });
-            above = lds.rest;
-            __syncthreads();
-        }
     }
-    if (bin >= 0) {
-        u64 last;
-        if (!border_of_bin(n, bin, above, target, lds, value_bin, units, last))
+    if (set.p < 1.0f) {
+        clear_bins(lds);
+        each_of(cand, n, [&](u64 key) {
+            if (value_key(key) >= least)
+                atomicAdd(&lds.hist[bin_of(key)], units(key));
+        });
+        const int bin = border_bin(0ull, lds, [&](u64 all) {
+            return target = r.share(set.k > 0 ? all : fixed(r.whole, bits));
+        });
+        const u64 above = lds.rest;
+        __syncthreads();
+        u64 last = 0ull;
+        if (bin >= 0 && !border_among(cand, n, above, target, lds,
+                                      [&](u64 key) { return bin_of(key) == bin && value_key(key) >= least; }, units,
+                                      last))
             return false;
         least = last > least ? last : least;
     }
     auto kept = [&](u64 key) {
-        return value_key(key) >= least && (set.mp <= 0.0f || r.mass(key, r.gm) >= (double)set.mp);
+        return value_key(key) >= least && (set.mp <= 0.0f || r.mass(key, gm) >= (double)set.mp);
     };
-    float ref = r.gm;
+    float ref = gm;
     out.p_draft = 0.0f;
     if (r.d >= 0) {
         // the draft's share, and the largest value without it
@@ -708,8 +751,7 @@ __device__ __forceinline__ bool draw_held(const Row &r, int n, int bin, u64 abov
         float v = kNegInf;
         u64 w = 0ull, all;
         __syncthreads();
-        for (int i = tid; i < n; i += kDrawThreads) {
-            const u64 key = lds.keys[i];
+        each_of(cand, n, [&](u64 key) {
             if (kept(key)) {
                 w += units(key);
                 if (key_token(key) == r.d) {
@@ -719,10 +761,10 @@ __device__ __forceinline__ bool draw_held(const Row &r, int n, int bin, u64 abov
                     v = fmaxf(v, key_value(key));
                 }
             }
-        }
+        });
         block_scan(w, lds.scan, all);
         if (lds.some)
-            out.p_draft = (float)((set.t > 0.0f ? mass_below(lds.value, r.gm, set.inv_t) : 1.0) / floating(all, bits));
+            out.p_draft = (float)((set.t > 0.0f ? mass_below(lds.value, gm, set.inv_t) : 1.0) / floating(all, bits));
         ref = block_max(v, lds.fl);
         if (ref == kNegInf)
             return true;
@@ -731,19 +773,19 @@ __device__ __forceinline__ bool draw_held(const Row &r, int n, int bin, u64 abov
     const int shift = max(0, 32 - __builtin_clz(r.a.V) - 10);
     auto drawable = [&](u64 key) { return kept(key) && key_token(key) != r.d ? r.units(key, ref) : 0ull; };
     clear_bins(lds);
-    for (int i = tid; i < n; i += kDrawThreads) {
-        const u64 w = drawable(lds.keys[i]);
+    each_of(cand, n, [&](u64 key) {
+        const u64 w = drawable(key);
         if (w)
-            atomicAdd(&lds.hist[key_token(lds.keys[i]) >> shift], w);
-    }
+            atomicAdd(&lds.hist[key_token(key) >> shift], w);
+    });
     u64 total = 0ull;
-    bin = border_bin(0ull, lds, [&](u64 all) {
+    const int bin = border_bin(0ull, lds, [&](u64 all) {
         total = all;
         return drawn(r.u, all) + 1ull;
     });
-    above = lds.rest;
+    const u64 above = lds.rest;
     __syncthreads();
-    const int m = gather_bin(n, bin, lds, [&](u64 key) { return key_token(key) >> shift; });
+    const int m = gather(cand, n, lds, [&](u64 key) { return key_token(key) >> shift == bin && kept(key); });
     if (m > kFew)
         return false;
     Ranked k(m, lds);
@@ -890,47 +932,26 @@ __global__ void __launch_bounds__(kDrawThreads) sample_draw_kernel(SampleArgs a)
                 __syncthreads();
                 const int chunk = lds.at;
                 const u64 rest = lds.rest;
-                // that chunk once more, under its rules
+                // that chunk once more, under its rules: a token a thread
                 SliceWalk<kDtype> walk(a, lds.words, chunk * kChunk, kChunk, req, t, 0, 1);
+                float *ruled = reinterpret_cast<float *>(lds.few);
                 if (wave == 0) {
                     walk.load_request();
                     walk.rule(chunk * kChunk, walk.ha);
-                    u64 sum = 0ull;
-                    int token = -1, last = -1;
-                    float value = 0.0f, last_value = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < kPer; ++i) {
-                        const int v = chunk * kChunk + 64 * i + lane;
-                        const float x = drafted && v == d ? kNegInf : walk.ha.x[i];
-                        const u64 own = x > kNegInf ? fixed(mass_below(x, ref, set.inv_t), a.bits) : 0ull;
-                        u64 w = own;
-#pragma unroll
-                        for (int off = 1; off < 64; off <<= 1) {
-                            const u64 o = shfl_up64(w, off);
-                            w += lane >= off ? o : 0ull;
-                        }
-                        const u64 past = __ballot(own && sum + w > rest);
-                        if (past && token < 0) {
-                            const int at = __builtin_ctzll(past);
-                            token = chunk * kChunk + 64 * i + at;
-                            value = __shfl(x, at);
-                        }
-                        const u64 some = __ballot(own != 0ull);
-                        if (some) {           // the chunk's own sum may be a rounding less
-                            const int at = 63 - __builtin_clzll(some);
-                            last = chunk * kChunk + 64 * i + at;
-                            last_value = __shfl(x, at);
-                        }
-                        sum += readlane64(w, 63);
-                    }
-                    if (token < 0) {
-                        token = last;
-                        value = last_value;
-                    }
-                    if (lane == 0) {
-                        lds.at = token;
-                        lds.value = (float)(mass_below(value, ref, set.inv_t) / floating(total, a.bits));
-                    }
+                    for (int i = 0; i < kPer; ++i)
+                        ruled[64 * i + lane] = walk.ha.x[i];
+                }
+                __syncthreads();
+                const float x = drafted && chunk * kChunk + tid == d ? kNegInf : ruled[tid];
+                const u64 w = fixed(mass_below(x, ref, set.inv_t), a.bits);
+                u64 all;
+                const u64 upto = block_scan(w, lds.scan, all);
+                // the chunk's own sum may be a few roundings less: then its last token
+                const u64 goal = min(rest, all - 1ull);
+                if (upto - w <= goal && goal < upto) {
+                    lds.at = chunk * kChunk + tid;
+                    lds.value = (float)(mass_below(x, ref, set.inv_t) / floating(total, a.bits));
                 }
                 __syncthreads();
                 out.token = lds.at;
@@ -938,57 +959,14 @@ __global__ void __launch_bounds__(kDrawThreads) sample_draw_kernel(SampleArgs a)
             }
         } else {
             const u64 *cand = a.cand + (size_t)row * V;
-            const int n_cand = a.counts[row];
+            const int n_cand = a.counts[row * kPad];
             const Row r = {a, set, gm, whole, d, u};
             if (n_cand <= kFew) {
                 if (tid < n_cand)
                     lds.few[tid] = cand[tid];
                 out = draw_few(r, n_cand, lds);
-            } else {
-                // many: a histogram, by their distance from the largest value, of
-                // all of them tells how deep the kept ones go
-                const float low = a.lows[row];
-                const float scale = gm > low && gm - low < __builtin_huge_valf() ? (float)kBins / (gm - low) : 0.0f;
-                auto bin_of = [&](float x) { return x >= gm ? 0 : min((int)((gm - x) * scale), kBins - 1); };
-                int bin = -1;
-                u64 above = 0ull, target = 0ull;
-                if (set.k > 0 || set.p < 1.0f) {
-                    const bool by_count = set.k > 0;
-                    target = by_count ? (u64)set.k : r.share(fixed(whole, a.bits));
-                    clear_bins(lds);
-#pragma unroll 4
-                    for (int i = tid; i < n_cand; i += kDrawThreads)
-                        atomicAdd(&lds.hist[bin_of(key_value(cand[i]))], by_count ? 1ull : r.units(cand[i], gm));
-                    bin = border_bin(0ull, lds, [&](u64) { return target; });
-                    above = lds.rest;
-                }
-                const int deepest = bin >= 0 ? bin : kBins - 1;
-                __syncthreads();
-                if (tid == 0)
-                    lds.n = 0;
-                __syncthreads();
-#pragma unroll 4
-                for (int i = tid; i < n_cand; i += kDrawThreads) {
-                    const u64 key = cand[i];
-                    if (bin_of(key_value(key)) <= deepest)
-                        append<kCap>(key, lds.keys, &lds.n);
-                }
-                __syncthreads();
-                const int n = lds.n;
-                bool done = false;
-                if (n <= kFew) {
-                    if (tid < n)
-                        lds.few[tid] = lds.keys[tid];
-                    out = draw_few(r, n, lds);
-                    done = true;
-                } else if (n <= kCap) {
-                    done = draw_held(r, n, bin, above, target, lds, bin_of, out);
-                }
-                if (!done)
-                    out = draw_many(r, [&](auto &&f) {
-                        for (int i = tid; i < n_cand; i += kDrawThreads)
-                            f(cand[i]);
-                    }, lds);
+            } else if (!draw_binned(r, cand, n_cand, a.lows[row], lds, out)) {
+                out = draw_many(r, [&](auto &&f) { each_of(cand, n_cand, f); }, lds);
             }
         }
     }
@@ -1031,7 +1009,7 @@ Layout layout_for(int R, int T, int V)
     l.refs = l.bars + round256(M * chunks * 4);
     l.sums = l.refs + round256(M * chunks * 4);
     l.counts = l.sums + round256(M * chunks * 8);
-    l.lows = l.counts + round256(M * 4);
+    l.lows = l.counts + round256(M * 4 * kPad);
     l.draft_logit = l.lows + round256(M * 4);
     l.tickets = l.draft_logit + round256(M * 4);
     l.oks = l.tickets + round256((size_t)R * 4);
