@@ -8,8 +8,8 @@
 // reach.  With no filter a token is drawn from these, and from one chunk that is
 // read again.  Otherwise they bound what can be kept: under min_p, nothing more
 // than temperature * ln(1 / min_p) below the largest value; under top_p, nothing
-// more than temperature * ln(V / (1 - top_p)) below, because all tokens behind it
-// together would have less than 1 - top_p of the best one's mass; under top_k,
+// more than temperature * ln(V / ((1 - top_p) * mass of the row)) below, because
+// all tokens behind it together would have less than 1 - top_p of that; under top_k,
 // nothing below a value that top_k tokens reach.  sample_collect_kernel reads the
 // chunks whose largest value passes, a few of them as a rule, and puts what
 // passes side by side; sample_draw_kernel, a workgroup per row, finds the
@@ -126,9 +126,10 @@ __device__ __forceinline__ double mass_below(float x, float m, double inv_t)
 }
 
 // How far below a row's largest value m a kept token may lie, with slack for the
-// roundings of this bound.  Infinite where the settings do not bound it, and 0
-// below an infinite m, as long as they do.
-__device__ __forceinline__ float reach_of(const Settings &set, int V, float m)
+// roundings of this bound; the row has at least the mass `mass` relative to m.
+// Infinite where the settings do not bound it, and 0 below an infinite m, as long
+// as they do.
+__device__ __forceinline__ float reach_of(const Settings &set, int V, float m, float mass)
 {
     float reach = __builtin_huge_valf();
     if (set.t == 0.0f)
@@ -136,7 +137,7 @@ __device__ __forceinline__ float reach_of(const Settings &set, int V, float m)
     if (set.mp > 0.0f && (set.k == 0 || set.p >= 1.0f))
         reach = -set.t * logf(set.mp);
     if (set.p < 1.0f && set.k == 0)
-        reach = fminf(reach, set.t * logf((float)V / (1.0f - set.p)));
+        reach = fminf(reach, set.t * logf((float)V / ((1.0f - set.p) * mass)));
     if (reach == __builtin_huge_valf())
         return reach;
     return m == __builtin_huge_valf() ? 0.0f : reach * (1.0f + 0x1p-18f) + set.t * 0x1p-18f + fabsf(m) * 0x1p-20f;
@@ -239,10 +240,22 @@ __device__ __forceinline__ float lowest_kept(const SampleArgs &a, const Settings
                 most[g] = fmaxf(most[g], bars[c0 + 64 * g + lane]);
             }
     gm = wave_max(m);
-    float low = gm - reach_of(set, a.V, gm);  // (NaN: no bound)
+    float mass = 1.0f;
+    if (set.p < 1.0f && set.k == 0 && fabsf(gm) < __builtin_huge_valf()) {
+        // (without a draft that is apart: at least this)
+        const float *refs = a.refs + (size_t)row * n;
+        const double *sums = a.sums + (size_t)row * n;
+        float s = 0.0f;
+        for (int c = lane; c < n; c += 64)
+            s += refs[c] > kNegInf ? (float)sums[c] * exp2f((refs[c] - gm) * (float)set.inv_t) : 0.0f;
+        mass = fmaxf(mass, wave_sum(s) * (1.0f - 0x1p-10f));
+    }
+    float low = gm - reach_of(set, a.V, gm, mass);  // (NaN: no bound)
     low = fmaxf(low, -3.402823466e38f);
     const int want = set.k > 0 ? (set.k + each - 1) / each : 0;
-    if (want > 0 && want <= n && want <= 64 * kGroups) {
+    if (set.k == 1)
+        low = gm;
+    else if (want > 0 && want <= n && want <= 64 * kGroups) {
         // a word that at least `want` groups reach, two bits at a time
         uint32_t word[kGroups], th = 0u;
 #pragma unroll
@@ -263,6 +276,8 @@ __device__ __forceinline__ float lowest_kept(const SampleArgs &a, const Settings
                                       : reach(th | 1u << shift) >= want ? 1u
                                                                         : 0u;
                 th |= bits << shift;
+                if (bits && reach(th) <= want + 8)
+                    break;
             }
             low = fmaxf(low, word_value(th));
         }
@@ -636,20 +651,32 @@ __device__ __forceinline__ Draw draw_few(const Row &r, int n, DrawLds &lds)
     return out;
 }
 
-// f with each of the n candidates, some loads in flight.
+// f with each of the n >= 2 candidates, 2 * kFly of each thread in flight.
+struct __attribute__((aligned(8))) KeyPair { u64 a, b; };
 template <class F>
 __device__ __forceinline__ void each_of(const u64 *cand, int n, F &&f)
 {
-    constexpr int kFly = 4;
-    for (int i0 = threadIdx.x; i0 - (int)threadIdx.x < n; i0 += kFly * kDrawThreads) {
-        u64 key[kFly];
+    constexpr int kFly = 8;
+    for (int i0 = 0; i0 < n; i0 += 2 * kFly * kDrawThreads) {
+        KeyPair key[kFly];
 #pragma unroll
-        for (int j = 0; j < kFly; ++j)
-            key[j] = i0 + j * kDrawThreads < n ? cand[i0 + j * kDrawThreads] : 0ull;
+        for (int j = 0; j < kFly; ++j) {
+            const int i = i0 + 2 * (j * kDrawThreads + (int)threadIdx.x);
+            // (the last pair of an odd number begins one key earlier)
+            key[j] = KeyPair{0ull, 0ull};
+            if (i < n) {
+                key[j] = *reinterpret_cast<const KeyPair *>(cand + min(i, n - 2));
+                if (i + 1 == n)
+                    key[j] = KeyPair{key[j].b, 0ull};
+            }
+        }
+        // one copy of f, or two: the keys move down
 #pragma nounroll
-        for (int j = 0; j < kFly; ++j) {       // one copy of f: the keys move down
-            if (key[0])
-                f(key[0]);
+        for (int j = 0; j < kFly && i0 + 2 * j * kDrawThreads < n; ++j) {
+            if (key[0].a)
+                f(key[0].a);
+            if (key[0].b)
+                f(key[0].b);
 #pragma unroll
             for (int k = 0; k + 1 < kFly; ++k)
                 key[k] = key[k + 1];
@@ -742,47 +769,55 @@ __device__ __forceinline__ bool draw_binned(const Row &r, const u64 *cand, int n
     auto kept = [&](u64 key) {
         return value_key(key) >= least && (set.mp <= 0.0f || r.mass(key, gm) >= (double)set.mp);
     };
+    // by token, the draft's apart: bins of 2^shift neighbours
+    const int shift = max(0, 32 - __builtin_clz(r.a.V) - 10);
     float ref = gm;
+    auto drawable = [&](u64 key) { return kept(key) && key_token(key) != r.d ? r.units(key, ref) : 0ull; };
+    u64 total = 0ull;
+    auto token_bin = [&]() {
+        return border_bin(0ull, lds, [&](u64 all) {
+            total = all;
+            return drawn(r.u, all) + 1ull;
+        });
+    };
+    if (tid == 0)
+        lds.some = 0;
+    clear_bins(lds);
+    float v = kNegInf;                        // the largest value beside the draft's
+    each_of(cand, n, [&](u64 key) {
+        if (kept(key)) {
+            if (key_token(key) == r.d) {
+                lds.some = 1;
+                lds.value = key_value(key);
+            } else {
+                v = fmaxf(v, key_value(key));
+                const u64 w = units(key);
+                if (w)
+                    atomicAdd(&lds.hist[key_token(key) >> shift], w);
+            }
+        }
+    });
+    int bin = token_bin();
     out.p_draft = 0.0f;
     if (r.d >= 0) {
-        // the draft's share, and the largest value without it
-        if (tid == 0)
-            lds.some = 0;
-        float v = kNegInf;
-        u64 w = 0ull, all;
-        __syncthreads();
-        each_of(cand, n, [&](u64 key) {
-            if (kept(key)) {
-                w += units(key);
-                if (key_token(key) == r.d) {
-                    lds.some = 1;
-                    lds.value = key_value(key);
-                } else {
-                    v = fmaxf(v, key_value(key));
-                }
-            }
-        });
-        block_scan(w, lds.scan, all);
-        if (lds.some)
-            out.p_draft = (float)((set.t > 0.0f ? mass_below(lds.value, gm, set.inv_t) : 1.0) / floating(all, bits));
+        if (lds.some) {
+            const double md = set.t > 0.0f ? mass_below(lds.value, gm, set.inv_t) : 1.0;
+            out.p_draft = (float)(md / (md + floating(total, bits)));
+        }
         ref = block_max(v, lds.fl);
         if (ref == kNegInf)
             return true;
+        if (ref < gm) {
+            // the draft was the best token: masses relative to the next one
+            clear_bins(lds);
+            each_of(cand, n, [&](u64 key) {
+                const u64 w = drawable(key);
+                if (w)
+                    atomicAdd(&lds.hist[key_token(key) >> shift], w);
+            });
+            bin = token_bin();
+        }
     }
-    // by token: bins of 2^shift neighbours
-    const int shift = max(0, 32 - __builtin_clz(r.a.V) - 10);
-    auto drawable = [&](u64 key) { return kept(key) && key_token(key) != r.d ? r.units(key, ref) : 0ull; };
-    clear_bins(lds);
-    each_of(cand, n, [&](u64 key) {
-        const u64 w = drawable(key);
-        if (w)
-            atomicAdd(&lds.hist[key_token(key) >> shift], w);
-    });
-    u64 total = 0ull;
-    const int bin = border_bin(0ull, lds, [&](u64 all) {
-        total = all;
-        return drawn(r.u, all) + 1ull;
-    });
     const u64 above = lds.rest;
     __syncthreads();
     const int m = gather(cand, n, lds, [&](u64 key) { return key_token(key) >> shift == bin && kept(key); });
