@@ -479,17 +479,13 @@ __global__ void __launch_bounds__(64 * kWM *kWN) mx_tile_kernel(MxArgs a)
         if constexpr (i == 3)
             store_scales(lds.scale[sbuf ^ 1]);
     };
+    // whole spans: steps past K multiply zeros (a way out of the middle of a span
+    // would copy all sums)
     int sbuf = 0;
     for (int s = s0; s < s1; s += 4, sbuf ^= 1) {
         turn_step(s, sbuf, std::integral_constant<int, 0>());
-        if (s + 1 >= s1)
-            break;
         turn_step(s, sbuf, std::integral_constant<int, 1>());
-        if (s + 2 >= s1)
-            break;
         turn_step(s, sbuf, std::integral_constant<int, 2>());
-        if (s + 3 >= s1)
-            break;
         turn_step(s, sbuf, std::integral_constant<int, 3>());
     }
 
