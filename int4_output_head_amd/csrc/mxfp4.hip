@@ -2,14 +2,16 @@
 // between two matrices in that format, for MI355X (gfx950); formulas and order
 // of rounding in int4vh_mxfp4.h.
 //
-// The products run on v_mfma_scale_f32_16x16x128_f8f6f4 with both operands in
-// 4 bits: a lane holds 32 channels of one row, 16 bytes as they lie in memory,
-// and their scale, a byte that the instruction picks out of a register.  So a
-// 16-byte chunk of codes is an operand without any work on it, and LDS moves
-// what the codes take in memory.
+// The products run on v_mfma_scale_f32_16x16x128 and _32x32x64_f8f6f4 with both
+// operands in 4 bits: a lane holds 32 channels of one row, 16 bytes as they lie in
+// memory, and their scale, a byte that the instruction picks out of a register.
+// So a 16-byte chunk of codes is an operand without any work on it, and LDS moves
+// what the codes take in memory.  The larger form reaches 8.0 PFLOP/s on this
+// card in a loop of its own, the smaller one 5.9.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
+
 #include <stdint.h>
 #include <type_traits>
 
@@ -29,6 +31,7 @@ typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 struct __attribute__((packed, aligned(1))) Words1 { uint32_t w[4]; };
 
@@ -156,7 +159,7 @@ struct MxArgs {
     int M, N, K;
     int n_pad;                     // N rounded up to 4
     int activation, dtype;
-    int splits, split_steps;       // parts of K, and steps of 128 channels in each
+    int splits, split_spans;       // parts of K, and spans of 512 channels in each
     int tiles_m, tiles_n;
 };
 
@@ -168,6 +171,16 @@ __device__ __forceinline__ f32x4 mma(const u32x4 &w, const u32x4 &x, const f32x4
     const i32x8 A = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
     const i32x8 B = {(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0};
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, acc, 4, 4, kByte, (int)ws, kByte, (int)xs);
+}
+
+// 32 weight rows and 32 activation rows over 64 channels; the scales are byte
+// kByte of their registers.
+template <int kByte>
+__device__ __forceinline__ f32x16 mma32(const u32x4 &w, const u32x4 &x, const f32x16 &acc, uint32_t ws, uint32_t xs)
+{
+    const i32x8 A = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+    const i32x8 B = {(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(A, B, acc, 4, 4, kByte, (int)ws, kByte, (int)xs);
 }
 
 __device__ __forceinline__ float column_bias(const MxArgs &a, int n)
@@ -188,9 +201,10 @@ __device__ __forceinline__ void finish_one(const MxArgs &a, int m, int n, float 
         static_cast<uint16_t *>(a.out)[o] = (uint16_t)to_bits16(y[0], a.dtype);
 }
 
-// Four consecutive output elements n .. n+3 <= N-1 of row m; res: the
-// residual's 16-bit words where `with` is set.
-__device__ __forceinline__ void finish_four(const MxArgs &a, int m, int n, const f32x4 &acc, const float (&bias)[4],
+// Four consecutive output elements at `to`; res: the residual's 16-bit words where
+// `with` is set.
+template <int kDtype>
+__device__ __forceinline__ void finish_four(const MxArgs &a, void *to, const f32x4 &acc, const float (&bias)[4],
                                             bool with, uint2 res)
 {
     float y[4];
@@ -198,24 +212,23 @@ __device__ __forceinline__ void finish_four(const MxArgs &a, int m, int n, const
     for (int r = 0; r < 4; ++r)
         y[r] = acc[r] + bias[r];
     activate(y, a.activation);
-    if (with) {
-        y[0] += from_bits16(res.x & 0xFFFFu, a.dtype);
-        y[1] += from_bits16(res.x >> 16, a.dtype);
-        y[2] += from_bits16(res.y & 0xFFFFu, a.dtype);
-        y[3] += from_bits16(res.y >> 16, a.dtype);
-    }
-    const size_t o = (size_t)m * a.out_stride + n;
-    if (a.dtype == INT4VH_ROWS_F32) {
+    if constexpr (kDtype == INT4VH_ROWS_F32) {
         Words4 v;
 #pragma unroll
         for (int r = 0; r < 4; ++r)
             v.w[r] = __float_as_uint(y[r]);
-        *reinterpret_cast<Words4 *>(static_cast<float *>(a.out) + o) = v;
+        *static_cast<Words4 *>(to) = v;
     } else {
+        if (with) {
+            y[0] += from_bits16(res.x & 0xFFFFu, kDtype);
+            y[1] += from_bits16(res.x >> 16, kDtype);
+            y[2] += from_bits16(res.y & 0xFFFFu, kDtype);
+            y[3] += from_bits16(res.y >> 16, kDtype);
+        }
         Pair2 v;
-        v.w[0] = to_bits16(y[0], a.dtype) | (to_bits16(y[1], a.dtype) << 16);
-        v.w[1] = to_bits16(y[2], a.dtype) | (to_bits16(y[3], a.dtype) << 16);
-        *reinterpret_cast<Pair2 *>(static_cast<uint16_t *>(a.out) + o) = v;
+        v.w[0] = to_bits16(y[0], kDtype) | (to_bits16(y[1], kDtype) << 16);
+        v.w[1] = to_bits16(y[2], kDtype) | (to_bits16(y[3], kDtype) << 16);
+        *static_cast<Pair2 *>(to) = v;
     }
 }
 
@@ -235,7 +248,7 @@ __global__ void __launch_bounds__(kSThreads) mx_stream_kernel(MxArgs a)
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int n16 = lane & 15, grp = lane >> 4;
     const int blocks = a.K / 32;
-    const int c_begin = (int)blockIdx.y * a.split_steps * 4, c_end = min(blocks, c_begin + a.split_steps * 4);
+    const int c_begin = (int)blockIdx.y * a.split_spans * 16, c_end = min(blocks, c_begin + a.split_spans * 16);
     const int c0 = c_begin + wave * (kSteps * 4) + grp;         // this lane's first block of 32 channels
 
     auto load_w = [&](int tile, u32x4 (&q)[kSteps], uint32_t (&s)[kSteps]) {
@@ -293,40 +306,76 @@ __global__ void __launch_bounds__(kSThreads) mx_stream_kernel(MxArgs a)
 }
 
 // ---------------------------------------------------------------- tiles
-// A workgroup computes kWM*kMB*16 activation rows x kWN*kNB*16 weight rows
-// with kWM x kWN waves.  Per step of 128 channels each thread brings 16-byte
-// chunks through registers into LDS, kDepth steps ahead (two LDS buffers, one
-// barrier a step); 4 consecutive lanes load a row's 64 bytes.  LDS holds blocks
-// of 16 rows: chunk c of row r lies in slot 4 r + (c ^ (r / 4 % 4)), which
-// spreads both the writes (lanes along a row) and the reads (lanes along a
-// column) over the banks.  The scales go by spans of 4 steps: a thread brings a
-// row's 16 bytes and writes them so that a lane reads its own four steps' as
-// one register.
-template <int kWM, int kWN, int kMB, int kNB, int kDepth, bool kWhole>
-__global__ void __launch_bounds__(64 * kWM *kWN) mx_tile_kernel(MxArgs a)
+__device__ __forceinline__ uint32_t lds_at(const void *p)
 {
-    constexpr int kThreads = 64 * kWM * kWN;
-    constexpr int kBM = kWM * kMB, kBN = kWN * kNB;           // blocks of 16
-    constexpr int kAPer = kBM * 64 / kThreads, kWPer = kBN * 64 / kThreads;
-    static_assert(kAPer * kThreads == kBM * 64 && kWPer * kThreads == kBN * 64, "whole chunks per thread");
-    static_assert(4 % kDepth == 0, "registers repeat with the spans");
-    constexpr int kRows = (kBM + kBN) * 16, kSPer = (kRows + kThreads - 1) / kThreads;
-    struct Lds {
-        u32x4 x[kBM][64];
-        u32x4 w[kBN][64];
-    };
+    return (uint32_t)(size_t)(const __attribute__((address_space(3))) void *)p;
+}
+// Values that the compiler cannot compute with ahead of here: what follows from
+// them would otherwise stay in registers all through a loop.
+__device__ __forceinline__ void hold(uint32_t &a, uint32_t &b, uint32_t &c)
+{
+    asm volatile("" : "+v"(a), "+v"(b), "+v"(c));
+}
+// The lane's number, found anew.
+__device__ __forceinline__ uint32_t lane_here()
+{
+    uint32_t lane;
+    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=&v"(lane));
+    return lane;
+}
+typedef const __attribute__((address_space(3))) u32x4 lds_words;
+__device__ __forceinline__ lds_words *lds_pointer(uint32_t at)
+{
+    return (lds_words *)at;
+}
+constexpr int waitcnt_vm(int n)
+{
+    return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 4) | (0xF << 8);
+}
+
+// A copy of 16 bytes per lane straight into LDS: lane l's, from base + offset,
+// land at dst + 16 l.  Inline asm: the compiler would order all reads of LDS
+// behind all copies that it knows to be in flight.  Nothing comes back into
+// registers; the kernel waits for its copies itself.
+__device__ __forceinline__ void copy_to_lds16(const uint8_t *base, uint32_t offset, uint32_t dst)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst), "v"(offset), "s"(base)
+                 : "memory");
+}
+
+// A workgroup computes kWM*kMB*32 activation rows x kWN*kNB*32 weight rows with
+// kWM x kWN waves, in steps of 256 channels.  A step's codes are copied from
+// memory straight into one of two buffers in LDS while the other is multiplied:
+// 1 KB, 8 rows' 128 bytes (whole cache lines: with 64 bytes of 16 rows the
+// copies alone took 187 us instead of 137 for 8192^3), an instruction.  In LDS
+// chunk c of row r lies in slot 8 r + (c ^ (r / 2 % 8)), which spreads the reads
+// (lanes along a column) over the banks; the copy's lanes are numbered
+// accordingly.  The operands of the next quarter of a step are read while this
+// one's are multiplied; the barrier stands in front of a step's last quarter, so
+// that the copies into the buffer that it frees, and the reads from the other
+// one, have its products to hide behind.  The scales, 16 bytes a row for 512
+// channels, are copied likewise for 1024 (kWhole), or go through registers where
+// rows do not end with a whole span of 512 or are not aligned to it.
+template <int kWM, int kWN, int kMB, int kNB, bool kWhole>
+__global__ void __launch_bounds__(64 * kWM *kWN, 2) mx_tile_kernel(MxArgs a)
+{
+    constexpr int kWaves = kWM * kWN;
+    constexpr int kBM = kWM * kMB, kBN = kWN * kNB;           // blocks of 32
+    constexpr int kRows = (kBM + kBN) * 32;
+    constexpr int kPer = kRows / 8 / kWaves;                  // copies of a wave per step
+    static_assert(kPer * kWaves * 8 == kRows && kBM * 32 % (8 * kWaves) == 0, "whole copies per wave, of one matrix each");
     struct Mem {
-        Lds step[2];
-        u32x4 scale[2][kRows];
+        u32x4 code[2][kRows][8];
+        u32x4 scale[2][kRows][2];
     };
-    // the epilogue's use of LDS (per wave: 16 rows of sums)
-    constexpr int kCols = kNB * 16, kPitch = kCols + 4;        // the pitch spreads the rows over the banks
-    constexpr int kArea = 16 * kPitch;
-    constexpr size_t kTurn = 4 * kWM * kWN * kArea;
+    // the epilogue's use of LDS (per wave: 32 rows of sums)
+    constexpr int kCols = kNB * 32, kPitch = kCols + 4;        // the pitch spreads the rows over the banks
+    constexpr int kArea = 32 * kPitch;
+    constexpr size_t kTurn = 4 * kWaves * kArea;
     __shared__ __attribute__((aligned(16))) uint8_t mem[sizeof(Mem) > kTurn ? sizeof(Mem) : kTurn];
     Mem &lds = *reinterpret_cast<Mem *>(mem);
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int n16 = lane & 15, grp = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n32 = lane & 31, half = lane >> 5;
     const int wm = wave % kWM, wn = wave / kWM;
 
     // Workgroups are dispatched to the 8 XCDs round-robin: renumber them so
@@ -339,176 +388,213 @@ __global__ void __launch_bounds__(64 * kWM *kWN) mx_tile_kernel(MxArgs a)
     constexpr int kGroup = 8;                                  // tiles of M that share a column of weights
     const int first = t / (kGroup * a.tiles_n) * kGroup, rows = min(kGroup, a.tiles_m - first);
     const int in = t % (kGroup * a.tiles_n);
-    const int m0 = (first + in % rows) * kBM * 16, n0 = (in / rows) * kBN * 16;
+    const int m0 = (first + in % rows) * kBM * 32, n0 = (in / rows) * kBN * 32;
     const int blocks = a.K / 32;
-    const int s0 = part * a.split_steps, s1 = min(s0 + a.split_steps, (blocks + 3) / 4);
+    // spans of 512 channels, two steps each
+    const int p0 = part * a.split_spans, p1 = min(p0 + a.split_spans, (blocks + 15) / 16);
 
-    // Rows past the end load the last one (never stored).  Addresses are a
-    // uniform base, advanced by the step, and a 32-bit offset per chunk.
-    const int cc = tid & 3;                                    // this thread's chunk of its rows
+    // Rows past the end load the last one (never stored); copies past the last
+    // step repeat it, and chunks past K are the row's last one, so that every step
+    // issues the same copies without a branch.
+    const int cr = wave * 8 + (lane >> 3), cc = (lane & 7) ^ ((cr >> 1) & 7);
     const uint8_t *xbase = a.x + (size_t)m0 * blocks * 16, *wbase = a.w + (size_t)n0 * blocks * 16;
-    uint32_t xoff[kAPer], woff[kWPer];
-    const int r0 = tid >> 2, slot = (r0 >> 4) * 64 + (r0 & 15) * 4 + (cc ^ ((r0 >> 2) & 3));
+    constexpr int kXPer = kBM * 32 / (8 * kWaves);             // the copies of activations
+    uint32_t row = (uint32_t)cr;
+    auto load = [&](int step, int buf) {
+        const int s = min(step, 2 * p1 - 1);
+        // (the offset added to a base is not negative)
+        const uint32_t chunk = kWhole ? (uint32_t)cc : (uint32_t)min(s * 8 + cc, blocks - 1);
 #pragma unroll
-    for (int j = 0; j < kAPer; ++j)
-        xoff[j] = (uint32_t)(min(r0 + j * (kThreads / 4), a.M - 1 - m0) * blocks + cc) * 16u;
-#pragma unroll
-    for (int j = 0; j < kWPer; ++j)
-        woff[j] = (uint32_t)(min(r0 + j * (kThreads / 4), a.N - 1 - n0) * blocks + cc) * 16u;
-    // Loads past the last step repeat it, and chunks past K load the row's last
-    // one, so that every step issues the same loads without a branch; the
-    // activations' codes past K are cleared on their way to LDS.
-    u32x4 rx[kDepth][kAPer], rw[kDepth][kWPer];
-    auto load = [&](int d, int step) {
-        const int s = min(step, s1 - 1);
-        const uint8_t *px = xbase + (size_t)s * 64, *pw = wbase + (size_t)s * 64;
-        const uint32_t back = kWhole ? 0u : 16u * (uint32_t)max(0, s * 4 + cc - (blocks - 1));
-#pragma unroll
-        for (int j = 0; j < kAPer; ++j)
-            rx[d][j] = *reinterpret_cast<const u32x4 *>(px + (xoff[j] - back));
-#pragma unroll
-        for (int j = 0; j < kWPer; ++j)
-            rw[d][j] = *reinterpret_cast<const u32x4 *>(pw + (woff[j] - back));
-    };
-    auto store = [&](int d, int s, Lds &l) {
-        if (!kWhole) {
-            const bool live = s * 4 + cc < blocks;
-#pragma unroll
-            for (int j = 0; j < kAPer; ++j)
-                rx[d][j] = live ? rx[d][j] : u32x4{0, 0, 0, 0};
+        for (int j = 0; j < kPer; ++j) {
+            const uint32_t r = j < kXPer ? min(row + j * 8 * kWaves, (uint32_t)(a.M - 1 - m0))
+                                         : min(row + (j - kXPer) * 8 * kWaves, (uint32_t)(a.N - 1 - n0));
+            copy_to_lds16((j < kXPer ? xbase : wbase) + (kWhole ? (size_t)s * 128 : 0), (r * (uint32_t)blocks + chunk) * 16u,
+                          lds_at(&lds.code[buf][wave * 8 + j * 8 * kWaves][0]));
         }
-#pragma unroll
-        for (int j = 0; j < kAPer; ++j)
-            (&l.x[0][0])[slot + j * kThreads] = rx[d][j];
-#pragma unroll
-        for (int j = 0; j < kWPer; ++j)
-            (&l.w[0][0])[slot + j * kThreads] = rw[d][j];
     };
-    // a thread's rows of scales: activations, then weights
-    const uint8_t *srow[kSPer];
+    // rows of scales: 32 an instruction, 32 bytes each, or one a lane through
+    // registers
+    const uint8_t *sxbase = a.x_scales + (size_t)m0 * blocks, *swbase = a.w_scales + (size_t)n0 * blocks;
+    constexpr int kSRows = kWhole ? 32 : 64, kSCopies = kRows / kSRows, kSPer = (kSCopies + kWaves - 1) / kWaves;
+    static_assert(kBM * 32 % kSRows == 0 && kRows % kSRows == 0, "a copy of scales is of one matrix");
+    uint32_t sfrom[kSPer];
 #pragma unroll
     for (int j = 0; j < kSPer; ++j) {
-        const int r = min(tid + j * kThreads, kRows - 1);
-        srow[j] = r < kBM * 16 ? a.x_scales + (size_t)min(m0 + r, a.M - 1) * blocks
-                               : a.w_scales + (size_t)min(n0 + r - kBM * 16, a.N - 1) * blocks;
+        const int r = min(wave + j * kWaves, kSCopies - 1) * kSRows + (kWhole ? lane >> 1 : lane);
+        sfrom[j] = (uint32_t)(r < kBM * 32 ? min(r, a.M - 1 - m0) : min(r - kBM * 32, a.N - 1 - n0)) * (uint32_t)blocks;
     }
-    uint32_t rs[kSPer][4];
-    auto load_scales = [&](int step) {                         // of steps step .. step + 3
-        const int s = min(step, (s1 - 1) & ~3);
+    auto copy_scales = [&](int span, int buf) {                // of spans `span` and the next
 #pragma unroll
         for (int j = 0; j < kSPer; ++j) {
-            if (kWhole) {
-                const Words1 v = *reinterpret_cast<const Words1 *>(srow[j] + 4 * s);
+            const int b = min(wave + j * kWaves, kSCopies - 1);
+            copy_to_lds16(b * kSRows < kBM * 32 ? sxbase : swbase,
+                          sfrom[j] + (uint32_t)min(16 * span + 16 * (lane & 1), blocks - 16),
+                          lds_at(&lds.scale[buf][b * kSRows][0]));
+        }
+    };
+    uint32_t rs[kSPer][4];
+    auto load_scales = [&](int span) {                         // of one span
+        const int s = min(span, p1 - 1);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    rs[j][i] = v.w[i];
-            } else {
+        for (int j = 0; j < kSPer; ++j) {
+            const uint8_t *base = min(wave + j * kWaves, kSCopies - 1) * kSRows < kBM * 32 ? sxbase : swbase;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    rs[j][i] = 0u;
+            for (int i = 0; i < 4; ++i) {
+                rs[j][i] = 0u;
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        const int c = 4 * s + 4 * i + b;
-                        const uint32_t v = srow[j][min(c, blocks - 1)];
-                        rs[j][i] |= (c < blocks ? v : 0u) << (8 * b);
-                    }
+                for (int q = 0; q < 4; ++q) {
+                    const int c = 16 * s + 4 * i + q;
+                    const uint32_t v = base[sfrom[j] + (uint32_t)min(c, blocks - 1)];
+                    rs[j][i] |= (c < blocks ? v : 0u) << (8 * q);
                 }
             }
         }
     };
-    auto store_scales = [&](u32x4 *to) {
+    auto store_scales = [&](int span) {
 #pragma unroll
-        for (int j = 0; j < kSPer; ++j) {
-            const uint32_t lo = __builtin_amdgcn_perm(rs[j][1], rs[j][0], 0x05010400u);
-            const uint32_t hi = __builtin_amdgcn_perm(rs[j][1], rs[j][0], 0x07030602u);
-            const uint32_t lo2 = __builtin_amdgcn_perm(rs[j][3], rs[j][2], 0x05010400u);
-            const uint32_t hi2 = __builtin_amdgcn_perm(rs[j][3], rs[j][2], 0x07030602u);
-            if (kRows % kThreads == 0 || tid + j * kThreads < kRows)
-                to[tid + j * kThreads] = u32x4{__builtin_amdgcn_perm(lo2, lo, 0x05040100u),
-                                               __builtin_amdgcn_perm(lo2, lo, 0x07060302u),
-                                               __builtin_amdgcn_perm(hi2, hi, 0x05040100u),
-                                               __builtin_amdgcn_perm(hi2, hi, 0x07060302u)};
-        }
+        for (int j = 0; j < kSPer; ++j)
+            lds.scale[(span >> 1) & 1][min(wave + j * kWaves, kSCopies - 1) * kSRows + lane][span & 1] =
+                u32x4{rs[j][0], rs[j][1], rs[j][2], rs[j][3]};
     };
 
-    f32x4 acc[kMB][kNB];
+    f32x16 acc[kMB][kNB];
 #pragma unroll
     for (int i = 0; i < kMB; ++i)
 #pragma unroll
         for (int j = 0; j < kNB; ++j)
-            acc[i][j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                acc[i][j][r] = 0.0f;
 
-    load_scales(s0);
+    // Quarter q of a step: chunk 2 q + (lane / 32) of the lane's row.  Two sets of
+    // operands take turns.
+    u32x4 x[2][kMB], w[2][kNB], xs[kMB], ws[kNB];
+    // addresses in LDS of the lane's first chunk; chunk c of its row lies 16 c away, bit
+    // by bit
+    const uint32_t turned = 16u * (uint32_t)(half ^ ((n32 >> 1) & 7));
+    uint32_t ax = lds_at(&lds.code[0][wm * kMB * 32 + n32][0]) + turned;
+    uint32_t aw = lds_at(&lds.code[0][(kBM + wn * kNB) * 32 + n32][0]) + turned;
+    auto read = [&](int step, int buf, int q) {
+        lds_words *px = lds_pointer((ax ^ (32u * q)) + buf * (uint32_t)sizeof(lds.code[0]));
+        lds_words *pw = lds_pointer((aw ^ (32u * q)) + buf * (uint32_t)sizeof(lds.code[0]));
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d)
-        load(d, s0 + d);
-    store_scales(lds.scale[0]);
-    store(0, s0, lds.step[0]);
-    const int rslot = n16 * 4 + (grp ^ ((n16 >> 2) & 3));
-    uint32_t xs[kMB], ws[kNB];
-    auto step = [&](const Lds &l, auto byte) {
-        u32x4 x[kMB];
+        for (int k = 0; k < kMB; ++k)
+            x[q & 1][k] = px[32 * 8 * k];
 #pragma unroll
-        for (int i = 0; i < kMB; ++i)
-            x[i] = l.x[wm * kMB + i][rslot];
-#pragma unroll
-        for (int j = 0; j < kNB; ++j) {
-            const u32x4 w = l.w[wn * kNB + j][rslot];
-#pragma unroll
-            for (int i = 0; i < kMB; ++i)
-                acc[i][j] = mma<decltype(byte)::value>(w, x[i], acc[i][j], ws[j], xs[i]);
-        }
-    };
-    auto turn_step = [&](int s, int sbuf, auto byte) {
-        constexpr int i = decltype(byte)::value;
-        __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
-        barrier_no_fence();
-        if constexpr (i == 0) {
-            const uint32_t *sc = reinterpret_cast<const uint32_t *>(lds.scale[sbuf]);
+        for (int k = 0; k < kNB; ++k)
+            w[q & 1][k] = pw[32 * 8 * k];
+        if (!kWhole && step * 8 + 8 > blocks) {
+            const bool live = step * 8 + 2 * q + half < blocks;
 #pragma unroll
             for (int k = 0; k < kMB; ++k)
-                xs[k] = sc[(wm * kMB + k) * 64 + lane / 16 + n16 * 4];
+                x[q & 1][k] = live ? x[q & 1][k] : u32x4{0, 0, 0, 0};
+        }
+    };
+    auto read_scales = [&](int span) {
+        const uint32_t own = lane_here(), shift = own >> 5 << 3;
+        lds_words *ps = lds_pointer(lds_at(&lds.scale[0][0][0]) + (uint32_t)((span >> 1) & 1) * (uint32_t)sizeof(lds.scale[0]) +
+                                    16u * (uint32_t)(span & 1) + (own & 31u) * 32u);
+#pragma unroll
+        for (int k = 0; k < kMB; ++k)
+            xs[k] = ps[(wm * kMB + k) * 64];
+#pragma unroll
+        for (int k = 0; k < kNB; ++k)
+            ws[k] = ps[(kBM + wn * kNB + k) * 64];
+        // a word holds 4 chunks' scales: the lane's are bytes 0 and 2 of these
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+#pragma unroll
+            for (int k = 0; k < kMB; ++k)
+                xs[k][q] >>= shift;
 #pragma unroll
             for (int k = 0; k < kNB; ++k)
-                ws[k] = sc[(kBM + wn * kNB + k) * 64 + lane / 16 + n16 * 4];
-            load_scales(s + 4);
+                ws[k][q] >>= shift;
         }
-        load(i % kDepth, s + i + kDepth);
-        step(lds.step[i & 1], byte);
-        store((i + 1) % kDepth, s + i + 1, lds.step[(i + 1) & 1]);
-        if constexpr (i == 3)
-            store_scales(lds.scale[sbuf ^ 1]);
     };
-    // whole spans: steps past K multiply zeros (a way out of the middle of a span
-    // would copy all sums)
-    int sbuf = 0;
-    for (int s = s0; s < s1; s += 4, sbuf ^= 1) {
-        turn_step(s, sbuf, std::integral_constant<int, 0>());
-        turn_step(s, sbuf, std::integral_constant<int, 1>());
-        turn_step(s, sbuf, std::integral_constant<int, 2>());
-        turn_step(s, sbuf, std::integral_constant<int, 3>());
+    // the products of quarter kQ of a span's step kS
+    auto multiply = [&](auto s, auto q) {
+        constexpr int kS = decltype(s)::value, kQ = decltype(q)::value, kWord = 2 * kS + kQ / 2, kByte = kQ % 2 * 2;
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < kNB; ++j)
+#pragma unroll
+            for (int k = 0; k < kMB; ++k)
+                acc[k][j] = mma32<kByte>(w[kQ & 1][j], x[kQ & 1][k], acc[k][j], ws[j][kWord], xs[k][kWord]);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto landed = [&]() {
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+        __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+        barrier_no_fence();
+    };
+    auto step = [&](int span, auto s) {
+        constexpr int kS = decltype(s)::value;
+        const int at = 2 * span + kS;
+        hold(ax, aw, row);
+        using Z = std::integral_constant<int, 0>;
+        using I = std::integral_constant<int, 1>;
+        using II = std::integral_constant<int, 2>;
+        using III = std::integral_constant<int, 3>;
+        read(at, kS, 1);
+        multiply(s, Z());
+        read(at, kS, 2);
+        multiply(s, I());
+        read(at, kS, 3);
+        multiply(s, II());
+        // all have read this buffer, and the next step's has landed
+        landed();
+        load(at + 2, kS);
+        if (kWhole && kS == 0 && (span - p0) % 2 == 0)
+            copy_scales(span + 2, ((span - p0) / 2 + 1) & 1);
+        if (!kWhole && kS == 0)
+            load_scales(span + 1);
+        read(at + 1, kS ^ 1, 0);
+        multiply(s, III());
+        if (kS == 1)
+            read_scales(span + 1 - p0);
+        if (!kWhole && kS == 0)
+            store_scales(span + 1 - p0);
+    };
+    load(2 * p0, 0);
+    if (kWhole) {
+        copy_scales(p0, 0);
+    } else {
+        load_scales(p0);
+        store_scales(0);
+    }
+    load(2 * p0 + 1, 1);
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(kPer));
+    __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+    barrier_no_fence();
+    read_scales(0);
+    read(2 * p0, 0, 0);
+    // whole spans: quarters past K multiply zeros (a way out of the middle of a
+    // span would copy all sums)
+    for (int span = p0; span < p1; ++span) {
+        step(span, std::integral_constant<int, 0>());
+        step(span, std::integral_constant<int, 1>());
     }
 
-    // D: column = activation row lane & 15, rows = weight rows 4 * grp + r.
-    // Each wave turns its sums around in LDS, 16 activation rows at a time, so
-    // that its lanes hold four columns of a row and rows are written whole.
-    // The residual of the next 16 rows is asked for before these are stored: a
+    // D: column = activation row lane & 31, rows = weight rows 8 (r / 4) + 4 (lane /
+    // 32) + r % 4.  Each wave turns its sums around in LDS, 32 activation rows at a
+    // time, so that its lanes hold four columns of a row and rows are written whole.
+    // The residual of the next 32 rows is asked for before these are stored: a
     // wait for a load also waits for the stores in front of it.
     float *turn = reinterpret_cast<float *>(mem) + wave * kArea;
-    constexpr int kLanes = kCols / 4, kStep = 64 / kLanes, kIter = 16 / kStep;   // lanes of a row; rows at a time
+    constexpr int kLanes = kCols / 4, kStep = 64 / kLanes, kIter = 32 / kStep;   // lanes of a row; rows at a time
     const int c4 = (lane % kLanes) * 4, n = n0 + wn * kCols + c4, lr = lane / kLanes;
-    const int mw = m0 + wm * kMB * 16;
-    float bs[4];
-    Pair2 res[2][kIter];
+    const int mw = m0 + wm * kMB * 32;
     // The usual case handles four columns at a time, with a 16-bit residual or
     // none; rows that end inside a lane's four columns, and binary32 residuals,
     // go element by element.
     const bool wide = !a.parts && a.N % 4 == 0 && (!a.residual || a.dtype != INT4VH_ROWS_F32);
     const bool early = wide && a.residual;
+    float bs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    Pair2 res[2][kIter];
     auto load_residual = [&](int i) {
 #pragma unroll
         for (int k = 0; k < kIter; ++k) {
-            const int m = min(mw + i * 16 + lr + k * kStep, a.M - 1);
+            const int m = min(mw + i * 32 + lr + k * kStep, a.M - 1);
             res[i & 1][k] = *reinterpret_cast<const Pair2 *>(static_cast<const uint16_t *>(a.residual) +
                                                              (size_t)m * a.residual_stride + min(n, a.N - 4));
         }
@@ -521,33 +607,59 @@ __global__ void __launch_bounds__(64 * kWM *kWN) mx_tile_kernel(MxArgs a)
             load_residual(0);
     }
     __builtin_amdgcn_s_waitcnt(0);
-    barrier_no_fence();                                        // the last step's reads are done
-#pragma unroll
-    for (int i = 0; i < kMB; ++i) {
-        const int mi = mw + i * 16;
+    barrier_no_fence();                                        // the last step's reads and copies are done
+    // sums of 32 activation rows, turned
+    auto turn_rows = [&](int i) {
 #pragma unroll
         for (int j = 0; j < kNB; ++j)
-            *reinterpret_cast<f32x4 *>(turn + n16 * kPitch + j * 16 + 4 * grp) = acc[i][j];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<f32x4 *>(turn + n32 * kPitch + j * 32 + 8 * q + 4 * half) =
+                    f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
         if (early && i + 1 < kMB)
             load_residual(i + 1);
         wave_fence();
-        if (wide) {
+    };
+    auto write_wide = [&](auto dtype) {
+        constexpr int kDtype = decltype(dtype)::value;
+        constexpr size_t kSize = kDtype == INT4VH_ROWS_F32 ? 4 : 2;
+#pragma unroll
+        for (int i = 0; i < kMB; ++i) {
+            turn_rows(i);
+            const int m = mw + i * 32 + lr;
+            char *to = static_cast<char *>(a.out) + ((size_t)m * a.out_stride + n) * kSize;
 #pragma unroll
             for (int k = 0; k < kIter; ++k) {
-                const int r = lr + k * kStep;
-                const f32x4 v = *reinterpret_cast<const f32x4 *>(turn + r * kPitch + c4);
-                if (mi + r < a.M && n < a.N)
-                    finish_four(a, mi + r, n, v, bs, early, make_uint2(res[i & 1][k].w[0], res[i & 1][k].w[1]));
+                const f32x4 v = *reinterpret_cast<const f32x4 *>(turn + (lr + k * kStep) * kPitch + c4);
+                if (m + k * kStep < a.M && n < a.N)
+                    finish_four<kDtype>(a, to, v, bs, early, make_uint2(res[i & 1][k].w[0], res[i & 1][k].w[1]));
+                to += (size_t)kStep * a.out_stride * kSize;
             }
-        } else if (a.parts) {
+            wave_fence();
+        }
+    };
+    if (wide) {
+        if (a.dtype == INT4VH_ROWS_F16)
+            write_wide(std::integral_constant<int, INT4VH_ROWS_F16>());
+        else if (a.dtype == INT4VH_ROWS_BF16)
+            write_wide(std::integral_constant<int, INT4VH_ROWS_BF16>());
+        else
+            write_wide(std::integral_constant<int, INT4VH_ROWS_F32>());
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < kMB; ++i) {
+        const int mi = mw + i * 32;
+        turn_rows(i);
+        if (a.parts) {
 #pragma nounroll
-            for (int r = lr; r < 16; r += kStep)
+            for (int r = lr; r < 32; r += kStep)
                 if (mi + r < a.M && n < a.N)
                     *reinterpret_cast<f32x4 *>(&a.parts[((size_t)part * a.M + mi + r) * a.n_pad + n]) =
                         *reinterpret_cast<const f32x4 *>(turn + r * kPitch + c4);
         } else {
 #pragma nounroll
-            for (int e = lane; e < 16 * kCols; e += 64) {
+            for (int e = lane; e < 32 * kCols; e += 64) {
                 const int m = mi + e / kCols, c = n0 + wn * kCols + e % kCols;
                 if (m < a.M && c < a.N)
                     finish_one(a, m, c, turn[e / kCols * kPitch + e % kCols], column_bias(a, c));
@@ -572,22 +684,23 @@ __global__ void __launch_bounds__(256) mx_join_kernel(MxArgs a)
 
 // ---------------------------------------------------------------- host side
 
-enum Kind { kStream, kTile32, kTile128 };
+// How a call of these sizes runs.
+enum Kind { kStream, kTile64, kTile128 };      // tiles of 64, 128 rows x 128 columns
 struct Plan {
     Kind kind;
-    int splits, split_steps;
+    int splits, split_spans;                   // parts of K, and spans of 512 channels in each
     int tiles_m, tiles_n;
 };
 
-long long tiles_of(int M, int N, int bm, int bn)
+long long tiles_of(int M, int N, int bm)
 {
-    return (long long)((M + bm - 1) / bm) * ((N + bn - 1) / bn);
+    return (long long)((M + bm - 1) / bm) * ((N + 127) / 128);
 }
 
 Plan plan_for(int M, int N, int K, int cus)
 {
     Plan p;
-    const int steps = (K + 127) / 128;
+    const int spans = (K + 511) / 512;
     p.splits = 1;
     if (M <= 16) {
         p.kind = kStream;
@@ -595,19 +708,17 @@ Plan plan_for(int M, int N, int K, int cus)
         p.tiles_n = (N + 15) / 16;
         p.splits = (K + kSMaxK - 1) / kSMaxK;
     } else {
-        p.kind = 2 * tiles_of(M, N, 128, 128) >= cus ? kTile128 : kTile32;
-        const int bm = p.kind == kTile128 ? 128 : 32;
+        p.kind = 2 * tiles_of(M, N, 128) >= cus ? kTile128 : kTile64;
+        const int bm = p.kind == kTile128 ? 128 : 64;
         p.tiles_m = (M + bm - 1) / bm;
         p.tiles_n = (N + 127) / 128;
-        // few tiles: parts of at least 4 steps, up to two workgroups a compute unit
-        if (p.kind == kTile32)
-            while (2 * p.splits * tiles_of(M, N, 32, 128) <= 2ll * cus && steps / (2 * p.splits) >= 4)
+        // few tiles: parts of a span at least, up to two workgroups a compute unit
+        if (p.kind == kTile64)
+            while (2 * p.splits * tiles_of(M, N, 64) <= 2ll * cus && spans / (2 * p.splits) >= 1)
                 p.splits *= 2;
     }
-    p.split_steps = (steps + p.splits - 1) / p.splits;
-    if (p.splits > 1)                          // whole spans of scales
-        p.split_steps = (p.split_steps + 3) / 4 * 4;
-    p.splits = (steps + p.split_steps - 1) / p.split_steps;
+    p.split_spans = (spans + p.splits - 1) / p.splits;
+    p.splits = (spans + p.split_spans - 1) / p.split_spans;
     return p;
 }
 
@@ -639,7 +750,7 @@ bool sizes_supported(int M, int N, int K)
 
 void launch_stream(const MxArgs &a, dim3 grid, hipStream_t s)
 {
-    const int per_wave = (a.split_steps + kSWaves - 1) / kSWaves;
+    const int per_wave = (4 * a.split_spans + kSWaves - 1) / kSWaves;
     const dim3 block(kSThreads);
     if (per_wave <= 1)
         hipLaunchKernelGGL(mx_stream_kernel<1>, grid, block, 0, s, a);
@@ -653,14 +764,14 @@ void launch_stream(const MxArgs &a, dim3 grid, hipStream_t s)
         hipLaunchKernelGGL(mx_stream_kernel<8>, grid, block, 0, s, a);
 }
 
-template <int kWM, int kWN, int kMB, int kNB, int kDepth>
+template <int kWM, int kWN, int kMB, int kNB>
 void launch_tiles(const MxArgs &a, hipStream_t s)
 {
     const dim3 grid((unsigned)((long long)a.tiles_m * a.tiles_n * a.splits)), block(64 * kWM * kWN);
-    if (a.K % 512 == 0)
-        hipLaunchKernelGGL((mx_tile_kernel<kWM, kWN, kMB, kNB, kDepth, true>), grid, block, 0, s, a);
+    if (a.K % 512 == 0 && rows_aligned(a.x_scales, 16) && rows_aligned(a.w_scales, 16))
+        hipLaunchKernelGGL((mx_tile_kernel<kWM, kWN, kMB, kNB, true>), grid, block, 0, s, a);
     else
-        hipLaunchKernelGGL((mx_tile_kernel<kWM, kWN, kMB, kNB, kDepth, false>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((mx_tile_kernel<kWM, kWN, kMB, kNB, false>), grid, block, 0, s, a);
 }
 
 template <int kDtype>
@@ -778,16 +889,16 @@ int linear_mxfp4_rows(const uint8_t *codes, const uint8_t *scales, const uint8_t
     a.activation = activation;
     a.dtype = dtype;
     a.splits = p.splits;
-    a.split_steps = p.split_steps;
+    a.split_spans = p.split_spans;
     a.tiles_m = p.tiles_m;
     a.tiles_n = p.tiles_n;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if (p.kind == kStream)
         launch_stream(a, dim3(p.tiles_n < 2 * cus ? p.tiles_n : 2 * cus, p.splits), s);
-    else if (p.kind == kTile32)
-        launch_tiles<1, 2, 2, 4, 2>(a, s);
+    else if (p.kind == kTile64)
+        launch_tiles<2, 2, 1, 2>(a, s);
     else
-        launch_tiles<2, 2, 4, 4, 2>(a, s);
+        launch_tiles<2, 2, 2, 2>(a, s);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return hip_fail(e, "mxfp4 linear kernel launch");
