@@ -33,7 +33,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-struct __attribute__((packed, aligned(1))) Words1 { uint32_t w[4]; };
+struct __attribute__((packed, aligned(1))) Word1 { uint32_t w; };
 
 constexpr int kMaxK = 65536;
 
@@ -240,41 +240,69 @@ constexpr int kSMaxK = kSWaves * kSMaxSteps * 128;    // 8192 channels per workg
 
 // Grid (workgroups over tiles of 16 weight rows, parts of K); kSteps: steps per
 // wave, whose activations stay in registers.  The waves' sums meet in LDS, and
-// are added in the order of the waves.
-template <int kSteps>
-__global__ void __launch_bounds__(kSThreads) mx_stream_kernel(MxArgs a)
+// are added in the order of the waves.  Scales: a lane needs a byte of each step,
+// the one of its own 32 channels; a row's 4 bytes of a step are loaded as a word
+// by one lane, step u's by the lanes of group u % 4, and passed on (kWhole: K is
+// a multiple of 128; otherwise each lane loads its bytes).
+template <int kSteps, bool kWhole>
+__global__ void __launch_bounds__(kSThreads, kSteps > 5 ? 2 : 4) mx_stream_kernel(MxArgs a)
 {
     __shared__ __attribute__((aligned(16))) float s_part[2][kSWaves][256];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    constexpr int kWords = kWhole ? (kSteps + 3) / 4 : kSteps;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n16 = lane & 15, grp = lane >> 4;
     const int blocks = a.K / 32;
     const int c_begin = (int)blockIdx.y * a.split_spans * 16, c_end = min(blocks, c_begin + a.split_spans * 16);
-    const int c0 = c_begin + wave * (kSteps * 4) + grp;         // this lane's first block of 32 channels
+    const int c0 = c_begin + wave * (kSteps * 4);               // this wave's first block of 32 channels
 
-    auto load_w = [&](int tile, u32x4 (&q)[kSteps], uint32_t (&s)[kSteps]) {
-        const size_t row = min(tile * 16 + n16, a.N - 1);
+    // Row r's chunks and scales; past the end any valid ones, which meet zero codes.
+    auto load_codes = [&](const uint8_t *codes, int r, int u) {
+        const int c = min(c0 + 4 * u + grp, blocks - 1);
+        return *reinterpret_cast<const u32x4 *>(codes + ((uint32_t)r * (uint32_t)blocks + (uint32_t)c) * 16u);
+    };
+    auto load_words = [&](const uint8_t *scales, int r, uint32_t (&s)[kWords]) {
+        const uint8_t *row = scales + (uint32_t)r * (uint32_t)blocks;
 #pragma unroll
-        for (int u = 0; u < kSteps; ++u) {
-            const int c = min(c0 + 4 * u, blocks - 1);          // past the end: it meets zero codes
-            q[u] = *reinterpret_cast<const u32x4 *>(a.w + (row * blocks + c) * 16);
-            s[u] = a.w_scales[row * blocks + c];
+        for (int i = 0; i < kWords; ++i) {
+            if constexpr (kWhole) {
+                const Word1 v = *reinterpret_cast<const Word1 *>(row + min(c0 + 16 * i + 4 * grp, blocks - 4));
+                s[i] = v.w;
+            } else {
+                s[i] = row[min(c0 + 4 * i + grp, blocks - 1)];
+            }
         }
     };
+    // step u's scale, in the lowest byte
+    auto scale = [&](const uint32_t (&s)[kWords], int u) {
+        if constexpr (kWhole)
+            return (uint32_t)__builtin_amdgcn_ds_bpermute(4 * ((u & 3) * 16 + n16), (int)s[u >> 2]) >> (8 * grp);
+        else
+            return s[u];
+    };
+    auto load_w = [&](int tile, u32x4 (&q)[kSteps], uint32_t (&s)[kWords]) {
+        const uint8_t *w = a.w + (size_t)tile * 16 * blocks * 16;
+        const int r = min(n16, a.N - 1 - tile * 16);
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u)
+            q[u] = load_codes(w, r, u);
+        load_words(a.w_scales + (size_t)tile * 16 * blocks, r, s);
+    };
     u32x4 q[kSteps];
-    uint32_t s[kSteps];
+    uint32_t s[kWords], xw[kWords];
     int tile = blockIdx.x;
     load_w(tile, q, s);
     u32x4 x[kSteps];
     uint32_t xs[kSteps];
+    const int xr = min(n16, a.M - 1);
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u)
+        x[u] = load_codes(a.x, xr, u);
+    load_words(a.x_scales, xr, xw);
 #pragma unroll
     for (int u = 0; u < kSteps; ++u) {
-        const int c = c0 + 4 * u;
-        x[u] = u32x4{0, 0, 0, 0};
-        xs[u] = 127u;
-        if (n16 < a.M && c < c_end) {
-            x[u] = *reinterpret_cast<const u32x4 *>(a.x + ((size_t)n16 * blocks + c) * 16);
-            xs[u] = a.x_scales[(size_t)n16 * blocks + c];
-        }
+        const bool live = n16 < a.M && c0 + 4 * u + grp < c_end;
+        x[u] = live ? x[u] : u32x4{0, 0, 0, 0};
+        xs[u] = scale(xw, u);
     }
     const int m = tid >> 4, nn = tid & 15;             // the output element of this thread in every tile
     for (int buf = 0; tile < a.tiles_n; buf ^= 1) {
@@ -283,7 +311,7 @@ __global__ void __launch_bounds__(kSThreads) mx_stream_kernel(MxArgs a)
         f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
         for (int u = 0; u < kSteps; ++u)
-            acc = mma<0>(q[u], x[u], acc, s[u], xs[u]);
+            acc = mma<0>(q[u], x[u], acc, scale(s, u), xs[u]);
         if (next < a.tiles_n)
             load_w(next, q, s);
         // D: column = activation row lane & 15, rows = weight rows 4 * grp + r
@@ -555,7 +583,27 @@ __global__ void __launch_bounds__(64 * kWM *kWN, 2) mx_tile_kernel(MxArgs a)
         if (!kWhole && kS == 0)
             store_scales(span + 1 - p0);
     };
+    // The epilogue's place: four columns of a row per lane.
+    constexpr int kLanes = kCols / 4, kStep = 64 / kLanes, kIter = 32 / kStep;   // lanes of a row; rows at a time
+    const int c4 = (lane % kLanes) * 4, n = n0 + wn * kCols + c4, lr = lane / kLanes;
+    const int mw = m0 + wm * kMB * 32;
+    // The usual case handles four columns at a time, with a 16-bit residual or
+    // none; rows that end inside a lane's four columns, and binary32 residuals,
+    // go element by element.
+    const bool wide = !a.parts && a.N % 4 == 0 && (!a.residual || a.dtype != INT4VH_ROWS_F32);
+    const bool early = wide && a.residual;
+    // The usual residual is asked for up front: it takes a memory's latency.
+    Pair2 res[kMB][kIter];
     load(2 * p0, 0);
+    if (early)
+#pragma unroll
+        for (int i = 0; i < kMB; ++i)
+#pragma unroll
+            for (int k = 0; k < kIter; ++k) {
+                const int m = min(mw + i * 32 + lr + k * kStep, a.M - 1);
+                res[i][k] = *reinterpret_cast<const Pair2 *>(static_cast<const uint16_t *>(a.residual) +
+                                                             (size_t)m * a.residual_stride + min(n, a.N - 4));
+            }
     if (kWhole) {
         copy_scales(p0, 0);
     } else {
@@ -578,34 +626,12 @@ __global__ void __launch_bounds__(64 * kWM *kWN, 2) mx_tile_kernel(MxArgs a)
     // D: column = activation row lane & 31, rows = weight rows 8 (r / 4) + 4 (lane /
     // 32) + r % 4.  Each wave turns its sums around in LDS, 32 activation rows at a
     // time, so that its lanes hold four columns of a row and rows are written whole.
-    // The residual of the next 32 rows is asked for before these are stored: a
-    // wait for a load also waits for the stores in front of it.
     float *turn = reinterpret_cast<float *>(mem) + wave * kArea;
-    constexpr int kLanes = kCols / 4, kStep = 64 / kLanes, kIter = 32 / kStep;   // lanes of a row; rows at a time
-    const int c4 = (lane % kLanes) * 4, n = n0 + wn * kCols + c4, lr = lane / kLanes;
-    const int mw = m0 + wm * kMB * 32;
-    // The usual case handles four columns at a time, with a 16-bit residual or
-    // none; rows that end inside a lane's four columns, and binary32 residuals,
-    // go element by element.
-    const bool wide = !a.parts && a.N % 4 == 0 && (!a.residual || a.dtype != INT4VH_ROWS_F32);
-    const bool early = wide && a.residual;
     float bs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    Pair2 res[2][kIter];
-    auto load_residual = [&](int i) {
-#pragma unroll
-        for (int k = 0; k < kIter; ++k) {
-            const int m = min(mw + i * 32 + lr + k * kStep, a.M - 1);
-            res[i & 1][k] = *reinterpret_cast<const Pair2 *>(static_cast<const uint16_t *>(a.residual) +
-                                                             (size_t)m * a.residual_stride + min(n, a.N - 4));
-        }
-    };
-    if (!a.parts) {
+    if (!a.parts)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
             bs[r] = column_bias(a, min(n + r, a.N - 1));
-        if (early)
-            load_residual(0);
-    }
     __builtin_amdgcn_s_waitcnt(0);
     barrier_no_fence();                                        // the last step's reads and copies are done
     // sums of 32 activation rows, turned
@@ -616,8 +642,6 @@ __global__ void __launch_bounds__(64 * kWM *kWN, 2) mx_tile_kernel(MxArgs a)
             for (int q = 0; q < 4; ++q)
                 *reinterpret_cast<f32x4 *>(turn + n32 * kPitch + j * 32 + 8 * q + 4 * half) =
                     f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-        if (early && i + 1 < kMB)
-            load_residual(i + 1);
         wave_fence();
     };
     auto write_wide = [&](auto dtype) {
@@ -632,7 +656,7 @@ __global__ void __launch_bounds__(64 * kWM *kWN, 2) mx_tile_kernel(MxArgs a)
             for (int k = 0; k < kIter; ++k) {
                 const f32x4 v = *reinterpret_cast<const f32x4 *>(turn + (lr + k * kStep) * kPitch + c4);
                 if (m + k * kStep < a.M && n < a.N)
-                    finish_four<kDtype>(a, to, v, bs, early, make_uint2(res[i & 1][k].w[0], res[i & 1][k].w[1]));
+                    finish_four<kDtype>(a, to, v, bs, early, make_uint2(res[i][k].w[0], res[i][k].w[1]));
                 to += (size_t)kStep * a.out_stride * kSize;
             }
             wave_fence();
@@ -748,20 +772,21 @@ bool sizes_supported(int M, int N, int K)
     return K <= kMaxK && N <= (1 << 24) && M <= (1 << 20) && (long long)M * N < (1ll << 40);
 }
 
+template <bool kWhole>
 void launch_stream(const MxArgs &a, dim3 grid, hipStream_t s)
 {
     const int per_wave = (4 * a.split_spans + kSWaves - 1) / kSWaves;
     const dim3 block(kSThreads);
     if (per_wave <= 1)
-        hipLaunchKernelGGL(mx_stream_kernel<1>, grid, block, 0, s, a);
+        hipLaunchKernelGGL((mx_stream_kernel<1, kWhole>), grid, block, 0, s, a);
     else if (per_wave <= 2)
-        hipLaunchKernelGGL(mx_stream_kernel<2>, grid, block, 0, s, a);
+        hipLaunchKernelGGL((mx_stream_kernel<2, kWhole>), grid, block, 0, s, a);
     else if (per_wave <= 3)
-        hipLaunchKernelGGL(mx_stream_kernel<3>, grid, block, 0, s, a);
+        hipLaunchKernelGGL((mx_stream_kernel<3, kWhole>), grid, block, 0, s, a);
     else if (per_wave <= 5)
-        hipLaunchKernelGGL(mx_stream_kernel<5>, grid, block, 0, s, a);
+        hipLaunchKernelGGL((mx_stream_kernel<5, kWhole>), grid, block, 0, s, a);
     else
-        hipLaunchKernelGGL(mx_stream_kernel<8>, grid, block, 0, s, a);
+        hipLaunchKernelGGL((mx_stream_kernel<8, kWhole>), grid, block, 0, s, a);
 }
 
 template <int kWM, int kWN, int kMB, int kNB>
@@ -893,8 +918,11 @@ int linear_mxfp4_rows(const uint8_t *codes, const uint8_t *scales, const uint8_t
     a.tiles_m = p.tiles_m;
     a.tiles_n = p.tiles_n;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    if (p.kind == kStream)
-        launch_stream(a, dim3(p.tiles_n < 2 * cus ? p.tiles_n : 2 * cus, p.splits), s);
+    const dim3 stream_grid(p.tiles_n < 2 * cus ? p.tiles_n : 2 * cus, p.splits);
+    if (p.kind == kStream && K % 128 == 0)
+        launch_stream<true>(a, stream_grid, s);
+    else if (p.kind == kStream)
+        launch_stream<false>(a, stream_grid, s);
     else if (p.kind == kTile64)
         launch_tiles<2, 2, 1, 2>(a, s);
     else
