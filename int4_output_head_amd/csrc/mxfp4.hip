@@ -188,30 +188,11 @@ __device__ __forceinline__ float column_bias(const MxArgs &a, int n)
     return a.bias ? load_one(a.bias, n, a.dtype) : 0.0f;
 }
 
-__device__ __forceinline__ void finish_one(const MxArgs &a, int m, int n, float acc, float bias)
-{
-    float y[1] = {acc + bias};
-    activate(y, a.activation);
-    if (a.residual)
-        y[0] += load_one(a.residual, (size_t)m * a.residual_stride + n, a.dtype);
-    const size_t o = (size_t)m * a.out_stride + n;
-    if (a.dtype == INT4VH_ROWS_F32)
-        static_cast<float *>(a.out)[o] = y[0];
-    else
-        static_cast<uint16_t *>(a.out)[o] = (uint16_t)to_bits16(y[0], a.dtype);
-}
-
-// Four consecutive output elements at `to`; res: the residual's 16-bit words where
-// `with` is set.
+// Four consecutive output elements at `to`, but for the residual, whose 16-bit words
+// res are added where `with` is set.
 template <int kDtype>
-__device__ __forceinline__ void finish_four(const MxArgs &a, void *to, const f32x4 &acc, const float (&bias)[4],
-                                            bool with, uint2 res)
+__device__ __forceinline__ void store_four(void *to, const f32x4 &y, bool with, uint2 res)
 {
-    float y[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-        y[r] = acc[r] + bias[r];
-    activate(y, a.activation);
     if constexpr (kDtype == INT4VH_ROWS_F32) {
         Words4 v;
 #pragma unroll
@@ -219,17 +200,37 @@ __device__ __forceinline__ void finish_four(const MxArgs &a, void *to, const f32
             v.w[r] = __float_as_uint(y[r]);
         *static_cast<Words4 *>(to) = v;
     } else {
+        f32x4 z = y;
         if (with) {
-            y[0] += from_bits16(res.x & 0xFFFFu, kDtype);
-            y[1] += from_bits16(res.x >> 16, kDtype);
-            y[2] += from_bits16(res.y & 0xFFFFu, kDtype);
-            y[3] += from_bits16(res.y >> 16, kDtype);
+            z[0] += from_bits16(res.x & 0xFFFFu, kDtype);
+            z[1] += from_bits16(res.x >> 16, kDtype);
+            z[2] += from_bits16(res.y & 0xFFFFu, kDtype);
+            z[3] += from_bits16(res.y >> 16, kDtype);
         }
         Pair2 v;
-        v.w[0] = to_bits16(y[0], kDtype) | (to_bits16(y[1], kDtype) << 16);
-        v.w[1] = to_bits16(y[2], kDtype) | (to_bits16(y[3], kDtype) << 16);
+        v.w[0] = to_bits16(z[0], kDtype) | (to_bits16(z[1], kDtype) << 16);
+        v.w[1] = to_bits16(z[2], kDtype) | (to_bits16(z[3], kDtype) << 16);
         *static_cast<Pair2 *>(to) = v;
     }
+}
+
+// One output element, but for the residual.
+__device__ __forceinline__ void store_one(const MxArgs &a, int m, int n, float y)
+{
+    if (a.residual)
+        y += load_one(a.residual, (size_t)m * a.residual_stride + n, a.dtype);
+    const size_t o = (size_t)m * a.out_stride + n;
+    if (a.dtype == INT4VH_ROWS_F32)
+        static_cast<float *>(a.out)[o] = y;
+    else
+        static_cast<uint16_t *>(a.out)[o] = (uint16_t)to_bits16(y, a.dtype);
+}
+
+__device__ __forceinline__ void finish_one(const MxArgs &a, int m, int n, float acc, float bias)
+{
+    float y[1] = {acc + bias};
+    activate(y, a.activation);
+    store_one(a, m, n, y[0]);
 }
 
 // ---------------------------------------------------------------- up to 16 rows
@@ -354,7 +355,7 @@ __device__ __forceinline__ uint32_t lane_here()
 typedef const __attribute__((address_space(3))) u32x4 lds_words;
 __device__ __forceinline__ lds_words *lds_pointer(uint32_t at)
 {
-    return (lds_words *)at;
+    return (lds_words *)(size_t)at;
 }
 constexpr int waitcnt_vm(int n)
 {
@@ -373,7 +374,7 @@ __device__ __forceinline__ void copy_to_lds16(const uint8_t *base, uint32_t offs
 
 // A workgroup computes kWM*kMB*32 activation rows x kWN*kNB*32 weight rows with
 // kWM x kWN waves, in steps of 256 channels.  A step's codes are copied from
-// memory straight into one of two buffers in LDS while the other is multiplied:
+// memory straight into one of kRing buffers in LDS while another is multiplied:
 // 1 KB, 8 rows' 128 bytes (whole cache lines: with 64 bytes of 16 rows the
 // copies alone took 187 us instead of 137 for 8192^3), an instruction.  In LDS
 // chunk c of row r lies in slot 8 r + (c ^ (r / 2 % 8)), which spreads the reads
@@ -384,8 +385,15 @@ __device__ __forceinline__ void copy_to_lds16(const uint8_t *base, uint32_t offs
 // one, have its products to hide behind.  The scales, 16 bytes a row for 512
 // channels, are copied likewise for 1024 (kWhole), or go through registers where
 // rows do not end with a whole span of 512 or are not aligned to it.
-template <int kWM, int kWN, int kMB, int kNB, bool kWhole>
-__global__ void __launch_bounds__(64 * kWM *kWN, 2) mx_tile_kernel(MxArgs a)
+//
+// What bounds it is the way of the codes into LDS: without any product 8192^3
+// takes 295 us of 345, without the copies 229.  128 rows and two buffers, two
+// workgroups a compute unit, are the fastest where there is work for half the
+// card (4096 x 5120 x 8192: 105 us; three buffers, one workgroup 144; 64 rows
+// 147); a few tiles of 64 rows have a compute unit each, and there a third
+// buffer hides more of memory's latency (256 x 5120 x 5120: 13.1 us, two 15.6).
+template <int kWM, int kWN, int kMB, int kNB, int kRing, bool kWhole>
+__global__ void __launch_bounds__(64 * kWM *kWN, kRing == 2 ? 2 : 1) mx_tile_kernel(MxArgs a)
 {
     constexpr int kWaves = kWM * kWN;
     constexpr int kBM = kWM * kMB, kBN = kWN * kNB;           // blocks of 32
@@ -393,7 +401,7 @@ __global__ void __launch_bounds__(64 * kWM *kWN, 2) mx_tile_kernel(MxArgs a)
     constexpr int kPer = kRows / 8 / kWaves;                  // copies of a wave per step
     static_assert(kPer * kWaves * 8 == kRows && kBM * 32 % (8 * kWaves) == 0, "whole copies per wave, of one matrix each");
     struct Mem {
-        u32x4 code[2][kRows][8];
+        u32x4 code[kRing][kRows][8];
         u32x4 scale[2][kRows][2];
     };
     // the epilogue's use of LDS (per wave: 32 rows of sums)
@@ -551,7 +559,7 @@ __global__ void __launch_bounds__(64 * kWM *kWN, 2) mx_tile_kernel(MxArgs a)
         __builtin_amdgcn_sched_barrier(0);
     };
     auto landed = [&]() {
-        __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm((kRing - 2) * kPer));
         __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
         barrier_no_fence();
     };
@@ -563,20 +571,21 @@ __global__ void __launch_bounds__(64 * kWM *kWN, 2) mx_tile_kernel(MxArgs a)
         using I = std::integral_constant<int, 1>;
         using II = std::integral_constant<int, 2>;
         using III = std::integral_constant<int, 3>;
-        read(at, kS, 1);
+        const int buf = (at - 2 * p0) % kRing, other = (at - 2 * p0 + 1) % kRing;
+        read(at, buf, 1);
         multiply(s, Z());
-        read(at, kS, 2);
+        read(at, buf, 2);
         multiply(s, I());
-        read(at, kS, 3);
+        read(at, buf, 3);
         multiply(s, II());
         // all have read this buffer, and the next step's has landed
         landed();
-        load(at + 2, kS);
+        load(at + kRing, buf);
         if (kWhole && kS == 0 && (span - p0) % 2 == 0)
             copy_scales(span + 2, ((span - p0) / 2 + 1) & 1);
         if (!kWhole && kS == 0)
             load_scales(span + 1);
-        read(at + 1, kS ^ 1, 0);
+        read(at + 1, other, 0);
         multiply(s, III());
         if (kS == 1)
             read_scales(span + 1 - p0);
@@ -594,7 +603,6 @@ __global__ void __launch_bounds__(64 * kWM *kWN, 2) mx_tile_kernel(MxArgs a)
     const bool early = wide && a.residual;
     // The usual residual is asked for up front: it takes a memory's latency.
     Pair2 res[kMB][kIter];
-    load(2 * p0, 0);
     if (early)
 #pragma unroll
         for (int i = 0; i < kMB; ++i)
@@ -610,8 +618,10 @@ __global__ void __launch_bounds__(64 * kWM *kWN, 2) mx_tile_kernel(MxArgs a)
         load_scales(p0);
         store_scales(0);
     }
-    load(2 * p0 + 1, 1);
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm(kPer));
+#pragma unroll
+    for (int i = 0; i < kRing; ++i)
+        load(2 * p0 + i, i);
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm((kRing - 1) * kPer));
     __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
     barrier_no_fence();
     read_scales(0);
@@ -627,11 +637,35 @@ __global__ void __launch_bounds__(64 * kWM *kWN, 2) mx_tile_kernel(MxArgs a)
     // 32) + r % 4.  Each wave turns its sums around in LDS, 32 activation rows at a
     // time, so that its lanes hold four columns of a row and rows are written whole.
     float *turn = reinterpret_cast<float *>(mem) + wave * kArea;
-    float bs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (!a.parts)
+    // Bias and activation where the sums are: what is executed once for every four
+    // outputs below stays short (with the activations there, every one of its
+    // copies was an instruction cache miss, 3 us a block of sums).
+    if (!a.parts) {
+        if (a.bias)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-            bs[r] = column_bias(a, min(n + r, a.N - 1));
+            for (int j = 0; j < kNB; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const float b = column_bias(a, min(n0 + (wn * kNB + j) * 32 + 8 * (r / 4) + 4 * half + r % 4, a.N - 1));
+#pragma unroll
+                    for (int i = 0; i < kMB; ++i)
+                        acc[i][j][r] += b;
+                }
+        if (a.activation != INT4VH_ACT_NONE)
+#pragma unroll
+            for (int i = 0; i < kMB; ++i)
+#pragma unroll
+                for (int j = 0; j < kNB; ++j) {
+                    float y[16];
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        y[r] = acc[i][j][r];
+                    activate(y, a.activation);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        acc[i][j][r] = y[r];
+                }
+    }
     __builtin_amdgcn_s_waitcnt(0);
     barrier_no_fence();                                        // the last step's reads and copies are done
     // sums of 32 activation rows, turned
@@ -656,7 +690,7 @@ __global__ void __launch_bounds__(64 * kWM *kWN, 2) mx_tile_kernel(MxArgs a)
             for (int k = 0; k < kIter; ++k) {
                 const f32x4 v = *reinterpret_cast<const f32x4 *>(turn + (lr + k * kStep) * kPitch + c4);
                 if (m + k * kStep < a.M && n < a.N)
-                    finish_four<kDtype>(a, to, v, bs, early, make_uint2(res[i][k].w[0], res[i][k].w[1]));
+                    store_four<kDtype>(to, v, early, make_uint2(res[i][k].w[0], res[i][k].w[1]));
                 to += (size_t)kStep * a.out_stride * kSize;
             }
             wave_fence();
@@ -686,7 +720,7 @@ __global__ void __launch_bounds__(64 * kWM *kWN, 2) mx_tile_kernel(MxArgs a)
             for (int e = lane; e < 32 * kCols; e += 64) {
                 const int m = mi + e / kCols, c = n0 + wn * kCols + e % kCols;
                 if (m < a.M && c < a.N)
-                    finish_one(a, m, c, turn[e / kCols * kPitch + e % kCols], column_bias(a, c));
+                    store_one(a, m, c, turn[e / kCols * kPitch + e % kCols]);
             }
         }
         wave_fence();
@@ -707,6 +741,9 @@ __global__ void __launch_bounds__(256) mx_join_kernel(MxArgs a)
 }
 
 // ---------------------------------------------------------------- host side
+
+// Spans of 512 channels that parts of K have to save a workgroup.
+constexpr int kSplitGain = 7;
 
 // How a call of these sizes runs.
 enum Kind { kStream, kTile64, kTile128 };      // tiles of 64, 128 rows x 128 columns
@@ -736,10 +773,18 @@ Plan plan_for(int M, int N, int K, int cus)
         const int bm = p.kind == kTile128 ? 128 : 64;
         p.tiles_m = (M + bm - 1) / bm;
         p.tiles_n = (N + 127) / 128;
-        // few tiles: parts of a span at least, up to two workgroups a compute unit
-        if (p.kind == kTile64)
-            while (2 * p.splits * tiles_of(M, N, 64) <= 2ll * cus && spans / (2 * p.splits) >= 1)
-                p.splits *= 2;
+        // Few tiles: parts of K, up to a workgroup a compute unit, where that takes
+        // kSplitGain spans out of a workgroup's way.  A span is about 1 us, and
+        // writing and joining the parts cost about 6: 64 x 5120 x 17408 takes 29.2 us
+        // whole and 16.3 in 4 parts, 17 x 5120 x 5120 12.1 and 10.5, but
+        // 128 x 5120 x 5120 12.8 whole and 14.6 in 2.
+        if (p.kind == kTile64) {
+            int s = 1;
+            while (2 * s * tiles_of(M, N, 64) <= cus && spans / (2 * s) >= 2)
+                s *= 2;
+            if (spans - (spans + s - 1) / s >= kSplitGain)
+                p.splits = s;
+        }
     }
     p.split_spans = (spans + p.splits - 1) / p.splits;
     p.splits = (spans + p.split_spans - 1) / p.split_spans;
@@ -789,14 +834,14 @@ void launch_stream(const MxArgs &a, dim3 grid, hipStream_t s)
         hipLaunchKernelGGL((mx_stream_kernel<8, kWhole>), grid, block, 0, s, a);
 }
 
-template <int kWM, int kWN, int kMB, int kNB>
+template <int kWM, int kWN, int kMB, int kNB, int kRing>
 void launch_tiles(const MxArgs &a, hipStream_t s)
 {
     const dim3 grid((unsigned)((long long)a.tiles_m * a.tiles_n * a.splits)), block(64 * kWM * kWN);
     if (a.K % 512 == 0 && rows_aligned(a.x_scales, 16) && rows_aligned(a.w_scales, 16))
-        hipLaunchKernelGGL((mx_tile_kernel<kWM, kWN, kMB, kNB, true>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((mx_tile_kernel<kWM, kWN, kMB, kNB, kRing, true>), grid, block, 0, s, a);
     else
-        hipLaunchKernelGGL((mx_tile_kernel<kWM, kWN, kMB, kNB, false>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((mx_tile_kernel<kWM, kWN, kMB, kNB, kRing, false>), grid, block, 0, s, a);
 }
 
 template <int kDtype>
@@ -924,9 +969,9 @@ int linear_mxfp4_rows(const uint8_t *codes, const uint8_t *scales, const uint8_t
     else if (p.kind == kStream)
         launch_stream<false>(a, stream_grid, s);
     else if (p.kind == kTile64)
-        launch_tiles<2, 2, 1, 2>(a, s);
+        launch_tiles<2, 2, 1, 2, 3>(a, s);
     else
-        launch_tiles<2, 2, 2, 2>(a, s);
+        launch_tiles<2, 2, 2, 2, 2>(a, s);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return hip_fail(e, "mxfp4 linear kernel launch");
