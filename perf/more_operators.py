@@ -354,6 +354,8 @@ def _run_own(s):
     from int4_output_head_amd import binding
 
     act = None if s.get("act") == "none" else s.get("act")
+    if s["op"] in ("block", "block8") and s["gate"] is None:
+        act = None                             # without a gate there is none to activate
     if s["op"] == "block":
         normed, total = binding.rms_norm_block(s["x"], s["residual"], s["post"], s["pre"], gate=s["gate"],
                                                gate_activation=act, scale=s["scale"], eps=s["eps"],
