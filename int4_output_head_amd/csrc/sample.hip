@@ -254,7 +254,7 @@ __device__ __forceinline__ float lowest_kept(const SampleArgs &a, const Settings
     low = fmaxf(low, -3.402823466e38f);
     const int want = set.k > 0 ? (set.k + each - 1) / each : 0;
     if (set.k == 1)
-        low = gm;
+        low = fmaxf(gm, -3.402823466e38f);    // not -infinity, which all of a row without a token has
     else if (want > 0 && want <= n && want <= 64 * kGroups) {
         // a word that at least `want` groups reach, two bits at a time
         uint32_t word[kGroups], th = 0u;

@@ -312,6 +312,26 @@ def test_longest_rows(b):
         check(got, x.double().numpy(), [s], u)
 
 
+@pytest.mark.parametrize("M,V", [(40, 1025), (2, 33), (1, 3001), (9, 9000)])
+def test_rows_without_a_token(b, M, V):
+    """Rows of which nothing is allowed leave their neighbours, and what lies behind the workspace, as they are."""
+    x = logits(M, V, torch.float32, M)
+    x[::2] = -math.inf
+    x[::4, ::3] = math.nan
+    u = torch.linspace(0, 0.999, M)
+    L, dev, du = b.load_library(), x.cuda(), u.cuda()
+    need = L.sample_logits_workspace_bytes(M, 1, V)
+    for s in ((0.0, 0, 1.0, 0.0), (1.0, 1, 1.0, 0.0), (1.0, 5, 0.9, 0.0), (1.0, 0, 0.9, 0.1), (1.0, 0, 1.0, 0.0)):
+        ids, probs = torch.empty(M, dtype=torch.int32).cuda(), torch.empty(M).cuda()
+        ws = torch.full((need + 65536,), 0xA5, dtype=torch.uint8).cuda()
+        st = L.sample_logits_rows(dev.data_ptr(), V, 2, None, M, 1, V, None, b._SAMPLING.pack(0, 0, 0, 0, *s),
+                                  du.data_ptr(), None, ids.data_ptr(), probs.data_ptr(), None, None,
+                                  ws.data_ptr(), need, torch.cuda.current_stream().cuda_stream)
+        assert st == 0
+        check((ids, probs, None, None), x.double().numpy(), [s] * M, u)
+        assert (ids[::2] == -1).all() and bool((ws[need:] == 0xA5).all())
+
+
 @pytest.mark.parametrize("n", [300, 700, 5000])
 def test_fewer_tokens_than_top_k(b, n):
     """A row that holds no top_k tokens above -infinity: top_p and min_p still hold."""
