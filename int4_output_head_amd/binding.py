@@ -820,6 +820,16 @@ def quantize_rows(x, *, channel_scales=None):
 _GATES = {None: 0, "sigmoid": 1}
 
 
+def _norm_weight(w, name, H, index):
+    """Address and type of a norm's weight."""
+    code = _row_code(w, name)
+    if w.shape != (H,) or not w.is_contiguous():
+        raise ValueError(f"{name} must be contiguous [H]")
+    if w.get_device() != index:
+        _same_device(index, **{name: w})
+    return w.data_ptr(), code
+
+
 def _block_args(x, residual, post_weight, pre_weight, gate, gate_activation):
     """The leading arguments of both block norms, and (M, H, device index, sum)."""
     dt = _row_code(x, "x")
@@ -828,15 +838,16 @@ def _block_args(x, residual, post_weight, pre_weight, gate, gate_activation):
     if _row_code(residual, "residual") != dt or residual.shape != x.shape:
         raise ValueError("residual must have the type and shape of x")
     rs = _rows2d(residual, "residual")[2]
-    wdt = None
-    for w, name in ((post_weight, "post_weight"), (pre_weight, "pre_weight")):
-        if w is not None:
-            code = _row_code(w, name)
-            if w.shape != (H,) or not w.is_contiguous():
-                raise ValueError(f"{name} must be contiguous [H]")
-            if wdt is not None and wdt != code:
-                raise TypeError("post_weight and pre_weight must have one type")
-            wdt = code
+    if residual.get_device() != index:
+        _same_device(index, residual=residual)
+    wdt = post = pre = at = None
+    if post_weight is not None:
+        post, wdt = _norm_weight(post_weight, "post_weight", H, index)
+    if pre_weight is not None:
+        pre, code = _norm_weight(pre_weight, "pre_weight", H, index)
+        if post is not None and wdt != code:
+            raise TypeError("post_weight and pre_weight must have one type")
+        wdt = code
     act = _GATES.get(gate_activation)
     if act is None:
         raise ValueError("gate_activation must be None or 'sigmoid'")
@@ -848,12 +859,13 @@ def _block_args(x, residual, post_weight, pre_weight, gate, gate_activation):
             gs = _rows2d(gate, "gate")[2]
         elif gate.shape != (H,) or not gate.is_contiguous():
             raise ValueError("gate must be contiguous [H], or of the shape of x")
+        if gate.get_device() != index:
+            _same_device(index, gate=gate)
+        at = gate.data_ptr()
     elif act:
         raise ValueError("gate_activation needs a gate")
-    _same_device(index, residual=residual, post_weight=post_weight, pre_weight=pre_weight, gate=gate)
     total = torch.empty_like(x, memory_format=torch.contiguous_format)
-    return ((x.data_ptr(), xs, residual.data_ptr(), rs, _at(gate), gs, act, dt, _at(post_weight), _at(pre_weight),
-             wdt or 0), M, H, index, total)
+    return (x.data_ptr(), xs, residual.data_ptr(), rs, at, gs, act, dt, post, pre, wdt or 0), M, H, index, total
 
 
 def rms_norm_block(x, residual, post_weight=None, pre_weight=None, *, gate=None, gate_activation=None,
@@ -870,7 +882,9 @@ def rms_norm_block(x, residual, post_weight=None, pre_weight=None, *, gate=None,
     odt = _ROW_DTYPES.get(out_dtype)
     if odt is None:
         raise TypeError("out_dtype must be float16, bfloat16 or float32")
-    out = None if pre_weight is None else x.new_empty(x.shape, dtype=out_dtype)
+    out = None
+    if pre_weight is not None:
+        out = torch.empty_like(total) if odt == args[7] else torch.empty_like(total, dtype=out_dtype)
     st = _on(index, load_library().rms_norm_block_rows, *args, scale, M, H, eps, total.data_ptr(), _at(out), odt,
              _raw_stream(index))
     if st != OK:
@@ -890,7 +904,7 @@ def rms_norm_block_int8(x, residual, post_weight, pre_weight, *, gate=None, gate
         _vector(channel_scales, "channel_scales", torch.float16, H)
         _same_device(index, channel_scales=channel_scales)
         cs = channel_scales.data_ptr()
-    codes = x.new_empty(x.shape, dtype=torch.int8)
+    codes = torch.empty_like(total, dtype=torch.int8)
     row_scales = x.new_empty(M, dtype=torch.float32)
     st = _on(index, load_library().rms_norm_block_rows_int8, *args, cs, scale, M, H, eps, total.data_ptr(),
              codes.data_ptr(), row_scales.data_ptr(), _raw_stream(index))
@@ -993,6 +1007,12 @@ def quantize_mxfp4(x):
 
 def _mx_rows(codes, scales, names=("codes", "scales")):
     """(M, K) of a matrix in 4-bit floating point."""
+    if (isinstance(codes, torch.Tensor) and isinstance(scales, torch.Tensor) and codes.dim() == 2 and codes.is_cuda
+            and scales.is_cuda and codes.dtype == scales.dtype == torch.uint8 and codes.is_contiguous()
+            and scales.is_contiguous()):
+        M, half = codes.shape                  # the usual matrix
+        if 1 <= M <= 0x7FFFFFFF and half >= 16 and half % 16 == 0 and scales.shape == (M, half // 16):
+            return M, 2 * half
     for t, name in ((codes, names[0]), (scales, names[1])):
         if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.uint8:
             raise TypeError(f"{name} must be a CUDA (HIP) uint8 tensor")
@@ -1064,7 +1084,10 @@ def linear_mxfp4(codes, scales, w_codes, w_scales, *, bias=None, activation=None
         if _row_code(out, "out") != dt or out.shape != shape:
             raise ValueError("out must be [..., N] of out_dtype")
         os_ = _rows2d(out, "out")[2]
-    _same_device(index, scales=scales, w_codes=w_codes, w_scales=w_scales, bias=bias, residual=residual, out=out)
+    for t in (scales, w_codes, w_scales, bias, residual, out):
+        if t is not None and t.get_device() != index:
+            _same_device(index, scales=scales, w_codes=w_codes, w_scales=w_scales, bias=bias, residual=residual,
+                         out=out)
     st = _on(index, _launch_linear_mxfp4, index, codes, scales.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
              _at(bias), act, _at(residual), rs, M, N, K, out.data_ptr(), os_, dt)
     if st != OK:
@@ -1389,7 +1412,8 @@ def sample_logits(logits, uniforms, rules=None, draft_ids=None, *, R: int | None
         raise TypeError("top_k must be a whole number or an int32 tensor")
     settings = _SAMPLING.pack(pt, pk, pp, pm, t, min(max(k, -1), V), p, m)
     new = logits.new_empty
-    ids, probs = new(M, dtype=i), new(M, dtype=f)
+    probs = torch.empty_like(uniforms) if uniforms.dim() == 1 else new(M, dtype=f)
+    ids = torch.empty_like(probs, dtype=i)
     ac = pdr = nacc = None
     if accept is not None:
         if T == 1:
