@@ -447,20 +447,118 @@ struct BlockArgs {
     float scale, eps;
 };
 
+// e / (1 + e) or 1 / (1 + e) of e = exp(-|g|), which neither overflows: with the
+// product's lost digits added to e, and a step of Newton's on the reciprocal, the
+// error is at most 6 half steps (libm's exp and a division took 22 instructions
+// instead of 14).  NaN stays.
+__device__ __forceinline__ float sigmoid(float g)
+{
+    const float a = fminf(fabsf(g), 104.0f), hi = a * -1.44269502e+00f;
+    const float lo = __builtin_fmaf(a, -1.92596299e-08f, __builtin_fmaf(a, -1.44269502e+00f, -hi));
+    float e = __builtin_amdgcn_exp2f(hi);
+    e = __builtin_fmaf(e, lo * 6.93147182e-01f, e);
+    const float d = 1.0f + e, r = __builtin_amdgcn_rcpf(d);
+    const float s = (g < 0.0f ? e : 1.0f) * __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+    return g == g ? s : g;
+}
 __device__ __forceinline__ void gate_values(float (&g)[8], int activation)
 {
     if (activation == INT4VH_GATE_SIGMOID)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            g[j] = 1.0f / (1.0f + expf(-g[j]));
+            g[j] = sigmoid(g[j]);
 }
+
+// Eight values of a row as they lie in memory; those past H are 0.
+template <int kDtype>
+struct Raw8 {
+    static constexpr int kWords = kDtype == INT4VH_ROWS_F32 ? 8 : 4;
+    uint32_t w[kWords];
+
+    __device__ __forceinline__ void load(const void *row, int c, int H)
+    {
+        if (c + 8 <= H) {
+            const Words4 *p = reinterpret_cast<const Words4 *>(static_cast<const char *>(row) + (size_t)c * (kWords / 2));
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i) {
+                const Words4 v = p[i];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[4 * i + j] = v.w[j];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kWords; ++j)
+                w[j] = 0u;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c + j < H) {
+                    if constexpr (kDtype == INT4VH_ROWS_F32)
+                        w[j] = static_cast<const uint32_t *>(row)[c + j];
+                    else
+                        w[j / 2] |= (uint32_t) static_cast<const uint16_t *>(row)[c + j] << (j % 2 * 16);
+                }
+        }
+    }
+    template <int kAs = kDtype>
+    __device__ __forceinline__ void values(float (&v)[8]) const
+    {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (kAs == INT4VH_ROWS_F32)
+                v[j] = __uint_as_float(w[j]);
+            else
+                v[j] = from_bits16((w[j / 2] >> (j % 2 * 16)) & 0xFFFFu, kAs);
+        }
+    }
+};
+
+template <int kDtype>
+__device__ __forceinline__ void hold(Raw8<kDtype> &r)
+{
+#pragma unroll
+    for (int i = 0; i < r.kWords; ++i)
+        asm volatile("" : "+v"(r.w[i]));
+}
+
+// Eight channels of a weight of any type: 16-bit ones stay as they lie in memory,
+// binary32 ones are loaded again for each row (L1's and L2's), so that all take
+// four registers.
+struct Weight8 {
+    Raw8<INT4VH_ROWS_F16> raw;
+    const void *from;
+    int dtype;
+
+    __device__ __forceinline__ Weight8(const void *weight, int type, int c, int H) : from(weight), dtype(type)
+    {
+        if (from && dtype != INT4VH_ROWS_F32)
+            raw.load(from, c, H);
+    }
+    // (held back: converted ahead of the rows they would take eight registers)
+    __device__ __forceinline__ void values(int c, int H, float (&v)[8])
+    {
+        hold(raw);
+        if (dtype == INT4VH_ROWS_F16)
+            raw.values(v);
+        else if (dtype == INT4VH_ROWS_BF16)
+            raw.values<INT4VH_ROWS_BF16>(v);
+        else
+            load8<INT4VH_ROWS_F32>(from, c, H, v);
+    }
+};
 
 // The norm behind a block, its gate and scale, the residual's addition and the
 // next block's norm: norm_rows_kernel with a second reduction in front.  The
 // block's output is normed in registers, so that the row is still read and
 // written once; the two reductions have LDS of their own and a barrier each.
+// A whole row waits at each, so what hides memory's latency is a second workgroup
+// on the compute unit: rows of 8192 channels take 1024 threads, and two of those
+// 64 registers a thread, which is why the weights stay packed (4096 x 8192 in
+// bfloat16 with a gate of elements, 336 MB: 78 us, 4.3 TB/s; with the weights
+// converted ahead of the rows 110, and with the next row's loads ahead of the
+// reductions, which takes one of the workgroups, 100).
 template <int kDtype, bool kInt8>
-__global__ void __launch_bounds__(kMaxThreads) norm_block_kernel(BlockArgs a)
+__global__ void __launch_bounds__(kMaxThreads, kDtype == INT4VH_ROWS_F32 ? 4 : 8) norm_block_kernel(BlockArgs a)
 {
     __shared__ float s_post[2][kMaxThreads / 64];
     __shared__ float s_sum[2][kMaxThreads / 64];
@@ -472,24 +570,8 @@ __global__ void __launch_bounds__(kMaxThreads) norm_block_kernel(BlockArgs a)
     const size_t out_size = a.out_dtype == INT4VH_ROWS_F32 ? 4 : 2;
 
     const int c = 8 * tid;                     // this thread's first channel
-    float post[8], pre[8], gate[8], cs[8];
-    if (a.post)
-        load8_any(a.post, a.weight_dtype, c, H, post);
-    if (a.pre)
-        load8_any(a.pre, a.weight_dtype, c, H, pre);
-    if (a.gate && a.gate_stride == 0) {
-        load8<kDtype>(a.gate, c, H, gate);
-        gate_values(gate, a.gate_activation);
-    }
-    if (kInt8) {
-        if (a.channel) {
-            load8<INT4VH_ROWS_F16>(a.channel, c, H, cs);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                cs[j] = 1.0f;
-        }
-    }
+    Weight8 post(a.post, a.weight_dtype, c, H), pre(a.pre, a.weight_dtype, c, H);
+    Weight8 cs(kInt8 ? a.channel : nullptr, INT4VH_ROWS_F16, c, H);
     // sums of squares that serve as they are
     const float low_sum = a.eps < kLowMean ? kLowMean * (float)H : 0.0f;
     const float high_sum = a.eps < 0x1p126f ? 0x1p127f : 0.0f;
@@ -526,13 +608,17 @@ __global__ void __launch_bounds__(kMaxThreads) norm_block_kernel(BlockArgs a)
         return 1.0f / sqrtf(ss / (float)H + eps);
     };
 
+    Raw8<kDtype> rx, rr, gate;
+    if (a.gate)
+        gate.load(a.gate, c, H);               // a gate of channels stays
     int buf = 0;
     for (unsigned m = blockIdx.x; m < (unsigned)a.M; m += gridDim.x, buf ^= 1) {
-        float u[8], h[8];
-        load8<kDtype>(static_cast<const char *>(a.x) + (size_t)m * a.x_stride * kSize, c, H, u);
-        load8<kDtype>(static_cast<const char *>(a.residual) + (size_t)m * a.residual_stride * kSize, c, H, h);
+        float u[8], h[8], f[8];
+        rx.load(static_cast<const char *>(a.x) + (size_t)m * a.x_stride * kSize, c, H);
+        rr.load(static_cast<const char *>(a.residual) + (size_t)m * a.residual_stride * kSize, c, H);
         if (a.gate_stride)
-            load8<kDtype>(static_cast<const char *>(a.gate) + (size_t)m * a.gate_stride * kSize, c, H, gate);
+            gate.load(static_cast<const char *>(a.gate) + (size_t)m * a.gate_stride * kSize, c, H);
+        rx.values(u);
         float before, behind;
         uint32_t none = 0u;
         if (a.post) {
@@ -549,16 +635,20 @@ __global__ void __launch_bounds__(kMaxThreads) norm_block_kernel(BlockArgs a)
                 reduce<16, true, false>(ss, none);
             }
             const float rstd = factor(u, ss, s_again[0], before, behind);
+            post.values(c, H, f);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                u[j] = u[j] * rstd * behind * post[j];
+                u[j] = u[j] * rstd * behind * f[j];
         }
-        if (a.gate_stride)
-            gate_values(gate, a.gate_activation);
-        if (a.gate)
+        if (a.gate) {
+            hold(gate);
+            gate.values(f);
+            gate_values(f, a.gate_activation);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                u[j] *= gate[j];
+                u[j] *= f[j];
+        }
+        rr.values(h);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             h[j] += u[j] * a.scale;
@@ -569,12 +659,23 @@ __global__ void __launch_bounds__(kMaxThreads) norm_block_kernel(BlockArgs a)
         float t[8];                            // what 8 bits stand for, up to rstd
         float ss = 0.0f;
         uint32_t peak = 0u;
+        if (kInt8) {
+            pre.values(c, H, t);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                t[j] *= h[j];
+            if (a.channel) {
+                cs.values(c, H, f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    t[j] *= f[j];
+            }
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             // channels past H hold 0 here: x, the residual and the gate do
             ss = __builtin_fmaf(h[j], h[j], ss);
             if (kInt8) {
-                t[j] = h[j] * pre[j] * cs[j];
                 const uint32_t w = __float_as_uint(t[j]) & 0x7FFFFFFFu;
                 peak = w > peak ? w : peak;
             }
@@ -610,9 +711,10 @@ __global__ void __launch_bounds__(kMaxThreads) norm_block_kernel(BlockArgs a)
         } else {
             const float rstd = factor(h, ss, s_again[1], before, behind);
             float y[8];
+            pre.values(c, H, f);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                y[j] = h[j] * rstd * behind * pre[j];
+                y[j] = h[j] * rstd * behind * f[j];
             store8(static_cast<char *>(a.out) + (size_t)m * H * out_size, a.out_dtype, c, H, y);
         }
     }
@@ -627,7 +729,10 @@ int launch_block_rows(const BlockArgs &a, hipStream_t s)
         return hip_fail(e, "hipGetDevice");
     const int nt = (a.H + 511) / 512 * 64;
     const int resident = cu_count(dev) * (2048 / nt);
-    const int grid = a.M < resident ? a.M : resident;
+    // Four rounds of workgroups: as they end at different times, the next ones'
+    // loads fill the gaps (bfloat16 4096 x 5120, gated: 63 us in one round, 54 in
+    // four or a workgroup a row; binary32 4096 x 8192 133, 137 and 140).
+    const int grid = a.M < 4 * resident ? a.M : 4 * resident;
     hipLaunchKernelGGL((norm_block_kernel<kDtype, kInt8>), dim3(grid), dim3(nt), 0, s, a);
     e = hipGetLastError();
     return e == hipSuccess ? INT4VH_OK : hip_fail(e, "block norm kernel launch");

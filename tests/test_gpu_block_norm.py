@@ -163,6 +163,20 @@ def test_rows_whose_squares_leave_binary32(b, dt, e):
                                      gate=dev["gate"], eps=0.0), s, None, eps=0.0)
 
 
+def test_gates_at_their_ends(b):
+    """Sigmoids of gates over all of binary32; one below 2^-126, the smallest normal number, may count as 0."""
+    z = torch.cat([torch.linspace(-110, 110, 4001), torch.tensor([0.0, -0.0, 1e-38, -1e-38, 1e30, -1e30, 3e38, -3e38,
+                                                                  float("inf"), -float("inf"), 87.5, -87.5, 1e-4, -1e-4])])
+    H = len(z)
+    x, r = torch.full((2, H), 3.0), torch.zeros(2, H)
+    total = b.rms_norm_block(x.cuda(), r.cuda(), gate=z.cuda(), gate_activation="sigmoid")[1]
+    want = 3.0 / (1.0 + np.exp(-f64(z)))
+    assert np.all(np.abs(f64(total) - want) <= 40 * U * want + U * want + 3.0 * 2.0 ** -126)
+    z[7] = float("nan")
+    total = b.rms_norm_block(x.cuda(), r.cuda(), gate=z.cuda(), gate_activation="sigmoid")[1].cpu()
+    assert total[:, 7].isnan().all() and total.isnan().sum() == 2
+
+
 def test_bad_values_stay_in_their_rows(b):
     s = make(6, 600, torch.float32, 9)
     clean = {k: gpu(v) for k, v in s.items()}
