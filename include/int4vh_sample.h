@@ -37,7 +37,7 @@
  *
  * Numerics.  The ruled logits are binary32; masses are computed in binary64 and
  * added as whole multiples of 2^-b, b = 62 - ceil(log2(V)) (44 for 151936
- * tokens), so that sums do not depend on an order; a mass below half of that
+ * tokens) and at most 50, so that sums do not depend on an order; a mass below half of that
  * counts as none, and its token is not drawn.  The sums of 1024 tokens from which
  * those of a whole row are made are binary64 in a fixed order.  Results are the
  * same in every run.

@@ -332,6 +332,26 @@ def test_rows_without_a_token(b, M, V):
         assert (ids[::2] == -1).all() and bool((ws[need:] == 0xA5).all())
 
 
+@pytest.mark.parametrize("V", [5000, 9000, 40000])
+@pytest.mark.parametrize("shape", ["flat", "shelf"])
+def test_many_candidates(b, V, shape):
+    """Thousands of candidates, of which few or most are kept, with and without drafts."""
+    R, T = 3, 2
+    g = torch.Generator().manual_seed(V)
+    x = torch.randn(R * T, V, generator=g)
+    if shape == "shelf":
+        x[:, : V // 4] += 6.0                   # most of the mass in a quarter of the tokens
+    u = torch.rand(R * T, generator=g)
+    d = x.topk(3, dim=1).indices.view(R, T, 3)[:, : T - 1, 1].to(torch.int32).contiguous()
+    accept = torch.rand(R, T - 1, generator=g)
+    for s in ((1.0, 0, 0.3, 0.0), (1.0, 0, 0.9, 0.0), (0.5, 0, 0.999, 0.0), (1.0, V // 3, 1.0, 0.0),
+              (1.0, V - 1, 0.6, 0.0), (3.0, 4200, 0.99, 0.01), (1.0, 0, 0.7, 0.2)):
+        kw = dict(R=R, temperature=s[0], top_k=s[1], top_p=s[2], min_p=s[3])
+        check(b.sample_logits(x.cuda(), u.cuda(), None, d.cuda(), **kw), x.double().numpy(), [s] * R, u, R=R, T=T)
+        check(b.sample_logits(x.cuda(), u.cuda(), None, d.cuda(), accept=accept.cuda(), **kw), x.double().numpy(),
+              [s] * R, u, d, accept, R, T)
+
+
 @pytest.mark.parametrize("n", [300, 700, 5000])
 def test_fewer_tokens_than_top_k(b, n):
     """A row that holds no top_k tokens above -infinity: top_p and min_p still hold."""
