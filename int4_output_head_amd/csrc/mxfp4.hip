@@ -128,21 +128,20 @@ __global__ void __launch_bounds__(256) dequantize_mxfp4_kernel(const uint32_t *c
                                                                long long chunks, void *out)
 {
     constexpr size_t kSize = kDtype == INT4VH_ROWS_F32 ? 4 : 2;
-    const long long c = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (c >= chunks)
-        return;
-    const uint32_t q = codes[c];
-    const int s = scales[c >> 2];
-    f32x2 p[4];
-    p[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 0);
-    p[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 1);
-    p[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 2);
-    p[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 3);
-    float v[8];
+    for (long long c = (long long)blockIdx.x * 256 + threadIdx.x; c < chunks; c += (long long)gridDim.x * 256) {
+        const uint32_t q = codes[c];
+        const int s = scales[c >> 2];
+        f32x2 p[4];
+        p[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 0);
+        p[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 1);
+        p[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 2);
+        p[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 3);
+        float v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        v[j] = s == 255 ? __builtin_nanf("") : __builtin_amdgcn_ldexpf(p[j >> 1][j & 1], s - 127);
-    store_values8<kDtype>(static_cast<char *>(out) + (size_t)c * 8 * kSize, v);
+        for (int j = 0; j < 8; ++j)
+            v[j] = s == 255 ? __builtin_nanf("") : __builtin_amdgcn_ldexpf(p[j >> 1][j & 1], s - 127);
+        store_values8<kDtype>(static_cast<char *>(out) + (size_t)c * 8 * kSize, v);
+    }
 }
 
 // ---------------------------------------------------------------- products
@@ -844,10 +843,13 @@ void launch_tiles(const MxArgs &a, hipStream_t s)
         hipLaunchKernelGGL((mx_tile_kernel<kWM, kWN, kMB, kNB, kRing, false>), grid, block, 0, s, a);
 }
 
+constexpr long long kGridThreads = 1ll << 31;
+
 template <int kDtype>
 void launch_quantize(const void *x, int64_t x_stride, int M, int H, uint8_t *codes, uint8_t *scales, hipStream_t s)
 {
-    const bool flat = M == 1 || x_stride == H;         // one long row
+    // one long row, unless it would take more threads than a grid may have
+    const bool flat = M == 1 || (x_stride == H && (long long)M * H / 8 <= kGridThreads);
     const long long chunks = flat ? (long long)M * H / 8 : H / 8;
     const int rows = flat ? 1 : M;
     const dim3 grid((unsigned)((chunks + 255) / 256), rows < 65535 ? rows : 65535);
@@ -859,7 +861,8 @@ template <int kDtype>
 void launch_dequantize(const uint8_t *codes, const uint8_t *scales, int M, int H, void *out, hipStream_t s)
 {
     const long long chunks = (long long)M * H / 8;
-    hipLaunchKernelGGL(dequantize_mxfp4_kernel<kDtype>, dim3((unsigned)((chunks + 255) / 256)), dim3(256), 0, s,
+    const long long threads = chunks < kGridThreads ? chunks : kGridThreads;
+    hipLaunchKernelGGL(dequantize_mxfp4_kernel<kDtype>, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s,
                        reinterpret_cast<const uint32_t *>(codes), scales, chunks, out);
 }
 

@@ -45,6 +45,21 @@ def test_quantize_many_rows(b):
         assert torch.equal(b.dequantize_mxfp4(c, s, out_dtype=torch.bfloat16), back[at: at + 3])
 
 
+def test_quantize_more_chunks_than_a_grid_has_threads(b):
+    """2^35 + 2^18 channels, 8 of them a thread."""
+    M, H = (1 << 19) + 4, 65536
+    x = torch.empty(M, H, dtype=torch.bfloat16, device="cuda")
+    x.random_(-100, 100)
+    codes, scales = b.quantize_mxfp4(x)
+    at = [0, (1 << 18) - 1, 1 << 18, (1 << 19) - 1, 1 << 19, M - 1]
+    want = [b.quantize_mxfp4(x[i: i + 1].contiguous()) for i in at]
+    del x
+    back = b.dequantize_mxfp4(codes, scales, out_dtype=torch.bfloat16)
+    for i, (c, s) in zip(at, want):
+        assert torch.equal(c[0], codes[i]) and torch.equal(s[0], scales[i])
+        assert torch.equal(b.dequantize_mxfp4(c, s, out_dtype=torch.bfloat16)[0], back[i])
+
+
 def operands(n, K):
     """Codes whose products' sums are quarters below 2^24, made on the device."""
     c = torch.empty(n, K // 2, dtype=torch.uint8, device="cuda")

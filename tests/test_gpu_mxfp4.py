@@ -207,6 +207,20 @@ def test_layouts(b, M):
         assert torch.equal(lead.view(M, N), want)
 
 
+@pytest.mark.parametrize("M,K", [(3, 1024), (16, 352), (60, 1024), (40, 8192), (300, 512), (500, 96)])
+def test_scales_at_any_address(b, M, K):
+    args = exact(M, 200, K, M)
+    want = b.linear_mxfp4(*(t.cuda() for t in args), out_dtype=torch.float32)
+    for off in (1, 2, 7):
+        dev = [t.cuda() for t in args]
+        for i in (1, 3):
+            flat = torch.zeros(args[i].numel() + 16, dtype=torch.uint8, device="cuda")
+            flat[off: off + args[i].numel()] = dev[i].view(-1)
+            dev[i] = flat[off: off + args[i].numel()].view(args[i].shape)
+        assert dev[1].data_ptr() % 4 == off % 4
+        assert torch.equal(b.linear_mxfp4(*dev, out_dtype=torch.float32), want)
+
+
 @pytest.mark.parametrize("M,N,K", [(8, 512, 8192), (8, 64, 16384), (40, 256, 8192), (300, 700, 1024)])
 def test_captured_and_on_another_stream(b, M, N, K):
     args, bias, _ = rough(M, N, K, 1, torch.bfloat16)
