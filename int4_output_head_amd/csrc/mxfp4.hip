@@ -80,7 +80,9 @@ __device__ __forceinline__ void store_values8(void *p, const float (&v)[8])
 }
 
 // 8 channels per thread: 4 neighbouring lanes hold the 32 that share a scale.
-// Grid (chunks of 8 of a row, rows), or the whole matrix as one row.
+// Grid (chunks of 8 of a row, rows), or the whole matrix as one row.  Bound by
+// memory: 4096 x 8192 in bfloat16, 85 MB, takes 17.4 us (4.9 TB/s), and the way
+// back below 13.8.
 template <int kDtype>
 __global__ void __launch_bounds__(256) quantize_mxfp4_kernel(const void *x, long long x_stride, int M, long long chunks,
                                                              uint32_t *codes, uint8_t *scales)
@@ -243,7 +245,10 @@ constexpr int kSMaxK = kSWaves * kSMaxSteps * 128;    // 8192 channels per workg
 // are added in the order of the waves.  Scales: a lane needs a byte of each step,
 // the one of its own 32 channels; a row's 4 bytes of a step are loaded as a word
 // by one lane, step u's by the lanes of group u % 4, and passed on (kWhole: K is
-// a multiple of 128; otherwise each lane loads its bytes).
+// a multiple of 128; otherwise each lane loads its bytes).  Bound by the weights'
+// stream where there are enough (16 x 34816 x 5120: 23.6 us, 4.1 TB/s), and by two
+// memory latencies, a tile's and the next one's, where there are not
+// (16 x 5120 x 5120: 9 us, 320 tiles for 512 workgroups).
 template <int kSteps, bool kWhole>
 __global__ void __launch_bounds__(kSThreads, kSteps > 5 ? 2 : 4) mx_stream_kernel(MxArgs a)
 {

@@ -554,7 +554,8 @@ struct Weight8 {
 // A whole row waits at each, so what hides memory's latency is a second workgroup
 // on the compute unit: rows of 8192 channels take 1024 threads, and two of those
 // 64 registers a thread, which is why the weights stay packed (4096 x 8192 in
-// bfloat16 with a gate of elements, 336 MB: 78 us, 4.3 TB/s; with the weights
+// bfloat16 with a gate of elements, 336 MB: 79 us, 4.3 TB/s and vector
+// instructions in 87 % of the cycles; without a gate 54 us, 5.0; with the weights
 // converted ahead of the rows 110, and with the next row's loads ahead of the
 // reductions, which takes one of the workgroups, 100).
 template <int kDtype, bool kInt8>
