@@ -34,6 +34,8 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 struct __attribute__((packed, aligned(1))) Word1 { uint32_t w; };
+struct __attribute__((packed, aligned(1))) Words1 { uint32_t w[4]; };
+typedef unsigned long long u64;
 
 constexpr int kMaxK = 65536;
 
@@ -473,28 +475,45 @@ __global__ void __launch_bounds__(64 * kWM *kWN, kRing == 2 ? 2 : 1) mx_tile_ker
         }
     };
     uint32_t rs[kSPer][4];
+    int skip = 0;
     auto load_scales = [&](int span) {                         // of one span
         const int s = min(span, p1 - 1);
+        // the last span's are the row's last 16, less those in front of it
+        const int from = min(16 * s, blocks - 16), off = 16 * s - from;
 #pragma unroll
         for (int j = 0; j < kSPer; ++j) {
-            const uint8_t *base = min(wave + j * kWaves, kSCopies - 1) * kSRows < kBM * 32 ? sxbase : swbase;
+            const uint8_t *row = (min(wave + j * kWaves, kSCopies - 1) * kSRows < kBM * 32 ? sxbase : swbase) + sfrom[j];
+            if (blocks >= 16) {
+                const Words1 v = *reinterpret_cast<const Words1 *>(row + from);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                rs[j][i] = 0u;
+                for (int i = 0; i < 4; ++i)
+                    rs[j][i] = v.w[i];
+            } else {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int c = 16 * s + 4 * i + q;
-                    const uint32_t v = base[sfrom[j] + (uint32_t)min(c, blocks - 1)];
-                    rs[j][i] |= (c < blocks ? v : 0u) << (8 * q);
+                for (int i = 0; i < 4; ++i) {
+                    rs[j][i] = 0u;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        rs[j][i] |= (4 * i + q < blocks ? (uint32_t)row[min(4 * i + q, blocks - 1)] : 0u) << (8 * q);
                 }
             }
         }
+        skip = blocks >= 16 ? off : 0;
     };
     auto store_scales = [&](int span) {
 #pragma unroll
-        for (int j = 0; j < kSPer; ++j)
+        for (int j = 0; j < kSPer; ++j) {
+            u64 lo = (u64)rs[j][1] << 32 | rs[j][0], hi = (u64)rs[j][3] << 32 | rs[j][2];
+            if (skip) {                                        // towards the first, zeros behind
+                lo = skip & 8 ? hi : lo;
+                hi = skip & 8 ? 0ull : hi;
+                const int bits = 8 * (skip & 7);
+                lo = bits ? lo >> bits | hi << (64 - bits) : lo;
+                hi >>= bits;
+            }
             lds.scale[(span >> 1) & 1][min(wave + j * kWaves, kSCopies - 1) * kSRows + lane][span & 1] =
-                u32x4{rs[j][0], rs[j][1], rs[j][2], rs[j][3]};
+                u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+        }
     };
 
     f32x16 acc[kMB][kNB];
@@ -584,17 +603,17 @@ __global__ void __launch_bounds__(64 * kWM *kWN, kRing == 2 ? 2 : 1) mx_tile_ker
         multiply(s, II());
         // all have read this buffer, and the next step's has landed
         landed();
+        if (!kWhole && kS == 0)
+            store_scales(span + 1 - p0);       // asked for a step ago; read behind the next barrier
         load(at + kRing, buf);
         if (kWhole && kS == 0 && (span - p0) % 2 == 0)
             copy_scales(span + 2, ((span - p0) / 2 + 1) & 1);
-        if (!kWhole && kS == 0)
-            load_scales(span + 1);
+        if (!kWhole && kS == 1)
+            load_scales(span + 2);
         read(at + 1, other, 0);
         multiply(s, III());
         if (kS == 1)
             read_scales(span + 1 - p0);
-        if (!kWhole && kS == 0)
-            store_scales(span + 1 - p0);
     };
     // The epilogue's place: four columns of a row per lane.
     constexpr int kLanes = kCols / 4, kStep = 64 / kLanes, kIter = 32 / kStep;   // lanes of a row; rows at a time
@@ -621,6 +640,7 @@ __global__ void __launch_bounds__(64 * kWM *kWN, kRing == 2 ? 2 : 1) mx_tile_ker
     } else {
         load_scales(p0);
         store_scales(0);
+        load_scales(p0 + 1);
     }
 #pragma unroll
     for (int i = 0; i < kRing; ++i)
