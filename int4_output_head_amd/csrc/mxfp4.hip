@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(64 * kWM *kWN, kRing == 2 ? 2 : 1) mx_tile_ker
     const uint32_t turned = 16u * (uint32_t)(half ^ ((n32 >> 1) & 7));
     uint32_t ax = lds_at(&lds.code[0][wm * kMB * 32 + n32][0]) + turned;
     uint32_t aw = lds_at(&lds.code[0][(kBM + wn * kNB) * 32 + n32][0]) + turned;
-    auto read = [&](int step, int buf, int q) {
+    auto read = [&](int step, int buf, int q, auto tail) {
         lds_words *px = lds_pointer((ax ^ (32u * q)) + buf * (uint32_t)sizeof(lds.code[0]));
         lds_words *pw = lds_pointer((aw ^ (32u * q)) + buf * (uint32_t)sizeof(lds.code[0]));
 #pragma unroll
@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(64 * kWM *kWN, kRing == 2 ? 2 : 1) mx_tile_ker
 #pragma unroll
         for (int k = 0; k < kNB; ++k)
             w[q & 1][k] = pw[32 * 8 * k];
-        if (!kWhole && step * 8 + 8 > blocks) {
+        if (!kWhole && decltype(tail)::value && step * 8 + 8 > blocks) {
             const bool live = step * 8 + 2 * q + half < blocks;
 #pragma unroll
             for (int k = 0; k < kMB; ++k)
@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(64 * kWM *kWN, kRing == 2 ? 2 : 1) mx_tile_ker
         __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
         barrier_no_fence();
     };
-    auto step = [&](int span, auto s) {
+    auto step = [&](int span, auto s, auto tail) {
         constexpr int kS = decltype(s)::value;
         const int at = 2 * span + kS;
         hold(ax, aw, row);
@@ -595,11 +595,11 @@ __global__ void __launch_bounds__(64 * kWM *kWN, kRing == 2 ? 2 : 1) mx_tile_ker
         using II = std::integral_constant<int, 2>;
         using III = std::integral_constant<int, 3>;
         const int buf = (at - 2 * p0) % kRing, other = (at - 2 * p0 + 1) % kRing;
-        read(at, buf, 1);
+        read(at, buf, 1, tail);
         multiply(s, Z());
-        read(at, buf, 2);
+        read(at, buf, 2, tail);
         multiply(s, I());
-        read(at, buf, 3);
+        read(at, buf, 3, tail);
         multiply(s, II());
         // all have read this buffer, and the next step's has landed
         landed();
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(64 * kWM *kWN, kRing == 2 ? 2 : 1) mx_tile_ker
             copy_scales(span + 2, ((span - p0) / 2 + 1) & 1);
         if (!kWhole && kS == 1)
             load_scales(span + 2);
-        read(at + 1, other, 0);
+        read(at + 1, other, 0, std::integral_constant<bool, kS == 1 || decltype(tail)::value>());
         multiply(s, III());
         if (kS == 1)
             read_scales(span + 1 - p0);
@@ -649,12 +649,16 @@ __global__ void __launch_bounds__(64 * kWM *kWN, kRing == 2 ? 2 : 1) mx_tile_ker
     __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
     barrier_no_fence();
     read_scales(0);
-    read(2 * p0, 0, 0);
+    read(2 * p0, 0, 0, std::true_type());
     // whole spans: quarters past K multiply zeros (a way out of the middle of a
-    // span would copy all sums)
-    for (int span = p0; span < p1; ++span) {
-        step(span, std::integral_constant<int, 0>());
-        step(span, std::integral_constant<int, 1>());
+    // span would copy all sums); only the last span can have any
+    for (int span = p0; span < (kWhole ? p1 : p1 - 1); ++span) {
+        step(span, std::integral_constant<int, 0>(), std::false_type());
+        step(span, std::integral_constant<int, 1>(), std::false_type());
+    }
+    if (!kWhole) {
+        step(p1 - 1, std::integral_constant<int, 0>(), std::true_type());
+        step(p1 - 1, std::integral_constant<int, 1>(), std::true_type());
     }
 
     // D: column = activation row lane & 31, rows = weight rows 8 (r / 4) + 4 (lane /
