@@ -389,8 +389,9 @@ __device__ __forceinline__ void copy_to_lds16(const uint8_t *base, uint32_t offs
 // one's are multiplied; the barrier stands in front of a step's last quarter, so
 // that the copies into the buffer that it frees, and the reads from the other
 // one, have its products to hide behind.  The scales, 16 bytes a row for 512
-// channels, are copied likewise for 1024 (kWhole), or go through registers where
-// rows do not end with a whole span of 512 or are not aligned to it.
+// channels, are copied likewise for 1024 (kWhole), or go through registers, asked
+// for two steps ahead, where rows do not end with a whole span of 512 or are not
+// aligned to it (1024 x 5120 x 4096: 23 us, 4128: 33; byte by byte, a step ahead, 47).
 //
 // What bounds it is the way of the codes into LDS: without any product 8192^3
 // takes 295 us of 345, without the copies 229.  128 rows and two buffers, two
@@ -658,7 +659,8 @@ __global__ void __launch_bounds__(64 * kWM *kWN, kRing == 2 ? 2 : 1) mx_tile_ker
     }
     if (!kWhole) {
         step(p1 - 1, std::integral_constant<int, 0>(), std::true_type());
-        step(p1 - 1, std::integral_constant<int, 1>(), std::true_type());
+        if (16 * (p1 - 1) + 8 < blocks)
+            step(p1 - 1, std::integral_constant<int, 1>(), std::true_type());
     }
 
     // D: column = activation row lane & 31, rows = weight rows 8 (r / 4) + 4 (lane /
