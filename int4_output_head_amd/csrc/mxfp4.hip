@@ -254,7 +254,10 @@ constexpr int kSMaxK = kSWaves * kSMaxSteps * 128;    // 8192 channels per workg
 template <int kSteps, bool kWhole>
 __global__ void __launch_bounds__(kSThreads, kSteps > 5 ? 2 : 4) mx_stream_kernel(MxArgs a)
 {
+    // the pitch spreads 16 rows' chunks over the banks
+    constexpr int kRow = 4 * kSteps, kPitch = kRow + (kSteps % 2 ? 0 : 4);
     __shared__ __attribute__((aligned(16))) float s_part[2][kSWaves][256];
+    __shared__ u32x4 s_turn[kSWaves][16 * kPitch];
     constexpr int kWords = kWhole ? (kSteps + 3) / 4 : kSteps;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n16 = lane & 15, grp = lane >> 4;
@@ -286,13 +289,16 @@ __global__ void __launch_bounds__(kSThreads, kSteps > 5 ? 2 : 4) mx_stream_kerne
         else
             return s[u];
     };
+    // A tile's codes, 64 chunks an instruction along the rows.
     auto load_w = [&](int tile, u32x4 (&q)[kSteps], uint32_t (&s)[kWords]) {
         const uint8_t *w = a.w + (size_t)tile * 16 * blocks * 16;
-        const int r = min(n16, a.N - 1 - tile * 16);
+        const int last = a.N - 1 - tile * 16;
 #pragma unroll
-        for (int u = 0; u < kSteps; ++u)
-            q[u] = load_codes(w, r, u);
-        load_words(a.w_scales + (size_t)tile * 16 * blocks, r, s);
+        for (int u = 0; u < kSteps; ++u) {
+            const int i = 64 * u + lane, r = min(i / kRow, last), c = min(c0 + i % kRow, blocks - 1);
+            q[u] = *reinterpret_cast<const u32x4 *>(w + ((uint32_t)r * (uint32_t)blocks + (uint32_t)c) * 16u);
+        }
+        load_words(a.w_scales + (size_t)tile * 16 * blocks, min(n16, last), s);
     };
     u32x4 q[kSteps];
     uint32_t s[kWords], xw[kWords];
@@ -315,12 +321,24 @@ __global__ void __launch_bounds__(kSThreads, kSteps > 5 ? 2 : 4) mx_stream_kerne
     for (int buf = 0; tile < a.tiles_n; buf ^= 1) {
         const int next = tile + gridDim.x, n = tile * 16 + nn;
         const float bs = column_bias(a, min(n, a.N - 1));
+        // turned to the products' layout in LDS of the wave's own
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+            const int i = 64 * u + lane;
+            s_turn[wave][i / kRow * kPitch + i % kRow] = q[u];
+        }
+        wave_fence();
+        uint32_t ws[kSteps];
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u)
+            ws[u] = scale(s, u);
+        if (next < a.tiles_n)
+            load_w(next, q, s);
         f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
         for (int u = 0; u < kSteps; ++u)
-            acc = mma<0>(q[u], x[u], acc, scale(s, u), xs[u]);
-        if (next < a.tiles_n)
-            load_w(next, q, s);
+            acc = mma<0>(s_turn[wave][n16 * kPitch + 4 * u + grp], x[u], acc, ws[u], xs[u]);
+        wave_fence();
         // D: column = activation row lane & 15, rows = weight rows 4 * grp + r
         *reinterpret_cast<f32x4 *>(&s_part[buf][wave][lane * 4]) = acc;
         __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
