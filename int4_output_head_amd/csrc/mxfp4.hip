@@ -248,11 +248,11 @@ constexpr int kSMaxK = kSWaves * kSMaxSteps * 128;    // 8192 channels per workg
 // the one of its own 32 channels; a row's 4 bytes of a step are loaded as a word
 // by one lane, step u's by the lanes of group u % 4, and passed on (kWhole: K is
 // a multiple of 128; otherwise each lane loads its bytes).  Bound by the weights'
-// stream where there are enough (16 x 34816 x 5120: 23.6 us, 4.1 TB/s), and by two
-// memory latencies, a tile's and the next one's, where there are not
-// (16 x 5120 x 5120: 9 us, 320 tiles for 512 workgroups).
+// stream where there are enough (16 x 34816 x 5120: 19.4 us, 4.9 TB/s), and by
+// latencies where there are not (16 x 5120 x 5120: 7 us, 320 tiles for 512
+// workgroups).
 template <int kSteps, bool kWhole>
-__global__ void __launch_bounds__(kSThreads, kSteps > 5 ? 2 : 4) mx_stream_kernel(MxArgs a)
+__global__ void __launch_bounds__(kSThreads, kSteps > 6 ? 2 : 4) mx_stream_kernel(MxArgs a)
 {
     // the pitch spreads 16 rows' chunks over the banks
     constexpr int kRow = 4 * kSteps, kPitch = kRow + (kSteps % 2 ? 0 : 4);
@@ -265,11 +265,28 @@ __global__ void __launch_bounds__(kSThreads, kSteps > 5 ? 2 : 4) mx_stream_kerne
     const int c_begin = (int)blockIdx.y * a.split_spans * 16, c_end = min(blocks, c_begin + a.split_spans * 16);
     const int c0 = c_begin + wave * (kSteps * 4);               // this wave's first block of 32 channels
 
-    // Row r's chunks and scales; past the end any valid ones, which meet zero codes.
-    auto load_codes = [&](const uint8_t *codes, int r, int u) {
-        const int c = min(c0 + 4 * u + grp, blocks - 1);
-        return *reinterpret_cast<const u32x4 *>(codes + ((uint32_t)r * (uint32_t)blocks + (uint32_t)c) * 16u);
+    // Sixteen rows' codes, 64 chunks an instruction along the rows (16 rows' 64 bytes
+    // each an instruction meet in few sets of L1 where rows are a multiple of 512
+    // bytes apart: 16 x 5120 x 5120 took 9.0 us instead of 7.0).  Rows and chunks past
+    // the end are any valid ones, which meet zero codes.
+    auto load_codes = [&](const uint8_t *codes, int last, u32x4 (&q)[kSteps]) {
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+            const int i = 64 * u + lane, r = min(i / kRow, last), c = min(c0 + i % kRow, blocks - 1);
+            q[u] = *reinterpret_cast<const u32x4 *>(codes + ((uint32_t)r * (uint32_t)blocks + (uint32_t)c) * 16u);
+        }
     };
+    // To the products' layout, in LDS of the wave's own.
+    auto turn = [&](const u32x4 (&q)[kSteps]) {
+        wave_fence();
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+            const int i = 64 * u + lane;
+            s_turn[wave][i / kRow * kPitch + i % kRow] = q[u];
+        }
+        wave_fence();
+    };
+    auto turned = [&](int u) { return s_turn[wave][n16 * kPitch + 4 * u + grp]; };
     auto load_words = [&](const uint8_t *scales, int r, uint32_t (&s)[kWords]) {
         const uint8_t *row = scales + (uint32_t)r * (uint32_t)blocks;
 #pragma unroll
@@ -289,15 +306,9 @@ __global__ void __launch_bounds__(kSThreads, kSteps > 5 ? 2 : 4) mx_stream_kerne
         else
             return s[u];
     };
-    // A tile's codes, 64 chunks an instruction along the rows.
     auto load_w = [&](int tile, u32x4 (&q)[kSteps], uint32_t (&s)[kWords]) {
-        const uint8_t *w = a.w + (size_t)tile * 16 * blocks * 16;
         const int last = a.N - 1 - tile * 16;
-#pragma unroll
-        for (int u = 0; u < kSteps; ++u) {
-            const int i = 64 * u + lane, r = min(i / kRow, last), c = min(c0 + i % kRow, blocks - 1);
-            q[u] = *reinterpret_cast<const u32x4 *>(w + ((uint32_t)r * (uint32_t)blocks + (uint32_t)c) * 16u);
-        }
+        load_codes(a.w + (size_t)tile * 16 * blocks * 16, last, q);
         load_words(a.w_scales + (size_t)tile * 16 * blocks, min(n16, last), s);
     };
     u32x4 q[kSteps];
@@ -306,28 +317,20 @@ __global__ void __launch_bounds__(kSThreads, kSteps > 5 ? 2 : 4) mx_stream_kerne
     load_w(tile, q, s);
     u32x4 x[kSteps];
     uint32_t xs[kSteps];
-    const int xr = min(n16, a.M - 1);
-#pragma unroll
-    for (int u = 0; u < kSteps; ++u)
-        x[u] = load_codes(a.x, xr, u);
-    load_words(a.x_scales, xr, xw);
+    load_codes(a.x, a.M - 1, x);
+    load_words(a.x_scales, min(n16, a.M - 1), xw);
+    turn(x);
 #pragma unroll
     for (int u = 0; u < kSteps; ++u) {
         const bool live = n16 < a.M && c0 + 4 * u + grp < c_end;
-        x[u] = live ? x[u] : u32x4{0, 0, 0, 0};
+        x[u] = live ? turned(u) : u32x4{0, 0, 0, 0};
         xs[u] = scale(xw, u);
     }
     const int m = tid >> 4, nn = tid & 15;             // the output element of this thread in every tile
     for (int buf = 0; tile < a.tiles_n; buf ^= 1) {
         const int next = tile + gridDim.x, n = tile * 16 + nn;
         const float bs = column_bias(a, min(n, a.N - 1));
-        // turned to the products' layout in LDS of the wave's own
-#pragma unroll
-        for (int u = 0; u < kSteps; ++u) {
-            const int i = 64 * u + lane;
-            s_turn[wave][i / kRow * kPitch + i % kRow] = q[u];
-        }
-        wave_fence();
+        turn(q);
         uint32_t ws[kSteps];
 #pragma unroll
         for (int u = 0; u < kSteps; ++u)
@@ -337,8 +340,7 @@ __global__ void __launch_bounds__(kSThreads, kSteps > 5 ? 2 : 4) mx_stream_kerne
         f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
         for (int u = 0; u < kSteps; ++u)
-            acc = mma<0>(s_turn[wave][n16 * kPitch + 4 * u + grp], x[u], acc, ws[u], xs[u]);
-        wave_fence();
+            acc = mma<0>(turned(u), x[u], acc, ws[u], xs[u]);
         // D: column = activation row lane & 15, rows = weight rows 4 * grp + r
         *reinterpret_cast<f32x4 *>(&s_part[buf][wave][lane * 4]) = acc;
         __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
@@ -876,8 +878,12 @@ void launch_stream(const MxArgs &a, dim3 grid, hipStream_t s)
         hipLaunchKernelGGL((mx_stream_kernel<2, kWhole>), grid, block, 0, s, a);
     else if (per_wave <= 3)
         hipLaunchKernelGGL((mx_stream_kernel<3, kWhole>), grid, block, 0, s, a);
+    else if (per_wave <= 4)
+        hipLaunchKernelGGL((mx_stream_kernel<4, kWhole>), grid, block, 0, s, a);
     else if (per_wave <= 5)
         hipLaunchKernelGGL((mx_stream_kernel<5, kWhole>), grid, block, 0, s, a);
+    else if (per_wave <= 6)
+        hipLaunchKernelGGL((mx_stream_kernel<6, kWhole>), grid, block, 0, s, a);
     else
         hipLaunchKernelGGL((mx_stream_kernel<8, kWhole>), grid, block, 0, s, a);
 }

@@ -160,6 +160,18 @@ def test_exact_products(b, M, N, K):
     assert torch.equal(got.double(), want)
 
 
+@pytest.mark.parametrize("K", [32, 992, 1024, 1056, 2080, 2944, 3616, 4064, 4096, 4640, 5632, 6112, 6144, 6176, 7200, 8160])
+@pytest.mark.parametrize("M,N", [(1, 9000), (7, 37), (16, 8200)])
+def test_exact_products_of_few_rows(b, M, N, K):
+    """Every number of steps per wave, and more tiles than workgroups."""
+    args = exact(M, N, K, M + N + K)
+    got = b.linear_mxfp4(*(t.cuda() for t in args), out_dtype=torch.float32)
+    want = torch.from_numpy(mxfp4.values(*(t.numpy() for t in args[:2]))).cuda() @ \
+        torch.from_numpy(mxfp4.values(*(t.numpy() for t in args[2:]))).cuda().T.contiguous()
+    assert want.abs().max() < 2 ** 22
+    assert torch.equal(got.double(), want)
+
+
 @pytest.mark.parametrize("dt", list(DT))
 @pytest.mark.parametrize("act", [None, "relu", "gelu", "silu"])
 @pytest.mark.parametrize("M,N,K", [(5, 70, 256), (40, 72, 256), (150, 131, 4096), (260, 300, 96), (900, 644, 512)])
