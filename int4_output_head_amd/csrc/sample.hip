@@ -767,9 +767,11 @@ __device__ __forceinline__ bool draw_binned(const Row &r, u64 *cand, int n, floa
     // (151936 logits at temperature 1.3 under top-p 0.95, 256 rows of 47000
     // candidates: 78 us instead of 130; below kMany the pass costs what it saves:
     // under top-p 0.5 and 0.95 at temperature 1 24.8 and 29.3 us without, 25.6 and
-    // 28.1 with it).
+    // 28.1 with it).  Under top_k and top_p they may move twice: what is left of the
+    // row's place counts from where they lie.
+    const u64 *const place_end = cand + r.a.V;
     auto narrow = [&](int bin) {
-        const int room = r.a.V - n;
+        const int room = (int)(place_end - cand) - n;
         if (bin < 0 || n <= kMany)
             return;
         if (tid == 0)
