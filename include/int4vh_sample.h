@@ -35,12 +35,15 @@
  *   request is the token behind its accepted drafts.
  * Without it, every row's token comes from all that is kept.
  *
- * Numerics.  The ruled logits are binary32; masses are computed in binary64 and
- * added as whole multiples of 2^-b, b = 62 - ceil(log2(V)) (44 for 151936
- * tokens) and at most 50, so that sums do not depend on an order; a mass below half of that
- * counts as none, and its token is not drawn.  The sums of 1024 tokens from which
- * those of a whole row are made are binary64 in a fixed order.  Results are the
- * same in every run.
+ * Numerics.  The ruled logits are binary32; masses are computed in binary64, to
+ * 2^-40 of each, and added as whole multiples of 2^-b, b = 62 - ceil(log2(V)) (44
+ * for 151936 tokens) and at most 50, so that sums do not depend on an order.  Under
+ * top_k, top_p or min_p a kept token's mass below half of that counts as none, and
+ * the token is not drawn.  Without them, and for the mass of a whole row that top_p
+ * is a part of, sums of 1024 tokens (binary64, in a fixed order) are rounded to
+ * multiples of 2^-b, and a token is found among its 1024 by masses relative to their
+ * largest: those far below the best keep their share.  Results are the same in
+ * every run.
  *
  * Calls are asynchronous on `stream`, allocate nothing and may be captured in a
  * graph.  Errors: as in int4vh_logits.h, and INT4VH_EINVAL for NULL uniforms,

@@ -1019,13 +1019,18 @@ __global__ void __launch_bounds__(kDrawThreads) sample_draw_kernel(SampleArgs a)
                     if (upto - w <= target && target < upto) {
                         lds.at = c0 + tid;
                         lds.rest = target - (upto - w);
+                        lds.found = w;
                     }
                     before += part;
                 }
                 __syncthreads();
                 const int chunk = lds.at;
-                const u64 rest = lds.rest;
-                // that chunk once more, under its rules: a token a thread
+                const u64 rest = lds.rest, size = lds.found;
+                // That chunk once more, under its rules: a token a thread, with masses
+                // relative to the chunk's own largest.  Each of its tokens may have less
+                // than half of the units that its sum is given in, but never all of them
+                // of these.
+                const float top = refs[chunk];
                 SliceWalk<kDtype> walk(a, lds.words, chunk * kChunk, kChunk, req, t, 0, 1);
                 float *ruled = reinterpret_cast<float *>(lds.few);
                 if (wave == 0) {
@@ -1037,11 +1042,14 @@ __global__ void __launch_bounds__(kDrawThreads) sample_draw_kernel(SampleArgs a)
                 }
                 __syncthreads();
                 const float x = drafted && chunk * kChunk + tid == d ? kNegInf : ruled[tid];
-                const u64 w = fixed_one(mass_below(x, ref, set.inv_t), a.bits);
+                const u64 w = fixed_one(mass_below(x, top, set.inv_t), a.bits);
                 u64 all;
                 const u64 upto = block_scan(w, lds.scan, all);
-                // the chunk's own sum may be a few roundings less: then its last token
-                const u64 goal = min(rest, all - 1ull);
+                // the same part of the tokens' sum as `rest` is of the chunk's; the row's
+                // last unit is its last token's
+                const u64 goal = target + 1ull == total
+                                     ? all - 1ull
+                                     : min(all - 1ull, (u64)((double)rest * ((double)all / (double)size)));
                 if (upto - w <= goal && goal < upto) {
                     lds.at = chunk * kChunk + tid;
                     lds.value = (float)(mass_below(x, ref, set.inv_t) / floating(total, a.bits));
