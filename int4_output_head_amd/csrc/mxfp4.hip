@@ -93,7 +93,8 @@ __global__ void __launch_bounds__(256) quantize_mxfp4_kernel(const void *x, long
     const long long c = (long long)blockIdx.x * 256 + threadIdx.x;
     if (c >= chunks)                           // chunks is a multiple of 4: lanes leave by fours
         return;
-    for (int m = blockIdx.y; m < M; m += gridDim.y) {
+    // (unsigned: a step past the last of 2^31 - 1 rows passes 31 bits)
+    for (unsigned m = blockIdx.y; m < (unsigned)M; m += gridDim.y) {
         float v[8];
         load_values8<kDtype>(static_cast<const char *>(x) + ((size_t)m * x_stride + 8 * c) * kSize, v);
         uint32_t peak = 0u;
