@@ -450,23 +450,20 @@ struct BlockArgs {
 // e / (1 + e) or 1 / (1 + e) of e = exp(-|g|), which neither overflows: with the
 // product's lost digits added to e, and a step of Newton's on the reciprocal, the
 // error is at most 6 half steps (libm's exp and a division took 22 instructions
-// instead of 14).  NaN stays.
+// instead of 14).  NaN stays.  Below -87.3, where e is no normal number, it is 0
+// here: kLow gives e for those, taken 2^64 times as large (half steps are 2^-150).
+template <bool kLow>
 __device__ __forceinline__ float sigmoid(float g)
 {
     const float a = fminf(fabsf(g), 104.0f), hi = a * -1.44269502e+00f;
     const float lo = __builtin_fmaf(a, -1.92596299e-08f, __builtin_fmaf(a, -1.44269502e+00f, -hi));
-    float e = __builtin_amdgcn_exp2f(hi);
+    float e = __builtin_amdgcn_exp2f(kLow ? hi + 64.0f : hi);
     e = __builtin_fmaf(e, lo * 6.93147182e-01f, e);
+    if (kLow)
+        return e * 0x1p-64f;
     const float d = 1.0f + e, r = __builtin_amdgcn_rcpf(d);
     const float s = (g < 0.0f ? e : 1.0f) * __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
     return g == g ? s : g;
-}
-__device__ __forceinline__ void gate_values(float (&g)[8], int activation)
-{
-    if (activation == INT4VH_GATE_SIGMOID)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            g[j] = sigmoid(g[j]);
 }
 
 // Eight values of a row as they lie in memory; those past H are 0.
@@ -500,6 +497,14 @@ struct Raw8 {
                 }
         }
     }
+    __device__ __forceinline__ void set_infinite(int j)
+    {
+        if constexpr (kDtype == INT4VH_ROWS_F32)
+            w[j] = 0x7F800000u;
+        else
+            w[j / 2] = (w[j / 2] & (j % 2 ? 0xFFFFu : 0xFFFF0000u)) |
+                       (kDtype == INT4VH_ROWS_F16 ? 0x7C00u : 0x7F80u) << (j % 2 * 16);
+    }
     template <int kAs = kDtype>
     __device__ __forceinline__ void values(float (&v)[8]) const
     {
@@ -519,6 +524,58 @@ __device__ __forceinline__ void hold(Raw8<kDtype> &r)
 #pragma unroll
     for (int i = 0; i < r.kWords; ++i)
         asm volatile("" : "+v"(r.w[i]));
+}
+
+// Whether a value of any lane's is below -87 (a negative NaN counts as one): as
+// unsigned words, negative values grow downwards and lie above the others.
+template <int kDtype>
+__device__ __forceinline__ bool any_low(const Raw8<kDtype> &r)
+{
+    if constexpr (kDtype == INT4VH_ROWS_F32) {
+        uint32_t top = r.w[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i)
+            top = r.w[i] > top ? r.w[i] : top;
+        return __ballot(top > 0xC2AE0000u) != 0ull;
+    } else {
+        typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+        u16x2 top = __builtin_bit_cast(u16x2, r.w[0]);
+#pragma unroll
+        for (int i = 1; i < 4; ++i)
+            top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, r.w[i]));
+        const uint16_t most = top[0] > top[1] ? top[0] : top[1];
+        return __ballot(most > (kDtype == INT4VH_ROWS_F16 ? 0xD570 : 0xC2AE)) != 0ull;
+    }
+}
+
+// v times a gate.
+template <int kDtype>
+__device__ __forceinline__ void times_gate(float (&v)[8], Raw8<kDtype> gate, int activation)
+{
+    float g[8];
+    hold(gate);
+    if (activation == INT4VH_GATE_SIGMOID) {
+        if (__builtin_expect(any_low(gate), false)) {
+            // these alone; to the others they are an infinite gate, which is 1
+            gate.values(g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (g[j] < -87.0f) {
+                    v[j] *= sigmoid<true>(g[j]);
+                    gate.set_infinite(j);
+                }
+            hold(gate);
+        }
+        gate.values(g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            g[j] = sigmoid<false>(g[j]);
+    } else {
+        gate.values(g);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        v[j] *= g[j];
 }
 
 // Eight channels of a weight of any type: 16-bit ones stay as they lie in memory,
@@ -570,7 +627,7 @@ __global__ void __launch_bounds__(kMaxThreads, kDtype == INT4VH_ROWS_F32 ? 4 : 8
     constexpr size_t kSize = kDtype == INT4VH_ROWS_F32 ? 4 : 2;
     const size_t out_size = a.out_dtype == INT4VH_ROWS_F32 ? 4 : 2;
 
-    const int c = 8 * tid;                     // this thread's first channel
+    int c = 8 * tid;                           // this thread's first channel
     Weight8 post(a.post, a.weight_dtype, c, H), pre(a.pre, a.weight_dtype, c, H);
     Weight8 cs(kInt8 ? a.channel : nullptr, INT4VH_ROWS_F16, c, H);
     // sums of squares that serve as they are
@@ -615,6 +672,7 @@ __global__ void __launch_bounds__(kMaxThreads, kDtype == INT4VH_ROWS_F32 ? 4 : 8
     int buf = 0;
     for (unsigned m = blockIdx.x; m < (unsigned)a.M; m += gridDim.x, buf ^= 1) {
         float u[8], h[8], f[8];
+        asm volatile("" : "+v"(c));            // the row's end is looked for anew: its masks would take registers
         rx.load(static_cast<const char *>(a.x) + (size_t)m * a.x_stride * kSize, c, H);
         rr.load(static_cast<const char *>(a.residual) + (size_t)m * a.residual_stride * kSize, c, H);
         if (a.gate_stride)
@@ -641,14 +699,8 @@ __global__ void __launch_bounds__(kMaxThreads, kDtype == INT4VH_ROWS_F32 ? 4 : 8
             for (int j = 0; j < 8; ++j)
                 u[j] = u[j] * rstd * behind * f[j];
         }
-        if (a.gate) {
-            hold(gate);
-            gate.values(f);
-            gate_values(f, a.gate_activation);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                u[j] *= f[j];
-        }
+        if (a.gate)
+            times_gate(u, gate, a.gate_activation);
         rr.values(h);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
