@@ -392,12 +392,17 @@ constexpr int waitcnt_vm(int n)
 // A copy of 16 bytes per lane straight into LDS: lane l's, from base + offset,
 // land at dst + 16 l.  Inline asm: the compiler would order all reads of LDS
 // behind all copies that it knows to be in flight.  Nothing comes back into
-// registers; the kernel waits for its copies itself.
+// registers; the kernel waits for its copies itself.  m0 is named so that the compiler
+// takes nothing of its own there for granted behind a copy (its warning is that it does
+// not keep a reserved register's value across, which nobody asks for).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void copy_to_lds16(const uint8_t *base, uint32_t offset, uint32_t dst)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst), "v"(offset), "s"(base)
-                 : "memory");
+                 : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // A workgroup computes kWM*kMB*32 activation rows x kWN*kNB*32 weight rows with
 // kWM x kWN waves, in steps of 256 channels.  A step's codes are copied from
