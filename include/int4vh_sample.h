@@ -41,9 +41,9 @@
  * top_k, top_p or min_p a kept token's mass below half of that counts as none, and
  * the token is not drawn.  Without them, and for the mass of a whole row that top_p
  * is a part of, sums of 1024 tokens (binary64, in a fixed order) are rounded to
- * multiples of 2^-b, and a token is found among its 1024 by masses relative to their
- * largest: those far below the best keep their share.  Results are the same in
- * every run.
+ * multiples of 2^-b, and a token is found among its 1024 by masses in these units, or,
+ * where the sum has less than 2^20 of them, relative to the largest of the 1024: those
+ * far below the best keep their share.  Results are the same in every run.
  *
  * Calls are asynchronous on `stream`, allocate nothing and may be captured in a
  * graph.  Errors: as in int4vh_logits.h, and INT4VH_EINVAL for NULL uniforms,

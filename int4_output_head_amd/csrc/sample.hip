@@ -1026,11 +1026,12 @@ __global__ void __launch_bounds__(kDrawThreads) sample_draw_kernel(SampleArgs a)
                 __syncthreads();
                 const int chunk = lds.at;
                 const u64 rest = lds.rest, size = lds.found;
-                // That chunk once more, under its rules: a token a thread, with masses
-                // relative to the chunk's own largest.  Each of its tokens may have less
-                // than half of the units that its sum is given in, but never all of them
-                // of these.
-                const float top = refs[chunk];
+                // That chunk once more, under its rules: a token a thread.  In one far below
+                // the best, tokens may have less than half a unit each, where their sum
+                // has some: there masses are relative to the chunk's own largest, and the
+                // target is the same part of their sum.
+                const bool far = size < 1ull << 20;
+                const float top = far ? refs[chunk] : ref;
                 SliceWalk<kDtype> walk(a, lds.words, chunk * kChunk, kChunk, req, t, 0, 1);
                 float *ruled = reinterpret_cast<float *>(lds.few);
                 if (wave == 0) {
@@ -1042,17 +1043,18 @@ __global__ void __launch_bounds__(kDrawThreads) sample_draw_kernel(SampleArgs a)
                 }
                 __syncthreads();
                 const float x = drafted && chunk * kChunk + tid == d ? kNegInf : ruled[tid];
-                const u64 w = fixed_one(mass_below(x, top, set.inv_t), a.bits);
+                const double mass = mass_below(x, top, set.inv_t);
+                const u64 w = fixed_one(mass, a.bits);
                 u64 all;
                 const u64 upto = block_scan(w, lds.scan, all);
-                // the same part of the tokens' sum as `rest` is of the chunk's; the row's
-                // last unit is its last token's
-                const u64 goal = target + 1ull == total
-                                     ? all - 1ull
-                                     : min(all - 1ull, (u64)((double)rest * ((double)all / (double)size)));
+                // the chunk's sum may be up to 512 units off that of its tokens' units; the
+                // row's last unit is its last token's
+                u64 goal = target + 1ull == total ? all - 1ull : min(rest, all - 1ull);
+                if (far && target + 1ull < total)
+                    goal = min((u64)((double)rest * ((double)all / (double)size)), all - 1ull);
                 if (upto - w <= goal && goal < upto) {
                     lds.at = chunk * kChunk + tid;
-                    lds.value = (float)(mass_below(x, ref, set.inv_t) / floating(total, a.bits));
+                    lds.value = (float)((far ? mass * mass_below(top, ref, set.inv_t) : mass) / floating(total, a.bits));
                 }
                 __syncthreads();
                 out.token = lds.at;
