@@ -76,8 +76,8 @@ typedef struct int4vh_sampling {
     float min_p;
 } int4vh_sampling;
 
-/* Bytes of workspace sample_logits_rows needs (0 if the sizes are invalid).  Pure
- * host function.  256-byte aligned, no initialisation; its contents mean nothing
+/* Bytes of workspace sample_logits_rows needs (0 if the sizes are invalid): 8 for
+ * each logit, whatever the settings, and little else.  Pure host function.  256-byte aligned, no initialisation; its contents mean nothing
  * between calls.  Calls in flight at the same time must not share it. */
 size_t sample_logits_workspace_bytes(int R, int T, int V);
 

@@ -83,7 +83,7 @@ __device__ __forceinline__ void store_values8(void *p, const float (&v)[8])
 
 // 8 channels per thread: 4 neighbouring lanes hold the 32 that share a scale.
 // Grid (chunks of 8 of a row, rows), or the whole matrix as one row.  Bound by
-// memory: 4096 x 8192 in bfloat16, 85 MB, takes 17.4 us (4.9 TB/s), and the way
+// memory: 4096 x 8192 in bfloat16, 85 MB, takes 17.6 us (4.8 TB/s), and the way
 // back below 13.8.
 template <int kDtype>
 __global__ void __launch_bounds__(256) quantize_mxfp4_kernel(const void *x, long long x_stride, int M, long long chunks,
@@ -417,7 +417,8 @@ __device__ __forceinline__ void copy_to_lds16(const uint8_t *base, uint32_t offs
 // one, have its products to hide behind.  The scales, 16 bytes a row for 512
 // channels, are copied likewise for 1024 (kWhole), or go through registers, asked
 // for two steps ahead, where rows do not end with a whole span of 512 or are not
-// aligned to it (1024 x 5120 x 4096: 23 us, 4128: 33; byte by byte, a step ahead, 47).
+// aligned to it (1024 x 5120 x 4096: 23 us, 4128: 33; byte by byte, a step ahead, 47;
+// the tiles of 128 rows spill 16 registers in this form).
 //
 // What bounds it is the way of the codes into LDS: without any product 8192^3
 // takes 295 us of 345, without the copies 229.  128 rows and two buffers, two

@@ -611,8 +611,8 @@ struct Weight8 {
 // A whole row waits at each, so what hides memory's latency is a second workgroup
 // on the compute unit: rows of 8192 channels take 1024 threads, and two of those
 // 64 registers a thread, which is why the weights stay packed (4096 x 8192 in
-// bfloat16 with a gate of elements, 336 MB: 79 us, 4.3 TB/s and vector
-// instructions in 87 % of the cycles; without a gate 54 us, 5.0; with the weights
+// bfloat16 with a gate of elements, 336 MB: 75.5 us, 4.4 TB/s and vector
+// instructions in 89 % of the cycles; without a gate 54 us, 5.0; with the weights
 // converted ahead of the rows 110, and with the next row's loads ahead of the
 // reductions, which takes one of the workgroups, 100).
 template <int kDtype, bool kInt8>
@@ -783,8 +783,8 @@ int launch_block_rows(const BlockArgs &a, hipStream_t s)
     const int nt = (a.H + 511) / 512 * 64;
     const int resident = cu_count(dev) * (2048 / nt);
     // Four rounds of workgroups: as they end at different times, the next ones'
-    // loads fill the gaps (bfloat16 4096 x 5120, gated: 63 us in one round, 54 in
-    // four or a workgroup a row; binary32 4096 x 8192 133, 137 and 140).
+    // loads fill the gaps (bfloat16 4096 x 5120, gated: 62 us in one round, 53 in
+    // four or a workgroup a row; binary32 4096 x 8192 125, 126 and 117).
     const int grid = a.M < 4 * resident ? a.M : 4 * resident;
     hipLaunchKernelGGL((norm_block_kernel<kDtype, kInt8>), dim3(grid), dim3(nt), 0, s, a);
     e = hipGetLastError();
