@@ -77,8 +77,9 @@ typedef struct int4vh_sampling {
 } int4vh_sampling;
 
 /* Bytes of workspace sample_logits_rows needs (0 if the sizes are invalid): 8 for
- * each logit, whatever the settings, and little else.  Pure host function.  256-byte aligned, no initialisation; its contents mean nothing
- * between calls.  Calls in flight at the same time must not share it. */
+ * each logit, whatever the settings, and little else.  Pure host function.
+ * 256-byte aligned, no initialisation; its contents mean nothing between calls.
+ * Calls in flight at the same time must not share it. */
 size_t sample_logits_workspace_bytes(int R, int T, int V);
 
 int sample_logits_rows(const void *logits, int64_t logits_stride, int dtype, const int32_t *draft_ids, int R, int T,
